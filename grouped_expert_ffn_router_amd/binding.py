@@ -18,12 +18,15 @@ LIB_DEBUG_PATH = os.path.join(PKG, "libmoe_debug.so")
 MOE_OK, MOE_EINVAL, MOE_EALIGN, MOE_EDTYPE, MOE_ECAP, MOE_EHIP = 0, -1, -2, -3, -4, -5
 MOE_ACT_BF16, MOE_ACT_F32 = 0, 1
 MOE_MAX_RANKS, MOE_MAX_LOCAL = 1024, 64
+MOE_FEW_TOKENS_MAX = 64
 
 ENTRY_POINTS = ["moe_capacity", "moe_workspace_size", "moe_route", "moe_pack_pools", "moe_pack_pools_noalloc",
                 "moe_pack_ragged",
                 "moe_recv_rank", "moe_recv_waves",
                 "moe_expert_gemm", "moe_shared_experts", "moe_combine", "moe_drop_stats", "moe_last_error", "moe_timing_enable",
-                "moe_timing_read"]
+                "moe_timing_read",
+                "moe_mx_strides", "moe_mx_quantize", "moe_mx_dequantize", "moe_mx_gemm",
+                "moe_mx_workspace_size", "moe_mx_expert_gemm", "moe_few_workspace_size", "moe_few_tokens"]
 
 
 class MoeError(RuntimeError):
@@ -59,6 +62,12 @@ class DropReport(ctypes.Structure):
 
 class KernelTime(ctypes.Structure):
     _fields_ = [("name", ctypes.c_char * 32), ("launches", ctypes.c_int32), ("total_ms", ctypes.c_double)]
+
+
+class MxRowsArg(ctypes.Structure):
+    """moe_mx_rows: where the rows of an MX-FP4 operand are."""
+    _fields_ = [("codes", ctypes.c_void_p), ("scales", ctypes.c_void_p), ("code_stride_bytes", ctypes.c_int64),
+                ("scale_stride_bytes", ctypes.c_int64)]
 
 
 _lib = None
@@ -119,6 +128,15 @@ def _load(path):
     L.moe_last_error.restype = ctypes.c_char_p
     L.moe_timing_enable.argtypes = [_I32]
     L.moe_timing_read.argtypes = [ctypes.POINTER(KernelTime), _I32, ctypes.POINTER(_I32)]
+    RP = ctypes.POINTER(MxRowsArg)
+    L.moe_mx_strides.argtypes = [_I64, ctypes.POINTER(_I64), ctypes.POINTER(_I64)]
+    L.moe_mx_quantize.argtypes = [_I32, _I64, _I64, _P, _I64, _P, _I64, _P, _I64, _P]
+    L.moe_mx_dequantize.argtypes = [_I32, _I64, _I64, _P, _I64, _P, _I64, _P, _I64, _P]
+    L.moe_mx_gemm.argtypes = [_I32, _I32, _I64, _I64, _I64, RP, _P, RP, _P, _I64, _P]
+    L.moe_mx_workspace_size.argtypes = [DP, ctypes.POINTER(ctypes.c_size_t)]
+    L.moe_mx_expert_gemm.argtypes = [DP, _I32, _P, _P, _I64, _P, _P, RP, RP, _P, _I64, _P, _P, _P]
+    L.moe_few_workspace_size.argtypes = [DP, ctypes.POINTER(ctypes.c_size_t)]
+    L.moe_few_tokens.argtypes = [DP, _P, _P, _P, _P, _I32] + [_P] * 12
     for n in ENTRY_POINTS:
         if n != "moe_last_error":
             getattr(L, n).restype = ctypes.c_int
@@ -137,6 +155,10 @@ def _ptr(t):
     if isinstance(t, int):
         return t
     return t.data_ptr()
+
+
+def _ref(struct):
+    return None if struct is None else ctypes.byref(struct)
 
 
 def _stream(stream):
@@ -228,6 +250,65 @@ def drop_stats(dims, ws, stream=None, raise_on_bad_ids=True):
         return rep
     _check(rc)
     return rep
+
+
+def mx_strides(cols):
+    """(code, scale) bytes of a row of `cols` MX-FP4 values."""
+    c, s = _I64(), _I64()
+    _check(lib().moe_mx_strides(int(cols), ctypes.byref(c), ctypes.byref(s)))
+    return c.value, s.value
+
+
+def mx_rows(codes, scales, code_stride_bytes, scale_stride_bytes):
+    return MxRowsArg(_ptr(codes), _ptr(scales), int(code_stride_bytes), int(scale_stride_bytes))
+
+
+def mx_quantize(act_dtype, rows, cols, x, x_stride_bytes, codes, code_stride_bytes, scales, scale_stride_bytes,
+                stream=None):
+    _check(lib().moe_mx_quantize(int(act_dtype), int(rows), int(cols), _ptr(x), int(x_stride_bytes), _ptr(codes),
+                                 int(code_stride_bytes), _ptr(scales), int(scale_stride_bytes), _stream(stream)))
+
+
+def mx_dequantize(act_dtype, rows, cols, codes, code_stride_bytes, scales, scale_stride_bytes, out, out_stride_bytes,
+                  stream=None):
+    _check(lib().moe_mx_dequantize(int(act_dtype), int(rows), int(cols), _ptr(codes), int(code_stride_bytes),
+                                   _ptr(scales), int(scale_stride_bytes), _ptr(out), int(out_stride_bytes),
+                                   _stream(stream)))
+
+
+def mx_gemm(out_dtype, groups, max_rows, n, k, a, counts, b, out, out_stride_bytes, stream=None):
+    """a, b: MxRowsArg (mx_rows) or None."""
+    _check(lib().moe_mx_gemm(int(out_dtype), int(groups), int(max_rows), int(n), int(k), _ref(a), _ptr(counts),
+                             _ref(b), _ptr(out), int(out_stride_bytes), _stream(stream)))
+
+
+def mx_workspace_size(dims):
+    b = ctypes.c_size_t()
+    _check(lib().moe_mx_workspace_size(ctypes.byref(dims), ctypes.byref(b)))
+    return b.value
+
+
+def mx_expert_gemm(dims, wave, wave_buf, recv_pools, src_stride_bytes, row_src, wave_count, w13, w2, ret_pools,
+                   ret_src_stride_bytes, ws, ws_mx, stream=None):
+    """w13, w2: MxRowsArg (mx_rows) or None."""
+    _check(lib().moe_mx_expert_gemm(ctypes.byref(dims), int(wave), _ptr(wave_buf), _ptr(recv_pools),
+                                    int(src_stride_bytes), _ptr(row_src), _ptr(wave_count), _ref(w13), _ref(w2),
+                                    _ptr(ret_pools), int(ret_src_stride_bytes), _ptr(ws), _ptr(ws_mx),
+                                    _stream(stream)))
+
+
+def few_workspace_size(dims):
+    b = ctypes.c_size_t()
+    _check(lib().moe_few_workspace_size(ctypes.byref(dims), ctypes.byref(b)))
+    return b.value
+
+
+def few_tokens(dims, x, w_router, w_down, bias, bias_row_tokens, w13, w13_scales, w2, w2_scales, w_up, ws13, ws2,
+               topk_idx, topk_w, out, ws, stream=None):
+    _check(lib().moe_few_tokens(ctypes.byref(dims), _ptr(x), _ptr(w_router), _ptr(w_down), _ptr(bias),
+                                int(bias_row_tokens), _ptr(w13), _ptr(w13_scales), _ptr(w2), _ptr(w2_scales),
+                                _ptr(w_up), _ptr(ws13), _ptr(ws2), _ptr(topk_idx), _ptr(topk_w), _ptr(out), _ptr(ws),
+                                _stream(stream)))
 
 
 def last_error():

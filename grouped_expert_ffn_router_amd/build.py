@@ -14,7 +14,8 @@ LIB = os.path.join(PKG, "libmoe.so")
 # the same sources with -DMOE_DEBUG: kernels record invariant violations in
 # the workspace and moe_drop_stats reports them (MOE_ECAP); nothing traps
 LIB_DEBUG = os.path.join(PKG, "libmoe_debug.so")
-SOURCES = ["kernels.hip", "api.hip"]
+# ops/entry.hip holds the whole C ABI: it includes api.hip
+SOURCES = ["kernels.hip", "ops/entry.hip", "ops/mx.hip", "ops/few.hip"]
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 FLAGS = [
@@ -33,6 +34,10 @@ def _run(cmd):
     return out
 
 
+def _object(bdir, src):
+    return os.path.join(bdir, os.path.splitext(os.path.basename(src))[0] + ".o")
+
+
 def build(verbose=False, extra_flags=()):
     """Build libmoe.so and its debug twin libmoe_debug.so (-DMOE_DEBUG)."""
     variants = [(LIB, BUILD, ()), (LIB_DEBUG, os.path.join(BUILD, "debug"), ("-DMOE_DEBUG",))]
@@ -40,7 +45,7 @@ def build(verbose=False, extra_flags=()):
     for _, bdir, flags in variants:
         os.makedirs(bdir, exist_ok=True)
         for src in SOURCES:
-            jobs.append((src, os.path.join(bdir, os.path.splitext(src)[0] + ".o"), flags))
+            jobs.append((src, _object(bdir, src), flags))
 
     def compile_one(job):
         src, obj, flags = job
@@ -49,7 +54,7 @@ def build(verbose=False, extra_flags=()):
     with ThreadPoolExecutor(max_workers=len(jobs)) as ex:
         logs = list(ex.map(compile_one, jobs))
     for lib, bdir, _ in variants:
-        objs = [os.path.join(bdir, os.path.splitext(s)[0] + ".o") for s in SOURCES]
+        objs = [_object(bdir, s) for s in SOURCES]
         tmp = lib + ".tmp"
         logs.append(_run([HIPCC, "--offload-arch=gfx950", "-shared", "-o", tmp, *objs]))
         os.replace(tmp, lib)

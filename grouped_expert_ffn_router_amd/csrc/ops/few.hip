@@ -1,0 +1,655 @@
+// The few-token layer (gfx950): one whole mixture-of-experts layer for up to
+// 64 tokens.
+//
+// Every product is [a few tokens] x [rows of weights], so the weights' bytes
+// bound it: each is read once, 16 bytes a lane straight from memory into the
+// A operand of a 16 x 16 matrix instruction (16 weight rows; the tokens are
+// the B operand, 16 at a time), and the tokens' rows come from the caches.
+// The layer is a chain of all-to-all dependencies:
+//   project  logits = x W_r^T, z = x W_d^T, hs = silu(x Wg^T) (x Wu^T)
+//   select   top-k of each token; the chosen experts and their tokens
+//   gate_up  h = silu(z Wg^T) (z Wu^T) of each chosen expert
+//   down     c = sum over the chosen experts of w (h W2^T)
+//   up       out = c U^T + sum hs W2s^T
+
+#include "few.h"
+
+namespace moe {
+
+namespace {
+
+constexpr int FEW_CUS = 256;  // what the split of the down product is sized for (the workspace's size depends on it)
+constexpr int NW = 8;  // waves of a workgroup
+constexpr int NTHREADS = NW * 64;
+
+// ------------------------------------------------------------ operands
+
+__device__ __forceinline__ float silu_exact(float a) { return a / (1.0f + expf(-a)); }
+
+// 16 rows of weights by 16-byte pieces.  Lane (r, g) = (lane % 16, lane / 16)
+// holds row r and the g-th piece of a step of KSTEP values.
+struct WBf16 {
+  static constexpr int KSTEP = 32;
+  const bf16_t* p;  // this lane's row
+  struct Piece { i32x4 w; };
+  __device__ Piece load(int k, int g) const { return {__builtin_nontemporal_load((const i32x4*)(p + k + g * 8))}; }
+};
+
+struct WMx {
+  static constexpr int KSTEP = 128;
+  const uint8_t* p;
+  const uint8_t* s;
+  struct Piece { i32x4 w; uint32_t scale; };
+  __device__ Piece load(int k, int g) const {
+    return {__builtin_nontemporal_load((const i32x4*)(p + (k >> 1) + g * 16)), s[(k >> 5) + g]};
+  }
+};
+
+struct WF32 {
+  static constexpr int KSTEP = 16;
+  const float* p;
+  struct Piece { float w[4]; };
+};
+
+// acc[t] += 16 weight rows x tokens 16 t .. over one step, tokens' rows at hi[t] / lo[t].
+template <bool LO, int NT>
+__device__ __forceinline__ void mma(f32x4 (&acc)[NT], const WBf16::Piece& w, const bf16_t* const (&hi)[NT], int64_t lo, int k,
+                                    int g) {
+#pragma unroll
+  for (int t = 0; t < NT; ++t) {
+    const bf16_t* a = hi[t] + k + g * 8;
+    acc[t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, w.w), *(const bf16x8*)a, acc[t], 0, 0, 0);
+    if (LO)
+      acc[t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, w.w), *(const bf16x8*)(a + lo), acc[t],
+                                                       0, 0, 0);
+  }
+}
+
+// Eight codes (one dword) with their block's scale as bf16 values: exact (a
+// code has two significant bits).  The conversion takes the scale's exponent
+// field as the scale byte itself.
+__device__ __forceinline__ bf16x8 mx_to_bf16(uint32_t codes, uint32_t scale) {
+  const float s = __uint_as_float(scale << 23);
+  typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+  const bf16x2 a = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(codes, s, 0);
+  const bf16x2 b = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(codes, s, 1);
+  const bf16x2 c = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(codes, s, 2);
+  const bf16x2 d = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(codes, s, 3);
+  return bf16x8{a[0], a[1], b[0], b[1], c[0], c[1], d[0], d[1]};
+}
+
+template <bool LO, int NT>
+__device__ __forceinline__ void mma(f32x4 (&acc)[NT], const WMx::Piece& w, const bf16_t* const (&hi)[NT], int64_t lo, int k,
+                                    int g) {
+#pragma unroll
+  for (int q = 0; q < 4; ++q) {
+    const bf16x8 wv = mx_to_bf16((uint32_t)w.w[q], w.scale);
+#pragma unroll
+    for (int t = 0; t < NT; ++t) {
+      const bf16_t* a = hi[t] + k + g * 32 + q * 8;
+      acc[t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(wv, *(const bf16x8*)a, acc[t], 0, 0, 0);
+      if (LO) acc[t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(wv, *(const bf16x8*)(a + lo), acc[t], 0, 0, 0);
+    }
+  }
+}
+
+// Products of RT x 16 weight rows with the tokens over the steps [s0, s1) that
+// fall to wave `part` of `parts`, in groups of U steps.  LO: the tokens' rows
+// have a second part, `lo` elements behind the first.
+template <class W, bool LO, int RT, int NT>
+__device__ __forceinline__ void dot(f32x4 (&acc)[RT][NT], const W (&w)[RT], const bf16_t* const (&hi)[NT], int64_t lo,
+                                    int K, int part, int parts) {
+  constexpr int U = sizeof(typename W::Piece) == 16 ? 4 : 2;
+  const int g = lane_id() >> 4;
+  const int full = K / W::KSTEP, groups = (full + U - 1) / U;
+  for (int i = part; i < groups; i += parts) {
+    const int s0 = i * U;
+    if (s0 + U <= full) {
+      typename W::Piece p[U][RT];
+#pragma unroll
+      for (int u = 0; u < U; ++u)
+#pragma unroll
+        for (int r = 0; r < RT; ++r) p[u][r] = w[r].load((s0 + u) * W::KSTEP, g);
+#pragma unroll
+      for (int u = 0; u < U; ++u)
+#pragma unroll
+        for (int r = 0; r < RT; ++r) mma<LO, NT>(acc[r], p[u][r], hi, lo, (s0 + u) * W::KSTEP, g);
+    } else {
+      for (int s = s0; s < full; ++s)
+#pragma unroll
+        for (int r = 0; r < RT; ++r) mma<LO, NT>(acc[r], w[r].load(s * W::KSTEP, g), hi, lo, s * W::KSTEP, g);
+    }
+  }
+  if constexpr (W::KSTEP == 128) {
+    // the last blocks of 32 that do not fill a step: lanes past them multiply zeros
+    const int k = full * W::KSTEP;
+    if (k < K && part == groups % parts) {
+      const bool in = k + g * 32 < K;
+#pragma unroll
+      for (int r = 0; r < RT; ++r) {
+        typename W::Piece p = {i32x4{0, 0, 0, 0}, 0};
+        if (in) p = w[r].load(k, g);
+        mma<LO, NT>(acc[r], p, hi, lo, in ? k : k - g * 32, g);
+      }
+    }
+  }
+}
+
+// fp32: any K and any alignment, 4 values a lane and step.
+template <class W, bool LO, int RT, int NT>
+__device__ __forceinline__ void dot(f32x4 (&acc)[RT][NT], const W (&w)[RT], const float* const (&hi)[NT], int64_t, int K,
+                                    int part, int parts) {
+  const int g = lane_id() >> 4;
+  const int steps = (K + 15) / 16;
+  uintptr_t at = 0;
+#pragma unroll
+  for (int r = 0; r < RT; ++r) at |= (uintptr_t)w[r].p;
+#pragma unroll
+  for (int t = 0; t < NT; ++t) at |= (uintptr_t)hi[t];
+  const bool vec = __all((at & 15) == 0);
+  for (int s = part; s < steps; s += parts) {
+    const int k = s * 16 + g * 4;
+    float a[NT][4], b[RT][4];
+    if (vec && s * 16 + 16 <= K) {
+#pragma unroll
+      for (int r = 0; r < RT; ++r) *(float4*)b[r] = *(const float4*)(w[r].p + k);
+#pragma unroll
+      for (int t = 0; t < NT; ++t) *(float4*)a[t] = *(const float4*)(hi[t] + k);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+#pragma unroll
+        for (int r = 0; r < RT; ++r) b[r][i] = k + i < K ? w[r].p[k + i] : 0.f;
+#pragma unroll
+        for (int t = 0; t < NT; ++t) a[t][i] = k + i < K ? hi[t][k + i] : 0.f;
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int r = 0; r < RT; ++r)
+#pragma unroll
+        for (int t = 0; t < NT; ++t)
+          acc[r][t] = __builtin_amdgcn_mfma_f32_16x16x4f32(b[r][i], a[t][i], acc[r][t], 0, 0, 0);
+  }
+}
+
+// ------------------------------------------------------------ activations
+
+__device__ __forceinline__ void put_act(const FewAct& a, bf16_t*, int64_t i, float v) {
+  const bf16_t hi = f32_to_bf16(v);
+  const float rest = v - bf16_to_f32(hi);
+  ((bf16_t*)a.hi)[i] = hi;
+  ((bf16_t*)a.lo)[i] = __builtin_isfinite(rest) ? f32_to_bf16(rest) : (bf16_t)0;
+}
+__device__ __forceinline__ void put_act(const FewAct& a, float*, int64_t i, float v) { ((float*)a.hi)[i] = v; }
+
+// Elements from a value's first part to its second.
+template <class T>
+__device__ __forceinline__ int64_t lo_offset(const FewAct& a) { return (const T*)a.lo - (const T*)a.hi; }
+
+// ------------------------------------------------------------ phases
+
+// Sums of the waves' accumulators, in wave order; f(r, t, sum) gets the sums
+// of row tile r and token tile t (4 weight rows 4 g .. of token r16).
+template <int RT, int NT, class F>
+__device__ __forceinline__ void reduce(f32x4 (&acc)[RT][NT], f32x4* lds, F f) {
+  const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
+  __syncthreads();
+#pragma unroll
+  for (int r = 0; r < RT; ++r)
+#pragma unroll
+    for (int t = 0; t < NT; ++t) lds[((wave * RT + r) * NT + t) * 64 + lane] = acc[r][t];
+  __syncthreads();
+  if (wave < NT) {  // wave t finishes token tile t
+    f32x4 s[RT];
+#pragma unroll
+    for (int r = 0; r < RT; ++r) {
+      s[r] = lds[(r * NT + wave) * 64 + lane];
+      for (int w = 1; w < NW; ++w) s[r] += lds[((w * RT + r) * NT + wave) * 64 + lane];
+    }
+    f(wave, s);
+  }
+}
+
+template <class T> struct Weights { using type = WBf16; };
+template <> struct Weights<float> { using type = WF32; };
+
+template <int RT, int NT>
+__device__ __forceinline__ void zero(f32x4 (&acc)[RT][NT]) {
+#pragma unroll
+  for (int r = 0; r < RT; ++r)
+#pragma unroll
+    for (int t = 0; t < NT; ++t) acc[r][t] = f32x4{0.f, 0.f, 0.f, 0.f};
+}
+
+// Items: 16 router rows, then 16 rows of W_down, then 16 hidden units of a shared expert.
+__host__ __device__ __forceinline__ int project_items(const FewDims& d) {
+  return (d.E + 15) / 16 + (d.L + 15) / 16 + d.S * ((d.HS + 15) / 16);
+}
+
+template <class T, int NT>
+__device__ void project(const FewArgs& a, int item, f32x4* lds) {
+  const FewDims& d = a.d;
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, r16 = lane & 15, g = lane >> 4;
+  using W = typename Weights<T>::type;
+  const T* hi[NT];
+#pragma unroll
+  for (int t = 0; t < NT; ++t) hi[t] = (const T*)a.x + (int64_t)min(t * 16 + r16, d.T - 1) * d.D;
+  const int nr = (d.E + 15) / 16, nd = (d.L + 15) / 16;
+  if (item < nr + nd) {
+    const bool router = item < nr;
+    const int n0 = (router ? item : item - nr) * 16, N = router ? d.E : d.L;
+    const W w[1] = {{(const T*)(router ? a.w_router : a.w_down) + (int64_t)min(n0 + r16, N - 1) * d.D}};
+    f32x4 acc[1][NT];
+    zero(acc);
+    dot<W, false, 1, NT>(acc, w, hi, 0, d.D, wave, NW);
+    reduce<1, NT>(acc, lds, [&](int t, const f32x4 (&s)[1]) {
+      const int m = t * 16 + r16;
+      if (m >= d.T) return;
+#pragma unroll
+      for (int v = 0; v < 4; ++v) {
+        const int n = n0 + g * 4 + v;
+        if (n >= N) break;
+        if (router) {
+          float b = 0.f;
+          if (a.bias) b = a.bias[(int64_t)(a.bias_row_tokens ? m / a.bias_row_tokens : 0) * d.E + n];
+          a.logits[(int64_t)m * d.E + n] = s[0][v] + b;
+        } else {
+          put_act(a.z, (T*)nullptr, (int64_t)m * d.L + n, s[0][v]);
+        }
+      }
+    });
+    return;
+  }
+  const int ns = (d.HS + 15) / 16, i = item - nr - nd, j = i / ns, u0 = (i - j * ns) * 16;
+  const T* base = (const T*)a.ws13 + (int64_t)j * 2 * d.HS * d.D + (int64_t)min(u0 + r16, d.HS - 1) * d.D;
+  const W w[2] = {{base}, {base + (int64_t)d.HS * d.D}};
+  f32x4 acc[2][NT];
+  zero(acc);
+  dot<W, false, 2, NT>(acc, w, hi, 0, d.D, wave, NW);
+  reduce<2, NT>(acc, lds, [&](int t, const f32x4 (&s)[2]) {
+    const int m = t * 16 + r16;
+    if (m >= d.T) return;
+#pragma unroll
+    for (int v = 0; v < 4; ++v) {
+      const int u = u0 + g * 4 + v;
+      if (u < d.HS) put_act(a.hs, (T*)nullptr, ((int64_t)m * d.S + j) * d.HS + u, silu_exact(s[0][v]) * s[1][v]);
+    }
+  });
+}
+
+// The tokens of chosen expert i, by rank.  One token id per thread below 64.
+__device__ __forceinline__ int token_list(uint64_t mask, int* list) {
+  const int t = threadIdx.x;
+  __syncthreads();
+  if (t < 64 && ((mask >> t) & 1)) list[__popcll(mask & ((1ull << t) - 1))] = t;
+  __syncthreads();
+  return __popcll(mask);
+}
+
+template <class W> struct Bank {  // a routed expert's weight rows
+  const void* codes;
+  const uint8_t* scales;
+  __device__ W row(int64_t r, int K) const;
+};
+template <> __device__ __forceinline__ WBf16 Bank<WBf16>::row(int64_t r, int K) const { return {(const bf16_t*)codes + r * K}; }
+template <> __device__ __forceinline__ WF32 Bank<WF32>::row(int64_t r, int K) const { return {(const float*)codes + r * K}; }
+template <> __device__ __forceinline__ WMx Bank<WMx>::row(int64_t r, int K) const {
+  return {(const uint8_t*)codes + r * (K / 2), scales + r * mx_scale_bytes(K)};
+}
+
+// Item: 16 hidden units of a chosen expert.
+template <class T, class W, int NT>
+__device__ void gate_up(const FewArgs& a, int i, int u0, const int* list, int n, f32x4* lds) {
+  const FewDims& d = a.d;
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, r16 = lane & 15, g = lane >> 4;
+  const T* hi[NT];
+#pragma unroll
+  for (int t = 0; t < NT; ++t) hi[t] = (const T*)a.z.hi + (int64_t)list[min(t * 16 + r16, n - 1)] * d.L;
+  const Bank<W> bank{a.w13, a.w13_scales};
+  const int64_t row = (int64_t)a.active[i] * 2 * d.H + min(u0 + r16, d.H - 1);
+  const W w[2] = {bank.row(row, d.L), bank.row(row + d.H, d.L)};
+  f32x4 acc[2][NT];
+  zero(acc);
+  dot<W, sizeof(T) == 2, 2, NT>(acc, w, hi, lo_offset<T>(a.z), d.L, wave, NW);
+  const int64_t first = a.first[i];
+  reduce<2, NT>(acc, lds, [&](int t, const f32x4 (&s)[2]) {
+    const int m = t * 16 + r16;
+    if (m >= n) return;
+#pragma unroll
+    for (int v = 0; v < 4; ++v) {
+      const int u = u0 + g * 4 + v;
+      if (u < d.H) put_act(a.h, (T*)nullptr, (first + m) * d.H + u, silu_exact(s[0][v]) * s[1][v]);
+    }
+  });
+}
+
+// Item: 16 rows of the latent width and one of `parts` shares of the chosen
+// experts' hidden units.  A wave takes pieces (expert, DOWN_K hidden units) in
+// turn, weighs each piece's sums with the tokens' routing weights and adds
+// them to its own rows in LDS; the waves' rows are added in wave order.
+constexpr int DOWN_K = 512;
+
+template <class T, class W, int NT>
+__device__ __forceinline__ void down_piece(const FewArgs& a, int i, int k0, int l0, uint64_t mask, float* rows) {
+  const FewDims& d = a.d;
+  const int lane = threadIdx.x & 63, r16 = lane & 15, g = lane >> 4, n = __popcll(mask);
+  const int K = min(DOWN_K, d.H - k0);
+  const int64_t first = a.first[i], e = a.active[i];
+  const T* hi[NT];
+  int tok[NT];
+  float gate[NT];
+#pragma unroll
+  for (int t = 0; t < NT; ++t) {
+    const int m = min(t * 16 + r16, n - 1);
+    hi[t] = (const T*)a.h.hi + (first + m) * d.H + k0;
+    uint64_t rest = mask;  // the m-th set bit
+    for (int s = 0; s < m; ++s) rest &= rest - 1;
+    tok[t] = __ffsll((unsigned long long)rest) - 1;
+    gate[t] = a.gate[(int64_t)tok[t] * d.X + e];
+  }
+  const Bank<W> bank{a.w2, a.w2_scales};
+  W w[1] = {bank.row(e * d.L + min(l0 + r16, d.L - 1), d.H)};
+  if constexpr (W::KSTEP == 128) {
+    w[0].p += k0 / 2;
+    w[0].s += k0 / 32;
+  } else {
+    w[0].p += k0;
+  }
+  f32x4 acc[1][NT];
+  zero(acc);
+  dot<W, sizeof(T) == 2, 1, NT>(acc, w, hi, lo_offset<T>(a.h), K, 0, 1);
+#pragma unroll
+  for (int t = 0; t < NT; ++t)
+    if (t * 16 + r16 < n) {
+      f32x4* p = (f32x4*)(rows + tok[t] * 16 + g * 4);
+      f32x4 v = *p;
+#pragma unroll
+      for (int q = 0; q < 4; ++q) v[q] = fmaf(gate[t], acc[0][t][q], v[q]);
+      *p = v;
+    }
+}
+
+template <class T, class W>
+__device__ void down(const FewArgs& a, int part, int l0, float* lds) {  // lds: [NW][T][16]
+  const FewDims& d = a.d;
+  const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
+  float* rows = lds + wave * d.T * 16;
+  for (int i = lane; i < d.T * 16; i += 64) rows[i] = 0.f;
+  const int active = a.count[0], chunks = (d.H + DOWN_K - 1) / DOWN_K, pieces = active * chunks;
+  for (int p = part * NW + wave; p < pieces; p += a.parts * NW) {
+    const int i = p / chunks, k0 = (p - i * chunks) * DOWN_K;
+    const uint64_t mask = a.mask[i];
+    const int n = __popcll(mask);
+    if (n <= 16) down_piece<T, W, 1>(a, i, k0, l0, mask, rows);
+    else if (n <= 32) down_piece<T, W, 2>(a, i, k0, l0, mask, rows);
+    else down_piece<T, W, 4>(a, i, k0, l0, mask, rows);
+  }
+  __syncthreads();
+  for (int i = threadIdx.x; i < d.T * 16; i += NTHREADS) {
+    float s = lds[i];
+    for (int w = 1; w < NW; ++w) s += lds[w * d.T * 16 + i];
+    const int t = i >> 4, l = l0 + (i & 15);
+    if (l < d.L) a.part[((int64_t)part * d.T + t) * d.L + l] = s;
+  }
+}
+
+// Item: 16 output columns.
+template <class T, int NT>
+__device__ void up(const FewArgs& a, int n0, f32x4* lds) {
+  const FewDims& d = a.d;
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, r16 = lane & 15, g = lane >> 4;
+  using W = typename Weights<T>::type;
+  const int64_t row = min(n0 + r16, d.D - 1);
+  f32x4 acc[1][NT];
+  zero(acc);
+  const T* hi[NT];
+  {
+    const W w[1] = {{(const T*)a.w_up + row * d.L}};
+#pragma unroll
+    for (int t = 0; t < NT; ++t) hi[t] = (const T*)a.c.hi + (int64_t)min(t * 16 + r16, d.T - 1) * d.L;
+    dot<W, sizeof(T) == 2, 1, NT>(acc, w, hi, lo_offset<T>(a.c), d.L, wave, NW);
+  }
+  for (int j = 0; j < d.S; ++j) {
+    const W w[1] = {{(const T*)a.ws2 + ((int64_t)j * d.D + row) * d.HS}};
+#pragma unroll
+    for (int t = 0; t < NT; ++t)
+      hi[t] = (const T*)a.hs.hi + ((int64_t)min(t * 16 + r16, d.T - 1) * d.S + j) * d.HS;
+    dot<W, sizeof(T) == 2, 1, NT>(acc, w, hi, lo_offset<T>(a.hs), d.HS, wave, NW);
+  }
+  reduce<1, NT>(acc, lds, [&](int t, const f32x4 (&s)[1]) {
+    const int m = t * 16 + r16;
+    if (m >= d.T) return;
+#pragma unroll
+    for (int v = 0; v < 4; ++v)
+      if (n0 + g * 4 + v < d.D) ((T*)a.out)[(int64_t)m * d.D + n0 + g * 4 + v] = Act<T>::store(s[0][v]);
+  });
+}
+
+}  // namespace
+
+// ------------------------------------------------------------ kernels
+
+template <class T, int NT>
+__global__ void __launch_bounds__(NTHREADS) few_project(FewArgs a) {
+  __shared__ f32x4 lds[NW * 2 * NT * 64];
+  project<T, NT>(a, blockIdx.x, lds);
+}
+
+// One workgroup: every wave takes tokens in turn, k rounds of a maximum over
+// (logit, lower expert first) keys; then the chosen experts in ascending
+// order with their tokens (a bit each: an expert is chosen once a token).
+__global__ void __launch_bounds__(1024) few_select(FewArgs a) {
+  __shared__ unsigned long long mask[2048];
+  __shared__ int scan_n[1024], scan_p[1024];
+  const FewDims& d = a.d;
+  const int tid = threadIdx.x, wave = tid >> 6, lane = tid & 63;
+  for (int e = tid; e < d.X; e += 1024) mask[e] = 0;
+  __syncthreads();
+  for (int t = wave; t < d.T; t += 16) {
+    uint64_t key[32];
+#pragma unroll
+    for (int j = 0; j < 32; ++j) {
+      const int e = lane + 64 * j;
+      key[j] = 0;
+      if (64 * j < d.E && e < d.E) {
+        uint32_t u = __float_as_uint(a.logits[(int64_t)t * d.E + e]);
+        if (u == 0x80000000u) u = 0;
+        key[j] = ((uint64_t)((u & 0x80000000u) ? ~u : (u | 0x80000000u)) << 32) | (uint32_t)~(uint32_t)e;
+      }
+    }
+    float my_v = 0.f, v0 = 0.f;
+    int my_e = 0;
+    for (int r = 0; r < d.k; ++r) {
+      uint64_t best = key[0];
+#pragma unroll
+      for (int j = 1; j < 32; ++j)
+        if (64 * j < d.E) best = key[j] > best ? key[j] : best;
+      for (int o = 1; o < 64; o <<= 1) {
+        const uint64_t other = ((uint64_t)(uint32_t)__shfl_xor((int)(best >> 32), o) << 32) |
+                               (uint32_t)__shfl_xor((int)(uint32_t)best, o);
+        best = other > best ? other : best;
+      }
+      const int e = (int)~(uint32_t)best;
+      const uint32_t o = (uint32_t)(best >> 32);
+      const float v = __uint_as_float((o & 0x80000000u) ? (o & 0x7fffffffu) : ~o);
+      if (r == 0) v0 = v;
+      if (lane == r) {
+        my_v = v;
+        my_e = e;
+      }
+#pragma unroll
+      for (int j = 0; j < 32; ++j)
+        if (lane + 64 * j == e) key[j] = 0;
+    }
+    const float ex = lane < d.k ? expf(my_v - v0) : 0.f;
+    float sum = ex;
+    for (int o = 32; o > 0; o >>= 1) sum += __shfl_xor(sum, o);
+    if (lane < d.k) {
+      a.topk_idx[(int64_t)t * d.k + lane] = my_e;
+      a.topk_w[(int64_t)t * d.k + lane] = ex / sum;
+      const int le = my_e - d.x0;
+      if (le >= 0 && le < d.X) {
+        atomicOr(&mask[le], 1ull << t);  // in LDS; the order does not matter
+        a.gate[(int64_t)t * d.X + le] = ex / sum;
+      }
+    }
+  }
+  __syncthreads();
+  // chosen experts and their pair rows: two experts a thread, scans over the threads
+  const int e0 = tid * 2;
+  const uint64_t m0 = e0 < d.X ? mask[e0] : 0, m1 = e0 + 1 < d.X ? mask[e0 + 1] : 0;
+  const int n = (m0 != 0) + (m1 != 0), p = __popcll(m0) + __popcll(m1);
+  scan_n[tid] = n;
+  scan_p[tid] = p;
+  __syncthreads();
+  for (int o = 1; o < 1024; o <<= 1) {
+    const int an = tid >= o ? scan_n[tid - o] : 0, ap = tid >= o ? scan_p[tid - o] : 0;
+    __syncthreads();
+    scan_n[tid] += an;
+    scan_p[tid] += ap;
+    __syncthreads();
+  }
+  int at = scan_n[tid] - n, row = scan_p[tid] - p;
+  if (m0) {
+    a.active[at] = e0;
+    a.mask[at] = m0;
+    a.first[at] = row;
+    ++at;
+    row += __popcll(m0);
+  }
+  if (m1) {
+    a.active[at] = e0 + 1;
+    a.mask[at] = m1;
+    a.first[at] = row;
+  }
+  if (tid == 1023) a.count[0] = scan_n[1023];
+}
+
+template <class T, class W, int NTMAX>
+__global__ void __launch_bounds__(NTHREADS) few_gate_up(FewArgs a) {
+  __shared__ f32x4 lds[NW * 2 * NTMAX * 64];
+  __shared__ int list[64];
+  const int tiles = (a.d.H + 15) / 16;
+  const int i = blockIdx.x / tiles, u0 = (blockIdx.x - i * tiles) * 16;
+  if (i >= a.count[0]) return;
+  const int n = token_list(a.mask[i], list);
+  if (NTMAX == 1 || n <= 16) gate_up<T, W, 1>(a, i, u0, list, n, lds);
+  else if (NTMAX == 2 || n <= 32) gate_up<T, W, (NTMAX >= 2 ? 2 : 1)>(a, i, u0, list, n, lds);
+  else gate_up<T, W, NTMAX>(a, i, u0, list, n, lds);
+}
+
+template <class T, class W>
+__global__ void __launch_bounds__(NTHREADS) few_down(FewArgs a) {
+  extern __shared__ float rows[];
+  const int tiles = (a.d.L + 15) / 16;
+  const int part = blockIdx.x / tiles;
+  down<T, W>(a, part, (blockIdx.x - part * tiles) * 16, rows);
+}
+
+template <class T>
+__global__ void __launch_bounds__(256) few_sum(FewArgs a) {
+  const int64_t n = (int64_t)a.d.T * a.d.L, i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  if (i >= n) return;
+  float s = a.part[i];
+  for (int p = 1; p < a.parts; ++p) s += a.part[p * n + i];
+  put_act(a.c, (T*)nullptr, i, s);
+}
+
+template <class T, int NT>
+__global__ void __launch_bounds__(NTHREADS) few_up(FewArgs a) {
+  __shared__ f32x4 lds[NW * NT * 64];
+  up<T, NT>(a, blockIdx.x * 16, lds);
+}
+
+// ------------------------------------------------------------ host
+
+FewWs few_layout(const FewDims& d) {
+  FewWs w;
+  size_t off = 0;
+  auto take = [&](size_t bytes) {
+    const size_t o = off;
+    off += (bytes + 255) / 256 * 256;
+    return o;
+  };
+  const size_t es = d.bf16 ? 2 : 4, second = d.bf16 ? 2 : 0;
+  w.logits = take((size_t)d.T * d.E * 4);
+  w.mask = take((size_t)d.X * 8);
+  w.active = take((size_t)d.X * 4);
+  w.first = take((size_t)d.X * 4);
+  w.count = take(64);
+  w.gate = take((size_t)d.T * d.X * 4);
+  w.z = take((size_t)d.T * d.L * es);
+  w.z_lo = take((size_t)d.T * d.L * second);
+  w.hs = take((size_t)d.T * d.S * d.HS * es);
+  w.hs_lo = take((size_t)d.T * d.S * d.HS * second);
+  w.h = take((size_t)d.T * d.k * d.H * es);
+  w.h_lo = take((size_t)d.T * d.k * d.H * second);
+  w.c = take((size_t)d.T * d.L * es);
+  w.c_lo = take((size_t)d.T * d.L * second);
+  // shares of the down product: as many as give every CU two workgroups, and
+  // every wave of a share something to do
+  const int64_t tiles = (d.L + 15) / 16, most = d.X < d.T * d.k ? d.X : d.T * d.k;
+  const int64_t pieces = most * ((d.H + DOWN_K - 1) / DOWN_K);
+  int64_t parts = (2 * FEW_CUS + tiles - 1) / tiles;
+  if (parts > (pieces + NW - 1) / NW) parts = (pieces + NW - 1) / NW;
+  w.parts = parts < 1 ? 1 : (int)parts;
+  w.part = take((size_t)w.parts * d.T * d.L * 4);
+  w.total = off;
+  return w;
+}
+
+// f(type tag, weight tag, token tiles) for the layer's types and tokens.
+template <class F>
+hipError_t few_dispatch(const FewDims& d, F f) {
+  auto tiles = [&](auto t, auto w) {
+    if (d.T <= 16) f(t, w, std::integral_constant<int, 1>());
+    else if (d.T <= 32) f(t, w, std::integral_constant<int, 2>());
+    else f(t, w, std::integral_constant<int, 4>());
+  };
+  if (!d.bf16) tiles(float(), WF32());
+  else if (d.mx) tiles(bf16_t(), WMx());
+  else tiles(bf16_t(), WBf16());
+  return hipGetLastError();
+}
+
+hipError_t launch_few_project(const FewArgs& a, hipStream_t st) {
+  return few_dispatch(a.d, [&](auto t, auto, auto nt) {
+    launch((few_project<decltype(t), decltype(nt)::value>), dim3((unsigned)project_items(a.d)), dim3(NTHREADS), 0, st, a);
+  });
+}
+
+hipError_t launch_few_select(const FewArgs& a, hipStream_t st) {
+  launch(few_select, dim3(1), dim3(1024), 0, st, a);
+  return hipGetLastError();
+}
+
+hipError_t launch_few_gate_up(const FewArgs& a, hipStream_t st) {
+  const unsigned most = (unsigned)(a.d.X < a.d.T * a.d.k ? a.d.X : a.d.T * a.d.k);
+  return few_dispatch(a.d, [&](auto t, auto w, auto nt) {
+    launch((few_gate_up<decltype(t), decltype(w), decltype(nt)::value>), dim3(most * ((a.d.H + 15) / 16)), dim3(NTHREADS),
+           0, st, a);
+  });
+}
+
+hipError_t launch_few_down(const FewArgs& a, hipStream_t st) {
+  return few_dispatch(a.d, [&](auto t, auto w, auto) {
+    launch((few_down<decltype(t), decltype(w)>), dim3((unsigned)(a.parts * ((a.d.L + 15) / 16))), dim3(NTHREADS),
+           (uint32_t)(NW * a.d.T * 16 * 4), st, a);
+  });
+}
+
+hipError_t launch_few_sum(const FewArgs& a, hipStream_t st) {
+  return few_dispatch(a.d, [&](auto t, auto, auto) {
+    launch(few_sum<decltype(t)>, dim3((unsigned)(((int64_t)a.d.T * a.d.L + 255) / 256)), dim3(256), 0, st, a);
+  });
+}
+
+hipError_t launch_few_up(const FewArgs& a, hipStream_t st) {
+  return few_dispatch(a.d, [&](auto t, auto, auto nt) {
+    launch((few_up<decltype(t), decltype(nt)::value>), dim3((unsigned)((a.d.D + 15) / 16)), dim3(NTHREADS), 0, st, a);
+  });
+}
+
+}  // namespace moe

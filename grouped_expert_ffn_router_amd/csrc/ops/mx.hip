@@ -1,0 +1,680 @@
+// MX-FP4 rows: quantisation, its inverse, and the grouped product (gfx950).
+
+#include "mx.h"
+
+namespace moe {
+
+// ------------------------------------------------------------ rows <-> MX-FP4
+//
+// One lane takes 16 bytes of activations (8 bf16 or 4 fp32 values), so a block
+// of 32 is a group of 4 or 8 neighbouring lanes: the block's largest magnitude
+// is a maximum over the bit patterns (sign dropped; infinities and NaN come out
+// on top) taken with DPP moves inside the group.  Bytes bound it: a value is
+// read once and 17/32 of a byte written.
+
+template <int CTRL>
+__device__ __forceinline__ uint32_t dpp_u32(uint32_t x) {
+  return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)x, CTRL, 0xf, 0xf, false);
+}
+
+// Maximum over groups of G = 4 or 8 lanes: quad permutations [1,0,3,2] and
+// [2,3,0,1], then a mirror of 8 lanes, which swaps the two quads.
+template <int G>
+__device__ __forceinline__ uint32_t group_max(uint32_t v) {
+  v = max(v, dpp_u32<0xB1>(v));
+  v = max(v, dpp_u32<0x4E>(v));
+  if (G == 8) v = max(v, dpp_u32<0x141>(v));
+  return v;
+}
+
+struct QStrided {  // row r of a plain buffer
+  const char* base;
+  int64_t ld;
+  int64_t rows;
+  // in: input row, out: output row index; false: no such row
+  __device__ bool at(int64_t r, const char*& in, int64_t& out) const {
+    in = base + r * ld;
+    out = r;
+    return r < rows;
+  }
+};
+
+struct QGather {  // row r = j * rcap + m of a wave
+  MxGather g;
+  int64_t row_bytes;
+  __device__ bool at(int64_t r, const char*& in, int64_t& out) const {
+    if (r >= (int64_t)g.nj * g.rcap) return false;
+    const int j = (int)(r / g.rcap), m = (int)(r - (int64_t)j * g.rcap);
+    if (m >= g.counts[j]) return false;
+    out = r;
+    if (g.ragged_rows > 0) {
+      out = ragged_row0(g.counts, j) + m;
+      if (out >= g.ragged_rows) return false;
+    }
+    if (g.wave_buf) {
+      in = g.wave_buf + r * row_bytes;
+    } else {
+      const int rs = g.row_src[r];
+      const int s = rs / g.cap;
+      in = g.pools + s * g.src_stride + (int64_t)(rs - s * g.cap) * g.row_stride;
+    }
+    return true;
+  }
+};
+
+constexpr int Q_UNROLL = 2;
+
+// cpr: 16-byte pieces of an input row.  Block b covers pieces b * 512 ..,
+// row after row.
+template <class T, class Src>
+__global__ void __launch_bounds__(256)
+mx_quantize_kernel(Src src, int cpr, uint8_t* __restrict__ codes, int64_t ldc, uint8_t* __restrict__ scales,
+                   int64_t lds) {
+  constexpr int V = 16 / sizeof(T), G = MX_BLOCK / V;
+  const int64_t first = (int64_t)blockIdx.x * (256 * Q_UNROLL);
+  const int64_t row0 = first / cpr;
+  const uint32_t off0 = (uint32_t)(first - row0 * cpr);
+  uint4 d[Q_UNROLL];
+  int64_t out[Q_UNROLL];
+  uint32_t piece[Q_UNROLL];
+  bool ok[Q_UNROLL];
+#pragma unroll
+  for (int u = 0; u < Q_UNROLL; ++u) {
+    const uint32_t loc = off0 + threadIdx.x + 256 * u;
+    const uint32_t r = loc / (uint32_t)cpr;
+    piece[u] = loc - r * (uint32_t)cpr;
+    const char* in = nullptr;
+    ok[u] = src.at(row0 + r, in, out[u]);
+    d[u] = make_uint4(0, 0, 0, 0);
+    if (ok[u]) d[u] = *(const uint4*)(in + (int64_t)piece[u] * 16);
+  }
+#pragma unroll
+  for (int u = 0; u < Q_UNROLL; ++u) {
+    float v[V];
+    if constexpr (sizeof(T) == 2) {
+      const uint32_t w[4] = {d[u].x, d[u].y, d[u].z, d[u].w};
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        v[2 * i] = __uint_as_float(w[i] << 16);
+        v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+      }
+    } else {
+      v[0] = __uint_as_float(d[u].x); v[1] = __uint_as_float(d[u].y);
+      v[2] = __uint_as_float(d[u].z); v[3] = __uint_as_float(d[u].w);
+    }
+    uint32_t m = 0;
+#pragma unroll
+    for (int i = 0; i < V; ++i) m = max(m, __float_as_uint(v[i]) & 0x7fffffffu);
+    m = group_max<G>(m);  // rows start at a group boundary, so a group is one block
+    const bool nan = (m >> 23) == 255;
+    const int e = mx_exponent(m);
+    const float inv = nan ? 0.f : mx_inverse_scale(e);
+#pragma unroll
+    for (int i = 0; i < V; ++i) v[i] = nan ? 0.f : v[i] * inv;
+    if (!ok[u]) continue;
+    uint8_t* crow = codes + out[u] * ldc;
+    if constexpr (sizeof(T) == 2)
+      *(uint32_t*)(crow + (int64_t)piece[u] * 4) =
+          mx_codes4(v[0], v[1], v[2], v[3]) | (mx_codes4(v[4], v[5], v[6], v[7]) << 16);
+    else
+      *(uint16_t*)(crow + (int64_t)piece[u] * 2) = (uint16_t)mx_codes4(v[0], v[1], v[2], v[3]);
+    if (piece[u] % G == 0) {
+      uint8_t* srow = scales + out[u] * lds;
+      const int nb = cpr / G, b = (int)piece[u] / G;
+      srow[b] = nan ? 255 : (uint8_t)(e + 127);
+      if (b == nb - 1)
+        for (int p = nb; p & 15; ++p) srow[p] = 0;
+    }
+  }
+}
+
+template <class T>
+__global__ void __launch_bounds__(256)
+mx_dequantize_kernel(const uint8_t* __restrict__ codes, int64_t ldc, const uint8_t* __restrict__ scales, int64_t lds,
+                     int64_t rows, int cpr, char* __restrict__ outp, int64_t ldo) {
+  constexpr int V = 16 / sizeof(T), G = MX_BLOCK / V;
+  const int64_t first = (int64_t)blockIdx.x * (256 * Q_UNROLL);
+  const int64_t row0 = first / cpr;
+  const uint32_t off0 = (uint32_t)(first - row0 * cpr);
+  uint32_t c[Q_UNROLL], s[Q_UNROLL], piece[Q_UNROLL];
+  int64_t row[Q_UNROLL];
+#pragma unroll
+  for (int u = 0; u < Q_UNROLL; ++u) {
+    const uint32_t loc = off0 + threadIdx.x + 256 * u;
+    const uint32_t r = loc / (uint32_t)cpr;
+    piece[u] = loc - r * (uint32_t)cpr;
+    row[u] = row0 + r;
+    c[u] = s[u] = 0;
+    if (row[u] < rows) {
+      const uint8_t* crow = codes + row[u] * ldc;
+      c[u] = sizeof(T) == 2 ? *(const uint32_t*)(crow + (int64_t)piece[u] * 4)
+                            : *(const uint16_t*)(crow + (int64_t)piece[u] * 2);
+      s[u] = scales[row[u] * lds + piece[u] / G];
+    }
+  }
+#pragma unroll
+  for (int u = 0; u < Q_UNROLL; ++u) {
+    if (row[u] >= rows) continue;
+    const float sc = mx_scale(s[u]);
+    float v[8];
+    const f32x2 p0 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(c[u], 1.0f, 0);
+    const f32x2 p1 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(c[u], 1.0f, 1);
+    const f32x2 p2 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(c[u], 1.0f, 2);
+    const f32x2 p3 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(c[u], 1.0f, 3);
+    v[0] = p0[0] * sc; v[1] = p0[1] * sc; v[2] = p1[0] * sc; v[3] = p1[1] * sc;
+    v[4] = p2[0] * sc; v[5] = p2[1] * sc; v[6] = p3[0] * sc; v[7] = p3[1] * sc;
+    char* o = outp + row[u] * ldo + (int64_t)piece[u] * 16;
+    if constexpr (sizeof(T) == 2)
+      *(uint4*)o = make_uint4(f32x2_to_bf16x2(v[0], v[1]), f32x2_to_bf16x2(v[2], v[3]), f32x2_to_bf16x2(v[4], v[5]),
+                              f32x2_to_bf16x2(v[6], v[7]));
+    else
+      *(float4*)o = make_float4(v[0], v[1], v[2], v[3]);
+  }
+}
+
+template <class T, class Src>
+hipError_t run_quantize(const Src& src, int64_t rows, int64_t cols, uint8_t* codes, int64_t ldc, uint8_t* scales,
+                        int64_t lds, hipStream_t st) {
+  if (rows <= 0) return hipSuccess;
+  const int64_t cpr = cols * sizeof(T) / 16, blocks = (rows * cpr + 256 * Q_UNROLL - 1) / (256 * Q_UNROLL);
+  launch((mx_quantize_kernel<T, Src>), dim3((unsigned)blocks), dim3(256), 0, st, src, (int)cpr, codes, ldc, scales, lds);
+  return hipGetLastError();
+}
+
+hipError_t launch_mx_quantize(bool bf16, int64_t rows, int64_t cols, const void* x, int64_t ldx, uint8_t* codes,
+                              int64_t ldc, uint8_t* scales, int64_t lds, hipStream_t st) {
+  const QStrided src{(const char*)x, ldx, rows};
+  return bf16 ? run_quantize<bf16_t>(src, rows, cols, codes, ldc, scales, lds, st)
+              : run_quantize<float>(src, rows, cols, codes, ldc, scales, lds, st);
+}
+
+hipError_t launch_mx_gather(bool bf16, const MxGather& g, int64_t cols, uint8_t* codes, uint8_t* scales,
+                            hipStream_t st) {
+  const int64_t rows = (int64_t)g.nj * g.rcap, ldc = cols / 2, lds = mx_scale_bytes(cols);
+  const QGather src{g, cols * (bf16 ? 2 : 4)};
+  return bf16 ? run_quantize<bf16_t>(src, rows, cols, codes, ldc, scales, lds, st)
+              : run_quantize<float>(src, rows, cols, codes, ldc, scales, lds, st);
+}
+
+hipError_t launch_mx_dequantize(bool bf16, int64_t rows, int64_t cols, const uint8_t* codes, int64_t ldc,
+                                const uint8_t* scales, int64_t lds, void* out, int64_t ldo, hipStream_t st) {
+  if (rows <= 0) return hipSuccess;
+  const int64_t cpr = cols * (bf16 ? 2 : 4) / 16, blocks = (rows * cpr + 256 * Q_UNROLL - 1) / (256 * Q_UNROLL);
+  if (bf16)
+    launch(mx_dequantize_kernel<bf16_t>, dim3((unsigned)blocks), dim3(256), 0, st, codes, ldc, scales, lds, rows,
+           (int)cpr, (char*)out, ldo);
+  else
+    launch(mx_dequantize_kernel<float>, dim3((unsigned)blocks), dim3(256), 0, st, codes, ldc, scales, lds, rows,
+           (int)cpr, (char*)out, ldo);
+  return hipGetLastError();
+}
+
+// ------------------------------------------------------------ product, rows by operand
+
+struct MxARows {  // rows of group g: bank rows g * group_rows .., or end to end (ragged_rows > 0)
+  MxView v;
+  int64_t group_rows;
+  const int32_t* counts;
+  int max_rows;
+  int64_t ragged_rows;
+  __device__ int rows(int g) const { return counts ? min(max(counts[g], 0), max_rows) : max_rows; }
+  __device__ int64_t index(int g, int m) const {
+    if (ragged_rows > 0) {
+      const int64_t r = ragged_row0(counts, g) + m;
+      return r < ragged_rows ? r : ragged_rows - 1;
+    }
+    return g * group_rows + m;
+  }
+};
+
+struct MxBRows {
+  MxView v;
+  int n;
+  __device__ int64_t index(int g, int i) const { return (int64_t)g * n + i; }
+};
+
+// Gate and up rows interleaved in blocks of 32 as in BGateUp: columns 64 b ..
+// 64 b + 31 are the gate rows of hidden units 32 b .., the next 32 their up rows.
+struct MxBGateUp {
+  MxView v;
+  int hidden;
+  __device__ int64_t index(int g, int i) const {
+    const int w = i & 63;
+    return (int64_t)g * 2 * hidden + (int64_t)(w >> 5) * hidden + (i >> 6) * 32 + (w & 31);
+  }
+};
+
+// Output rows of any alignment: 4 columns at a time where `vec` says that
+// rows and columns stay aligned to 4 values, else one by one.
+template <class T>
+struct EMxOut {
+  static constexpr bool STAGED = sizeof(T) == 2;
+  char* out;
+  int64_t ldo;  // bytes
+  int64_t group_rows;
+  bool vec, wide;  // rows aligned to 4 values; to 16 bytes with n a multiple of 8 (the staged epilogue)
+  struct Row { T* p; };
+  __device__ Row row(int g, int m) const { return {(T*)(out + (g * group_rows + m) * ldo)}; }
+  __device__ bool staged_tile(int) const { return wide; }
+  __device__ int64_t row_key(int g, int m) const { return g * group_rows + m; }
+  __device__ T* key_dst(int64_t key) const { return (T*)(out + key * ldo); }
+  __device__ void store4(const Row& r, int n, int N, const float* v) const {
+    if (vec && n + 4 <= N) {
+      if constexpr (sizeof(T) == 2) *(uint2*)(r.p + n) = pack_bf16x4(v);
+      else *(float4*)(r.p + n) = make_float4(v[0], v[1], v[2], v[3]);
+      return;
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (n + i < N) r.p[n + i] = Act<T>::store(v[i]);
+  }
+};
+
+__device__ __forceinline__ i32x8 mx_operand(i32x4 v) { return __builtin_shufflevector(v, v, 0, 1, 2, 3, -1, -1, -1, -1); }
+
+// ------------------------------------------------------------ product, few rows
+//
+// A workgroup of 4 waves computes 16 columns (rows of B) for up to 16 * MT
+// rows of A, straight from memory: the waves take K in pieces of 512 in turn
+// and their sums meet in LDS.  v_mfma_scale_f32_16x16x128: a lane holds one
+// block of one row (16 bytes of codes) and its scale byte.  The 16 scales of
+// a 512-piece are one 16-byte load, whose dword j holds the scales of MFMA j.
+// The last piece may end early: codes past the row are read from its last
+// block, and their scales are 0 on both sides (2^-254: nothing in fp32).
+template <int MT, class T>
+__global__ void __launch_bounds__(256)
+mx_gemm_rows(MxARows a, MxBRows b, EMxOut<T> e, int N, int K) {
+  const int g = blockIdx.z, M = a.rows(g), m0 = blockIdx.y * 16 * MT, n0 = blockIdx.x * 16;
+  if (m0 >= M) return;
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, r16 = lane & 15, grp = lane >> 4;
+  const int nb = K / MX_BLOCK, pieces = (nb + 15) / 16;
+  const int64_t br = b.index(g, min(n0 + r16, N - 1));
+  const uint8_t* bc = b.v.codes + br * b.v.ldc;
+  const uint8_t* bs = b.v.scales + br * b.v.lds;
+  const uint8_t *ac[MT], *as[MT];
+#pragma unroll
+  for (int t = 0; t < MT; ++t) {
+    const int64_t ar = a.index(g, min(m0 + t * 16 + r16, M - 1));
+    ac[t] = a.v.codes + ar * a.v.ldc;
+    as[t] = a.v.scales + ar * a.v.lds;
+  }
+  f32x4 acc[MT];
+#pragma unroll
+  for (int t = 0; t < MT; ++t) acc[t] = f32x4{0.f, 0.f, 0.f, 0.f};
+  for (int p = wave; p < pieces; p += 4) {
+    int64_t off[4];
+    uint32_t keep[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const int blk = p * 16 + j * 4 + grp;
+      off[j] = (int64_t)min(blk, nb - 1) * 16;
+      keep[j] = blk < nb ? 0xffu : 0u;
+    }
+    i32x4 bv[4], av[MT][4];
+    const i32x4 bsc = *(const i32x4*)(bs + p * 16);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) bv[j] = *(const i32x4*)(bc + off[j]);
+    i32x4 asc[MT];
+#pragma unroll
+    for (int t = 0; t < MT; ++t) {
+      asc[t] = *(const i32x4*)(as[t] + p * 16);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) av[t][j] = *(const i32x4*)(ac[t] + off[j]);
+    }
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const int sb = (int)(((uint32_t)bsc[j] >> (8 * grp)) & keep[j]);
+#pragma unroll
+      for (int t = 0; t < MT; ++t) {
+        const int sa = (int)(((uint32_t)asc[t][j] >> (8 * grp)) & keep[j]);
+        acc[t] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(mx_operand(bv[j]), mx_operand(av[t][j]), acc[t], 4, 4,
+                                                                   0, sb, 0, sa);
+      }
+    }
+  }
+  // lane: row m0 + 16 t + lane % 16, columns n0 + 4 (lane / 16) ..
+  __shared__ f32x4 part[4][MT][64];
+#pragma unroll
+  for (int t = 0; t < MT; ++t) part[wave][t][lane] = acc[t];
+  __syncthreads();
+  for (int t = wave; t < MT; t += 4) {
+    const f32x4 s = part[0][t][lane] + part[1][t][lane] + part[2][t][lane] + part[3][t][lane];
+    const int m = m0 + t * 16 + r16, n = n0 + grp * 4;
+    if (m < M && n < N) {
+      const float v[4] = {s[0], s[1], s[2], s[3]};
+      e.store4(e.row(g, m), n, N, v);
+    }
+  }
+}
+
+// ------------------------------------------------------------ product, many rows
+//
+// The layout of the bf16 core (gemm.h) carries over byte for byte: a
+// workgroup of 8 waves (2 x 4) per 256 x 256 tile, two LDS buffers of 128-byte
+// row pieces (256 values here) with the same chunk swizzle, one 16-byte chunk
+// a lane and fragment: v_mfma_scale_f32_32x32x64_f8f6f4 takes a block of 32
+// values of one row from each lane, four times the bf16 instruction's work for
+// the same LDS bytes and the same number of cycles.  Lane (row, half) of
+// fragment step ks holds block 2 ks + half of the step's eight.
+//
+// Scales: a row's 16 scale bytes of two K steps are one 16-byte piece, so one
+// more global->LDS load a thread every second step brings in those of all 512
+// rows (two buffers of 8 KB).  A lane reads the 4 bytes of a row and half a
+// step, shifts its half's bytes down once, and the MFMA picks byte 0 or 2.
+//
+// A last step that reaches past K reads the row's last block again in the
+// place of what is missing, and clears the scales of those blocks on both
+// sides: 2^-254 times at most 36 adds nothing to an fp32 sum.
+struct MxTile {
+  static constexpr int BM = 256, BN = 256, NT = 512, WTM = 128, WTN = 64, FM = 4, FN = 2, NF = FM + FN;
+  static constexpr int ROW = 128, STAGE = (BM + BN) * ROW;  // bytes of an LDS row and of one buffer
+  static constexpr int RPW = 32, WBYTES = RPW * ROW;        // rows of each operand that one wave loads
+  static constexpr int SCALES = (BM + BN) * 16;             // bytes of one scale buffer
+  static constexpr int STEP = 8;                            // 32-value blocks of one K step
+};
+
+struct MxFrags {
+  i32x4 a[MxTile::FM], b[MxTile::FN];
+};
+
+__device__ __forceinline__ void mx_read16(i32x4& v, uint32_t addr) {
+  asm volatile("ds_read_b128 %0, %1" : "=v"(v) : "v"(addr) : "memory");
+}
+__device__ __forceinline__ void mx_read4(int& v, uint32_t addr) {
+  asm volatile("ds_read_b32 %0, %1" : "=v"(v) : "v"(addr) : "memory");
+}
+// Every LDS read so far has landed; the registers pass through, so that their
+// consumers stay behind it.
+__device__ __forceinline__ void mx_wait(MxFrags& f) {
+  asm volatile("s_waitcnt lgkmcnt(0)"
+               : "+v"(f.a[0]), "+v"(f.a[1]), "+v"(f.a[2]), "+v"(f.a[3]), "+v"(f.b[0]), "+v"(f.b[1])::"memory");
+}
+__device__ __forceinline__ void mx_wait(MxFrags& f, int (&s)[MxTile::NF]) {
+  asm volatile("s_waitcnt lgkmcnt(0)"
+               : "+v"(f.a[0]), "+v"(f.a[1]), "+v"(f.a[2]), "+v"(f.a[3]), "+v"(f.b[0]), "+v"(f.b[1]), "+v"(s[0]),
+                 "+v"(s[1]), "+v"(s[2]), "+v"(s[3]), "+v"(s[4]), "+v"(s[5])::"memory");
+}
+
+// Hidden rows out of a gate / up tile: a wave's 64 columns are the 32 gate and
+// the 32 up columns of one block of hidden units, 16 of them in this lane and
+// 16 in lane ^ 32, so silu(gate) * up is quantised where it is: one exchange
+// for the block's maximum and one that pairs the halves' codes.
+struct EMxHidden {
+  static constexpr bool STAGED = false;
+  MxView h;
+  int64_t group_rows;
+  const int32_t* counts;
+  int64_t ragged_rows;  // as MxARows; a row past the bank is not stored
+  __device__ void store(int g, int m, int M, int block, bool in, int half, const f32x16& gate, const f32x16& up) const {
+    float v[16];
+    uint32_t top = 0;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      v[i] = silu(gate[i]) * up[i];
+      top = max(top, __float_as_uint(v[i]) & 0x7fffffffu);
+    }
+    top = max(top, (uint32_t)__shfl_xor((int)top, 32));
+    const bool nan = (top >> 23) == 255;
+    const int ex = mx_exponent(top);
+    const float inv = mx_inverse_scale(nan ? 0 : ex);
+#pragma unroll
+    for (int i = 0; i < 16; ++i) v[i] = nan ? 0.f : v[i] * inv;
+    // units 8 q + 4 half + 0..3 are 16 bits of dword q of the block's codes
+    const uint32_t lo = mx_codes4(v[0], v[1], v[2], v[3]) | (mx_codes4(v[4], v[5], v[6], v[7]) << 16);
+    const uint32_t hi = mx_codes4(v[8], v[9], v[10], v[11]) | (mx_codes4(v[12], v[13], v[14], v[15]) << 16);
+    const uint32_t olo = (uint32_t)__shfl_xor((int)lo, 32), ohi = (uint32_t)__shfl_xor((int)hi, 32);
+    const uint2 d = half ? make_uint2((ohi & 0xffffu) | (hi << 16), (ohi >> 16) | (hi & 0xffff0000u))
+                         : make_uint2((lo & 0xffffu) | (olo << 16), (lo >> 16) | (olo & 0xffff0000u));
+    if (m >= M || !in) return;
+    const int64_t r = ragged_rows > 0 ? ragged_row0(counts, g) + m : g * group_rows + m;
+    if (ragged_rows > 0 && r >= ragged_rows) return;
+    *(uint2*)(const_cast<uint8_t*>(h.codes) + r * h.ldc + block * 16 + half * 8) = d;
+    if (!half) const_cast<uint8_t*>(h.scales)[r * h.lds + block] = nan ? 255 : (uint8_t)(ex + 127);
+  }
+};
+
+// grid: gemm_grid(groups * ceil(max_rows / 256) * tiles_n, P); block: 512.
+template <bool GATEUP, class B, class E>
+__global__ void __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(2, 2)))
+mx_gemm_tile(MxARows a, B b, E e, int N, int K, int groups, int tiles_n, int P) {
+  using C = MxTile;
+  constexpr int FM = C::FM, FN = C::FN, NF = C::NF;
+  __shared__ __attribute__((aligned(1024))) char smem[2 * C::STAGE + 2 * C::SCALES];
+  const int nch = K / MX_BLOCK, nk = (nch + C::STEP - 1) / C::STEP;
+  const TailPlan plan = tail_plan(a, groups, tiles_n, nk, P, false);
+  int t, kb, ke, slot;
+  if (!block_work(plan, nk, blockIdx.x, t, kb, ke, slot)) return;
+  int g, tm, tn;
+  tile_coords(a, groups, tiles_n, t, g, tm, tn);
+  const int M = a.rows(g);
+  const int m0 = tm * C::BM, n0 = tn * C::BN;
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int wm = wave >> 2, wn = wave & 3;
+  __shared__ int64_t keys[E::STAGED ? C::BM : 1];
+  int64_t my_key = -1;
+  bool staged = false;
+  if constexpr (E::STAGED) {
+    staged = e.staged_tile(n0);
+    if (staged && tid < C::BM && m0 + tid < M) my_key = e.row_key(g, m0 + tid);
+  }
+
+  // codes: slot d of a wave holds rows 32 wave + 8 d + lane / 8; the load's
+  // immediate offset moves both addresses by 1024 d, taken off the row pointer
+  const int lrow = lane >> 3, lcol = lane & 7;
+  const int gcol = lcol ^ swz(wave * C::RPW + lrow);  // rows 8 further: ^ 4
+  const uint8_t *pa[4], *pb[4];
+#pragma unroll
+  for (int d = 0; d < 4; ++d) {
+    pa[d] = a.v.codes + a.index(g, min(m0 + wave * C::RPW + d * 8 + lrow, M - 1)) * a.v.ldc - 1024 * d;
+    pb[d] = b.v.codes + b.index(g, min(n0 + wave * C::RPW + d * 8 + lrow, N - 1)) * b.v.ldc - 1024 * d;
+  }
+  // scales: thread tid brings in row tid of A (below 256) or of B
+  const uint8_t* ps = tid < C::BM ? a.v.scales + a.index(g, min(m0 + tid, M - 1)) * a.v.lds
+                                  : b.v.scales + b.index(g, min(n0 + tid - C::BM, N - 1)) * b.v.lds;
+
+  const int frow = lane & 31, half = lane >> 5, fswz = swz(frow);
+  const uint32_t lds0 = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) char*)smem;
+  const uint32_t fa_base = lds0 + (wm * C::WTM + frow) * C::ROW, fb_base = lds0 + (C::BM + wn * C::WTN + frow) * C::ROW;
+  const uint32_t sa_base = lds0 + 2 * C::STAGE + (wm * C::WTM + frow) * 16;
+  const uint32_t sb_base = lds0 + 2 * C::STAGE + (C::BM + wn * C::WTN + frow) * 16;
+
+  f32x16 acc[FM][FN];
+#pragma unroll
+  for (int i = 0; i < FM; ++i)
+#pragma unroll
+    for (int j = 0; j < FN; ++j)
+#pragma unroll
+      for (int v = 0; v < 16; ++v) acc[i][j][v] = 0.f;
+
+  int sc[2][NF];  // the scale bytes of substeps 2 w and 2 w + 1 (bytes 0 and 2)
+  auto read_codes = [&](MxFrags& f, int kt, int ks, int q) {
+    const uint32_t st = (uint32_t)((kt & 1) * C::STAGE) + (uint32_t)(((ks * 2 + half) ^ fswz) << 4);
+    if (q < FM) mx_read16(f.a[q], fa_base + st + q * 32 * C::ROW);
+    else mx_read16(f.b[q - FM], fb_base + st + (q - FM) * 32 * C::ROW);
+  };
+  auto read_scales = [&](int kt, int w, int q) {  // blocks 4 w .. 4 w + 3 of step kt
+    const uint32_t st = (uint32_t)(((kt >> 1) & 1) * C::SCALES + (kt & 1) * 8 + w * 4);
+    if (q < FM) mx_read4(sc[w][q], sa_base + st + q * 32 * 16);
+    else mx_read4(sc[w][q], sb_base + st + (q - FM) * 32 * 16);
+  };
+  auto load_codes = [&](int kt, int d) {  // d in [0, 8)
+    const int dd = d & 3;
+    const void* gp = (const void*)((d < 4 ? pa[dd] : pb[dd]) + min(kt * C::STEP + (gcol ^ (dd & 1) * 4), nch - 1) * 16);
+    auto lp = (__attribute__((address_space(3))) void*)(smem + (kt & 1) * C::STAGE + (d < 4 ? 0 : C::BM * C::ROW) +
+                                                         wave * C::WBYTES);
+    switch (dd) {
+      case 0: __builtin_amdgcn_global_load_lds(gp, lp, 16, 0, 0); break;
+      case 1: __builtin_amdgcn_global_load_lds(gp, lp, 16, 1024, 0); break;
+      case 2: __builtin_amdgcn_global_load_lds(gp, lp, 16, 2048, 0); break;
+      default: __builtin_amdgcn_global_load_lds(gp, lp, 16, 3 * 1024, 0); break;
+    }
+  };
+  auto load_scales = [&](int pair) {  // steps 2 pair and 2 pair + 1
+    auto lp = (__attribute__((address_space(3))) void*)(smem + 2 * C::STAGE + (pair & 1) * C::SCALES + wave * 1024);
+    __builtin_amdgcn_global_load_lds((const void*)(ps + (int64_t)pair * 16), lp, 16, 0, 0);
+  };
+
+  // Scale dwords are read one half step ahead, where their registers are
+  // free: those of substeps 0 and 1 in the last substep of the step before,
+  // those of 2 and 3 in the first of their own.
+  auto shift_scales = [&](int w, uint32_t keep) {
+#pragma unroll
+    for (int q = 0; q < NF; ++q) sc[w][q] = (int)(((uint32_t)sc[w][q] >> (8 * half)) & keep);
+  };
+  MxFrags F[2];
+  // MODE 0: issues the loads of step kt + 2; 1: no new loads; 2: the last
+  // step.  HALF: loads 4..7 of step kt + 1 were left to this step's start.
+  auto substep = [&](int kt, auto ks_tag, auto mode_tag, auto half_tag) {
+    constexpr int ks = decltype(ks_tag)::value, MODE = decltype(mode_tag)::value;
+    constexpr bool HALF = decltype(half_tag)::value;
+    constexpr int SEL = (ks & 1) * 2;
+    MxFrags& cur = F[ks & 1];
+    MxFrags& nxt = F[(ks + 1) & 1];
+    if constexpr (ks == 3 && MODE != 2) {
+      vm_wait<0>();   // step kt + 1's codes and scales (this lane's part)
+      lds_barrier();  // ... every lane's; every wave is done with step kt's buffers
+    }
+#pragma unroll
+    for (int q = 0; q < FM * FN; ++q) {
+      const int j = q / FM, i = q % FM;
+      acc[i][j] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(mx_operand(cur.b[j]), mx_operand(cur.a[i]), acc[i][j],
+                                                                  4, 4, SEL, sc[ks >> 1][FM + j], SEL, sc[ks >> 1][i]);
+      if constexpr (ks < 3) {
+        if (q < NF) read_codes(nxt, kt, ks + 1, q);
+        if (ks == 0) {
+          if (q < NF) read_scales(kt, 1, q);
+          if (HALF && q < 4) load_codes(kt + 1, 4 + q);
+          // the scales of the next pair of steps, into the buffer that step kt - 1 was the last to use
+          if (q == 4 && MODE == 0 && !(kt & 1)) load_scales(kt / 2 + 1);
+        }
+      } else if constexpr (MODE != 2) {
+        if (q < NF) {
+          read_codes(nxt, kt + 1, 0, q);
+          read_scales(kt + 1, 0, q);
+        }
+        if (MODE == 0 && q < 4) load_codes(kt + 2, q);
+      }
+      __builtin_amdgcn_sched_barrier(0);
+    }
+    if constexpr (ks == 0) mx_wait(nxt, sc[1]);
+    else if constexpr (ks < 3) mx_wait(nxt);
+    else if constexpr (MODE != 2) mx_wait(nxt, sc[0]);
+  };
+  auto step = [&](int kt, auto mode_tag, auto half_tag) {
+    uint32_t keep[2] = {~0u, ~0u};
+    if constexpr (decltype(mode_tag)::value == 2) {  // blocks of this step that K still has
+      const int have = nch - kt * C::STEP - half;
+      keep[0] = (have > 0 ? 0xffu : 0u) | (have > 2 ? 0xff0000u : 0u);
+      keep[1] = (have > 4 ? 0xffu : 0u) | (have > 6 ? 0xff0000u : 0u);
+    }
+    shift_scales(0, keep[0]);
+    substep(kt, std::integral_constant<int, 0>(), mode_tag, half_tag);
+    shift_scales(1, keep[1]);
+    substep(kt, std::integral_constant<int, 1>(), mode_tag, half_tag);
+    substep(kt, std::integral_constant<int, 2>(), mode_tag, half_tag);
+    substep(kt, std::integral_constant<int, 3>(), mode_tag, half_tag);
+  };
+  using Loads = std::integral_constant<int, 0>;
+  using NoLoads = std::integral_constant<int, 1>;
+  using Last = std::integral_constant<int, 2>;
+  load_scales(0);
+#pragma unroll
+  for (int d = 0; d < 8; ++d) load_codes(0, d);
+  vm_wait<0>();
+  lds_barrier();
+  if (nk > 1) {
+#pragma unroll
+    for (int d = 0; d < 8; ++d) load_codes(1, d);
+  }
+#pragma unroll
+  for (int q = 0; q < NF; ++q) {
+    read_codes(F[0], 0, 0, q);
+    read_scales(0, 0, q);
+  }
+  mx_wait(F[0], sc[0]);
+  if (nk >= 3) {
+    step(0, Loads(), std::false_type());
+    for (int kt = 1; kt + 2 < nk; ++kt) step(kt, Loads(), std::true_type());
+    step(nk - 2, NoLoads(), std::true_type());
+    step(nk - 1, Last(), std::false_type());
+  } else if (nk == 2) {
+    step(0, NoLoads(), std::false_type());
+    step(1, Last(), std::false_type());
+  } else {
+    step(0, Last(), std::false_type());
+  }
+
+  if constexpr (GATEUP) {
+    const int n = n0 + wn * C::WTN;
+#pragma unroll
+    for (int i = 0; i < FM; ++i)
+      e.store(g, m0 + wm * C::WTM + i * 32 + frow, M, n >> 6, n < N, half, acc[i][0], acc[i][1]);
+  } else {
+    if constexpr (E::STAGED) {
+      if (staged) {  // uniform per workgroup
+        staged_epilogue<TileCfg<256, 256>, false>(e, m0, n0, M, N, smem, keys, my_key, acc);
+        return;
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < FM; ++i)
+      epilogue_row<false, FN>(e, g, m0 + wm * C::WTM + i * 32 + frow, M, n0 + wn * C::WTN, N, half, acc[i]);
+  }
+}
+
+template <bool GATEUP, class B, class E>
+hipError_t run_mx_tile(const MxARows& a, const B& b, const E& e, int N, int K, int groups, int cus, hipStream_t st) {
+  const int64_t tiles_n = (N + 255) / 256, tiles = groups * ((a.max_rows + 255) / 256) * tiles_n;
+  if (tiles <= 0) return hipSuccess;
+  launch((mx_gemm_tile<GATEUP, B, E>), dim3((unsigned)gemm_grid(tiles, cus)), dim3(512), 0, st, a, b, e, N, K, groups,
+         (int)tiles_n, cus);
+  return hipGetLastError();
+}
+
+template <class T>
+hipError_t run_mx_gemm(const MxGemmArgs& q, int cus, hipStream_t st) {
+  const MxARows a{q.a, q.max_rows, q.counts, q.max_rows, 0};
+  const MxBRows b{q.b, q.n};
+  const uintptr_t at = (uintptr_t)q.out | (uintptr_t)q.ldo;
+  const EMxOut<T> e{(char*)q.out, q.ldo, q.max_rows, at % (4 * sizeof(T)) == 0, at % 16 == 0 && q.n % 8 == 0};
+  const dim3 grid((unsigned)((q.n + 15) / 16), 1, (unsigned)q.groups);
+  if (q.max_rows <= 16)
+    launch((mx_gemm_rows<1, T>), grid, dim3(256), 0, st, a, b, e, q.n, q.k);
+  else if (q.max_rows <= 32)
+    launch((mx_gemm_rows<2, T>), grid, dim3(256), 0, st, a, b, e, q.n, q.k);
+  else if (q.max_rows <= 64)
+    launch((mx_gemm_rows<4, T>), grid, dim3(256), 0, st, a, b, e, q.n, q.k);
+  else
+    return run_mx_tile<false>(a, b, e, q.n, q.k, q.groups, cus, st);
+  return hipGetLastError();
+}
+
+hipError_t launch_mx_gemm(const MxGemmArgs& g, int cus, hipStream_t st) {
+  return g.bf16 ? run_mx_gemm<bf16_t>(g, cus, st) : run_mx_gemm<float>(g, cus, st);
+}
+
+hipError_t launch_mx_gate_up(const MxExpertArgs& g, int cus, hipStream_t st) {
+  const MxARows a{g.x, g.rcap, g.counts, g.rcap, g.ragged_rows};
+  const MxBGateUp b{g.w13, g.H};
+  const EMxHidden e{g.h, g.rcap, g.counts, g.ragged_rows};
+  return run_mx_tile<true>(a, b, e, 2 * g.H, g.L, g.nj, cus, st);
+}
+
+template <class T>
+struct EMxReturn : EScatter<T> {
+  static constexpr bool STAGED = sizeof(T) == 2;  // the staged copy of a tile is bf16
+};
+
+template <class T>
+hipError_t run_mx_down(const MxExpertArgs& g, int cus, hipStream_t st) {
+  const MxARows a{g.h, g.rcap, g.counts, g.rcap, g.ragged_rows};
+  const MxBRows b{g.w2, g.L};
+  const EMxReturn<T> e{{g.ret, g.ret_src_stride, g.row_bytes, g.cap, g.row_src, g.rcap}};
+  return run_mx_tile<false>(a, b, e, g.L, g.H, g.nj, cus, st);
+}
+
+hipError_t launch_mx_down(const MxExpertArgs& g, int cus, hipStream_t st) {
+  return g.bf16 ? run_mx_down<bf16_t>(g, cus, st) : run_mx_down<float>(g, cus, st);
+}
+
+}  // namespace moe

@@ -70,11 +70,31 @@ def pool_block_host(ids, rows, prow, act):
     return out
 
 
-class OneRankLayer:
-    """One EP rank's layer.  ``inp`` is a workload.gen.generate() dict."""
+def _expert_form(experts):
+    if experts not in ("act", "mx"):
+        raise ValueError(f"experts={experts!r}: 'act' (the layer's type) or 'mx' (MX-FP4)")
+    return experts
 
-    def __init__(self, shape, inp, device="cuda", gather="fused", keep_source_logits=False, live_waves=0):
+
+def _expert_gemm(dims, wave, wave_buf, pools, src_stride, row_src, wave_count, w13, w2, ret, ret_stride, ws, ws_mx,
+                 stream):
+    """The expert FFNs of one wave, by the form of the weights (tensors or MxRows)."""
+    if ws_mx is None:
+        B.expert_gemm(dims, wave, wave_buf, pools, src_stride, row_src, wave_count, w13, w2, ret, ret_stride, ws, stream)
+    else:
+        B.mx_expert_gemm(dims, wave, wave_buf, pools, src_stride, row_src, wave_count, w13.arg, w2.arg, ret, ret_stride,
+                         ws, ws_mx, stream)
+
+
+class OneRankLayer:
+    """One EP rank's layer.  ``inp`` is a workload.gen.generate() dict.
+    experts="mx" quantises the routed experts to MX-FP4 rows and runs their
+    products on them (moe_mx_expert_gemm)."""
+
+    def __init__(self, shape, inp, device="cuda", gather="fused", keep_source_logits=False, live_waves=0,
+                 experts="act"):
         self.shape, self.device = shape, device
+        self.experts = _expert_form(experts)
         self.gather = gather
         # waves whose scratch (hidden rows, partial tiles) the workspace holds at once
         self.live_waves = live_waves if live_waves else shape.waves
@@ -118,6 +138,7 @@ class OneRankLayer:
         if self.full:
             self.w13 = upload(inp["w13"], dev)
             self.w2 = upload(inp["w2"], dev)
+            self._quantize_experts(self.dims)
             self.w_up = upload(inp["w_up"], dev)
             self.ws13 = upload(inp["ws13"], dev)
             self.ws2 = upload(inp["ws2"], dev)
@@ -175,10 +196,17 @@ class OneRankLayer:
         B.recv_waves(self.dims, self.recv_pools, self.scap * self.prow, w, self.wave_buf, self.row_src[w],
                      self.wave_count[w], self.ws, stream)
 
+    def _quantize_experts(self, dims):
+        """experts="mx": the routed experts as MX-FP4 rows, and the scratch of their products."""
+        self.ws_mx = None
+        if self.experts == "mx":
+            self.w13, self.w2 = mx_quantize(self.w13), mx_quantize(self.w2)
+            self.ws_mx = torch.empty((B.mx_workspace_size(dims),), dtype=torch.uint8, device=self.device)
+
     def expert_wave(self, w, stream=None):
-        B.expert_gemm(self.dims, w, self.wave_buf, self.recv_pools, self.scap * self.prow, self.row_src[w],
-                      self.wave_count[w], self.w13, self.w2, self.ret_send, self.scap * self.shape.latent * self.esize,
-                      self.ws, stream)
+        _expert_gemm(self.dims, w, self.wave_buf, self.recv_pools, self.scap * self.prow, self.row_src[w],
+                     self.wave_count[w], self.w13, self.w2, self.ret_send, self.scap * self.shape.latent * self.esize,
+                     self.ws, self.ws_mx, stream)
 
     def shared(self, stream=None):
         B.shared_experts(self.dims, self.x, self.ws13, self.ws, stream)
@@ -262,8 +290,10 @@ class RaggedOneRankLayer(OneRankLayer):
     exchange would send ahead of the rows, split by expert); otherwise every
     expert has a bank of expert_rows rows."""
 
-    def __init__(self, shape, inp, expert_rows, device="cuda", gather="fused", ragged_banks=True, live_waves=2):
+    def __init__(self, shape, inp, expert_rows, device="cuda", gather="fused", ragged_banks=True, live_waves=2,
+                 experts="act"):
         from workload.configs import exact_fit
+        self.experts = _expert_form(experts)
         if "sources" not in inp:
             raise ValueError("the ragged layer needs a workload whose other ranks route their own tokens")
         self.shape, self.device, self.gather = shape, device, gather
@@ -341,6 +371,7 @@ class RaggedOneRankLayer(OneRankLayer):
         if self.full:
             self.w13 = upload(inp["w13"], dev)
             self.w2 = upload(inp["w2"], dev)
+            self._quantize_experts(self.recv_dims)
             self.w_up = upload(inp["w_up"], dev)
             self.ws13 = upload(inp["ws13"], dev)
             self.ws2 = upload(inp["ws2"], dev)
@@ -378,9 +409,9 @@ class RaggedOneRankLayer(OneRankLayer):
                      self.wave_count[w], self.ws_recv, stream)
 
     def expert_wave(self, w, stream=None):
-        B.expert_gemm(self.recv_dims, w, self.wave_buf, self.recv_pools, self.view_rows * self.prow,
-                      self.row_src[w], self.wave_count[w], self.w13, self.w2, self.ret_send,
-                      self.view_rows * self.shape.latent * self.esize, self.ws_recv, stream)
+        _expert_gemm(self.recv_dims, w, self.wave_buf, self.recv_pools, self.view_rows * self.prow,
+                     self.row_src[w], self.wave_count[w], self.w13, self.w2, self.ret_send,
+                     self.view_rows * self.shape.latent * self.esize, self.ws_recv, self.ws_mx, stream)
 
     def combine(self, stream=None):
         r = self.rank
@@ -413,10 +444,12 @@ def receive_arrivals(shape, fit_shape, rank, recv_pools, src_stride_bytes, devic
 
 
 class AllRanksLayer:
-    """Every rank of a small EP domain on one device (zero-copy exchanges)."""
+    """Every rank of a small EP domain on one device (zero-copy exchanges).
+    experts="mx": the routed experts as MX-FP4 rows."""
 
-    def __init__(self, shape, inp, device="cuda", gather="fused"):
+    def __init__(self, shape, inp, device="cuda", gather="fused", experts="act"):
         self.shape, self.device, self.gather = shape, device, gather
+        self.experts = _expert_form(experts)
         T, D, L, E, k, R = shape.tokens, shape.d_model, shape.latent, shape.n_experts, shape.top_k, shape.n_ranks
         X, W = shape.local_experts, shape.waves
         WX = X // W
@@ -453,6 +486,10 @@ class AllRanksLayer:
         self.out = rank_blocks(R, (T, D), act, dev)
         self.ws = [torch.empty((B.workspace_size(self.dims[0]),), dtype=torch.uint8, device=dev)
                    for _ in range(R)]
+        self.ws_mx = None   # the ranks run one after the other: one scratch serves them all
+        if self.experts == "mx":
+            self.w13, self.w2 = mx_quantize(self.w13), mx_quantize(self.w2)
+            self.ws_mx = torch.empty((B.mx_workspace_size(self.dims[0]),), dtype=torch.uint8, device=dev)
 
     def run(self, stream=None):
         sh = self.shape
@@ -475,9 +512,9 @@ class AllRanksLayer:
                 wb = None if self.wave_buf is None else self.wave_buf[r, w]
                 B.recv_waves(d, recv_view, R * pool_bytes, w, wb, self.row_src[r, w],
                              self.wave_count[r, w], self.ws[r], stream)
-                B.expert_gemm(d, w, wb, recv_view, R * pool_bytes, self.row_src[r, w],
-                              self.wave_count[r, w], self.w13[r * X:(r + 1) * X], self.w2[r * X:(r + 1) * X],
-                              self.ret[r], self.scap * L * esize, self.ws[r], stream)
+                _expert_gemm(d, w, wb, recv_view, R * pool_bytes, self.row_src[r, w],
+                             self.wave_count[r, w], self.w13[r * X:(r + 1) * X], self.w2[r * X:(r + 1) * X],
+                             self.ret[r], self.scap * L * esize, self.ws[r], self.ws_mx, stream)
         for s in range(R):
             d = self.dims[s]
             ret_view = self.ret[0, s]                    # rows from receiver d at + d * R * scap * L
@@ -509,8 +546,9 @@ class RaggedAllRanksLayer:
     to the rows that receiver's fullest wave keeps (per-expert arrival counts
     at set-up, see RaggedOneRankLayer); a number forces that bank size."""
 
-    def __init__(self, shape, inp, expert_rows, device="cuda", gather="fused", wave_rows=None):
+    def __init__(self, shape, inp, expert_rows, device="cuda", gather="fused", wave_rows=None, experts="act"):
         from workload.configs import exact_fit
+        self.experts = _expert_form(experts)
         self.wave_rows_arg = wave_rows
         self.shape, self.device, self.gather = shape, device, gather
         T, D, L, E, k, R = shape.tokens, shape.d_model, shape.latent, shape.n_experts, shape.top_k, shape.n_ranks
@@ -553,6 +591,8 @@ class RaggedAllRanksLayer:
         self.out = rank_blocks(R, (T, D), act, dev)
         self.ws_send = [torch.zeros((B.workspace_size(d),), dtype=torch.uint8, device=dev) for d in self.send_dims]
         self.recv_dims, self.recv, self.ret, self.ws_recv, self.seg_off = [], [], [], [], []
+        if self.experts == "mx":
+            self.w13, self.w2 = mx_quantize(self.w13), mx_quantize(self.w2)
 
     def run(self, stream=None):
         sh = self.shape
@@ -589,15 +629,17 @@ class RaggedAllRanksLayer:
             d = B.make_dims(self._fit(view_rows), my_rank=r, wave_rows=wave_rows)
             assert B.capacity(d)[:2] == (view_rows, self.rcap)
             ws = torch.zeros((B.workspace_size(d),), dtype=torch.uint8, device=self.device)
+            ws_mx = (torch.empty((B.mx_workspace_size(d),), dtype=torch.uint8, device=self.device)
+                     if self.experts == "mx" else None)
             ret = torch.zeros((R * view_rows, L), dtype=self.out.dtype, device=self.device)
             pool_bytes = view_rows * self.prow
             B.recv_rank(d, buf, pool_bytes, ws, stream)
             for w in range(sh.waves):
                 B.recv_waves(d, buf, pool_bytes, w, self.wave_buf, self.row_src[r, w], self.wave_count[r, w], ws,
                              stream)
-                B.expert_gemm(d, w, self.wave_buf, buf, pool_bytes, self.row_src[r, w], self.wave_count[r, w],
-                              self.w13[r * X:(r + 1) * X], self.w2[r * X:(r + 1) * X], ret, view_rows * L * esize,
-                              ws, stream)
+                _expert_gemm(d, w, self.wave_buf, buf, pool_bytes, self.row_src[r, w], self.wave_count[r, w],
+                             self.w13[r * X:(r + 1) * X], self.w2[r * X:(r + 1) * X], ret, view_rows * L * esize,
+                             ws, ws_mx, stream)
             for s in range(R):                                  # the return exchange
                 c = int(cnt[s, r])
                 if c:
@@ -625,3 +667,206 @@ class RaggedAllRanksLayer:
                 snd[key] = rcv[key]
             out.append(snd)
         return out
+
+
+# ---------------------------------------------------------------- MX-FP4 rows
+
+_DTYPE = {torch.bfloat16: B.MOE_ACT_BF16, torch.float32: B.MOE_ACT_F32}
+
+
+def _on(t):
+    """(stream handle, device guard) for work on tensor t: its device's current stream."""
+    if not t.is_cuda:
+        raise ValueError("the library works on GPU tensors")
+    return torch.cuda.current_stream(t.device).cuda_stream, torch.cuda.device(t.device)
+
+
+def _row_stride(t, what):
+    """Elements from row to row of t [..., rows, cols], whose rows must be evenly spaced and contiguous."""
+    if t.dim() < 2 or t.stride(-1) != 1 and t.shape[-1] > 1:
+        raise ValueError(f"{what}: rows of contiguous values are needed")
+    if t.numel() == 0:
+        return max(t.shape[-1], 1)
+    stride = None
+    rows = 1
+    for size, st in zip(reversed(t.shape[:-1]), reversed(t.stride()[:-1])):
+        if size > 1:
+            if stride is None:
+                if st % rows:
+                    raise ValueError(f"{what}: its rows are not evenly spaced")
+                stride = st // rows
+            elif st != stride * rows:
+                raise ValueError(f"{what}: its rows are not evenly spaced")
+        rows *= size
+    return t.shape[-1] if stride is None else stride
+
+
+class MxRows:
+    """Rows of `cols` MX-FP4 values on the GPU (include/moe.h describes the format):
+    codes [..., rows, cols / 2] and scales [..., rows, cols / 32 rounded up to 16], uint8."""
+
+    def __init__(self, codes, scales, cols):
+        cb, sb = B.mx_strides(cols)
+        if codes.dtype != torch.uint8 or scales.dtype != torch.uint8:
+            raise TypeError("codes and scales are uint8")
+        if codes.shape[:-1] != scales.shape[:-1] or codes.shape[-1] != cb or scales.shape[-1] < sb:
+            raise ValueError(f"codes {tuple(codes.shape)} and scales {tuple(scales.shape)} are not rows of {cols} values")
+        if codes.device != scales.device:
+            raise ValueError("codes and scales are on different devices")
+        self.codes, self.scales, self.cols = codes, scales, cols
+        self.arg = B.mx_rows(codes, scales, _row_stride(codes, "codes"), _row_stride(scales, "scales"))
+
+    @property
+    def shape(self):
+        return tuple(self.codes.shape[:-1]) + (self.cols,)
+
+    @property
+    def rows(self):
+        n = 1
+        for s in self.codes.shape[:-1]:
+            n *= s
+        return n
+
+    def __getitem__(self, i):
+        """A part along the leading dimension(s), as of the tensors."""
+        return MxRows(self.codes[i], self.scales[i], self.cols)
+
+
+def mx_quantize(x):
+    """x [..., rows, cols] (bf16 or fp32, evenly spaced rows) as MxRows."""
+    if x.dtype not in _DTYPE:
+        raise TypeError(f"mx_quantize takes bf16 or fp32, not {x.dtype}")
+    st, dev = _on(x)
+    ld = _row_stride(x, "x")
+    cols = x.shape[-1]
+    cb, sb = B.mx_strides(cols)
+    with dev:
+        codes = torch.empty(x.shape[:-1] + (cb,), dtype=torch.uint8, device=x.device)
+        scales = torch.empty(x.shape[:-1] + (sb,), dtype=torch.uint8, device=x.device)
+        B.mx_quantize(_DTYPE[x.dtype], x.numel() // cols, cols, x, ld * x.element_size(), codes, cb, scales, sb, st)
+    return MxRows(codes, scales, cols)
+
+
+def mx_dequantize(q, dtype=torch.bfloat16):
+    """The values of MxRows q as a bf16 or fp32 tensor."""
+    if dtype not in _DTYPE:
+        raise TypeError(f"mx_dequantize gives bf16 or fp32, not {dtype}")
+    st, dev = _on(q.codes)
+    with dev:
+        out = torch.empty(q.shape, dtype=dtype, device=q.codes.device)
+        B.mx_dequantize(_DTYPE[dtype], q.rows, q.cols, q.codes, q.arg.code_stride_bytes, q.scales,
+                        q.arg.scale_stride_bytes, out, q.cols * out.element_size(), st)
+    return out
+
+
+def mx_gemm(a, b, counts=None, out=None, dtype=torch.bfloat16):
+    """out[g] = a[g] . b[g]^T of MxRows a [G, M, K] and b [G, N, K] (or [M, K] and
+    [N, K]) as bf16 or fp32.  counts: int32 [G] rows of each group (the rows of
+    `out` behind them are left as they were)."""
+    if len(a.shape) != len(b.shape) or len(a.shape) not in (2, 3) or a.cols != b.cols or a.shape[:-2] != b.shape[:-2]:
+        raise ValueError(f"mx_gemm of rows {a.shape} and {b.shape}")
+    G = a.shape[0] if len(a.shape) == 3 else 1
+    M, N = a.shape[-2], b.shape[-2]
+    st, dev = _on(a.codes)
+    shape = a.shape[:-1] + (N,)
+    with dev:
+        if out is None:
+            out = (torch.empty if counts is None else torch.zeros)(shape, dtype=dtype, device=a.codes.device)
+        if tuple(out.shape) != shape or out.dtype not in _DTYPE:
+            raise ValueError(f"out {tuple(out.shape)} {out.dtype}, expected {shape} bf16 or fp32")
+        if counts is not None and (counts.dtype != torch.int32 or tuple(counts.shape) != (G,) or not counts.is_contiguous()):
+            raise ValueError("counts is a contiguous int32 tensor with one value a group")
+        for t in (b.codes, out) + (() if counts is None else (counts,)):
+            if t.device != a.codes.device:
+                raise ValueError("mx_gemm: tensors on different devices")
+        B.mx_gemm(_DTYPE[out.dtype], G, M, N, a.cols, a.arg, counts, b.arg, out,
+                  _row_stride(out, "out") * out.element_size(), st)
+    return out
+
+
+class FewTokenLayer:
+    """A whole layer for up to 64 tokens at a time on one GPU (moe_few_tokens), as a
+    decode step runs it: __call__(x [T, D]) -> (out [T, D], topk_idx [T, k] int32,
+    topk_w [T, k] fp32).
+
+    w_router [E, D], w_down [L, D], w_up [D, L], ws13 [S, 2 HS, D], ws2 [S, D, HS]
+    are bf16 or fp32, as x; the routed experts w13 [X, 2H, L] and w2 [X, L, H] too,
+    or MxRows of those shapes (bf16 layers).  ws13 = ws2 = None (or S = 0): no
+    shared experts.  bias: fp32 [E], or [nb, E] of which row t // bias_row_tokens
+    serves token t.  With n_ranks > 1 this rank holds X = E / n_ranks experts and
+    `out` is its share of the sum over the ranks.
+
+    The layer keeps its weights and one workspace: its calls run in order on one
+    stream (graphs captured from it too); a second layer object over the same
+    weights serves a second stream.
+    """
+
+    def __init__(self, w_router, w_down, w13, w2, w_up, ws13=None, ws2=None, bias=None, bias_row_tokens=0, top_k=1,
+                 n_ranks=1, rank=0):
+        dt, dev = w_router.dtype, w_router.device
+        if dt not in _DTYPE:
+            raise TypeError(f"weights are bf16 or fp32, not {dt}")
+        if w_router.dim() != 2 or w_down.dim() != 2:
+            raise ValueError("w_router is [E, D] and w_down [L, D]")
+        E, D = w_router.shape
+        L = w_down.shape[0]
+        S = 0 if ws13 is None else ws13.shape[0]
+        HS = ws13.shape[1] // 2 if S else 64
+        if len(w13.shape) != 3 or n_ranks < 1 or E % n_ranks:
+            raise ValueError("w13 is [E / n_ranks, 2 H, L]")
+        X, H = E // n_ranks, w13.shape[1] // 2
+        self._mx = isinstance(w13, MxRows)
+        if self._mx != isinstance(w2, MxRows):
+            raise TypeError("w13 and w2 are both MxRows, or neither")
+        want = {"w_router": (w_router, (E, D)), "w_down": (w_down, (L, D)), "w_up": (w_up, (D, L)),
+                "w13": (w13, (X, 2 * H, L)), "w2": (w2, (X, L, H))}
+        if S:
+            want |= {"ws13": (ws13, (S, 2 * HS, D)), "ws2": (ws2, (S, D, HS))}
+        if bias is not None:
+            if bias.dtype != torch.float32 or bias.dim() not in (1, 2) or (bias.dim() == 2) != (bias_row_tokens > 0):
+                raise ValueError("bias is fp32 [E], or [nb, E] with bias_row_tokens > 0")
+            want["bias"] = (bias, tuple(bias.shape[:-1]) + (E,))
+            self._bias_tokens = bias.shape[0] * bias_row_tokens if bias.dim() == 2 else B.MOE_FEW_TOKENS_MAX
+        for name, (t, shape) in want.items():
+            if tuple(t.shape) != shape:
+                raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {shape}")
+            parts = [t.codes, t.scales] if isinstance(t, MxRows) else [t]
+            for p in parts:
+                if p.device != dev or not p.is_contiguous():
+                    raise ValueError(f"{name} must be contiguous and on {dev}")
+            if name != "bias" and not isinstance(t, MxRows) and t.dtype != dt:
+                raise TypeError(f"{name} is {t.dtype}, not {dt}")
+            if isinstance(t, MxRows) and t.scales.shape[-1] != B.mx_strides(t.cols)[1]:
+                raise ValueError(f"{name}: scale rows at their smallest stride are needed")
+        self.w_router, self.w_down, self.w13, self.w2, self.w_up = w_router, w_down, w13, w2, w_up
+        self.ws13, self.ws2 = (ws13, ws2) if S else (None, None)
+        self.bias, self.bias_row_tokens = bias, int(bias_row_tokens)
+        self.dims = B.Dims(tokens=B.MOE_FEW_TOKENS_MAX, d_model=D, latent=L, n_experts=E, top_k=top_k, n_ranks=n_ranks,
+                           waves=1, expert_hidden=H, shared_experts=S, shared_hidden=HS, my_rank=rank,
+                           act_dtype=_DTYPE[dt], send_num=1, send_den=1, recv_num=1, recv_den=1)
+        self.ws = torch.empty((B.few_workspace_size(self.dims),), dtype=torch.uint8, device=dev)
+        self._weights = (self.w_router.data_ptr(), self.w_down.data_ptr(), B._ptr(bias), self.bias_row_tokens) + (
+            (w13.codes.data_ptr(), w13.scales.data_ptr(), w2.codes.data_ptr(), w2.scales.data_ptr()) if self._mx
+            else (w13.data_ptr(), None, w2.data_ptr(), None)) + (w_up.data_ptr(), B._ptr(self.ws13), B._ptr(self.ws2))
+
+    def __call__(self, x, out=None):
+        T, k = x.shape[0], self.dims.top_k
+        if x.dim() != 2 or x.shape[1] != self.dims.d_model or x.dtype != self.w_router.dtype or not x.is_contiguous():
+            raise ValueError(f"x {tuple(x.shape)} {x.dtype}: contiguous rows of {self.dims.d_model} "
+                             f"{self.w_router.dtype} values are needed")
+        if x.device != self.w_router.device:
+            raise ValueError("x is on another device than the layer")
+        if T > B.MOE_FEW_TOKENS_MAX or self.bias is not None and T > self._bias_tokens:
+            raise ValueError(f"{T} tokens are more than the layer (or its bias) takes")
+        if out is not None and (out.shape != x.shape or out.dtype != x.dtype or not out.is_contiguous()
+                                or out.device != x.device):
+            raise ValueError("out must be like x")
+        st, dev = _on(x)
+        with dev:
+            if out is None:
+                out = torch.empty_like(x)
+            idx = torch.empty((T, k), dtype=torch.int32, device=x.device)
+            w = torch.empty((T, k), dtype=torch.float32, device=x.device)
+            self.dims.tokens = T
+            B.few_tokens(self.dims, x.data_ptr(), *self._weights, idx, w, out, self.ws, st)
+        return out, idx, w

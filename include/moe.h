@@ -300,7 +300,9 @@ const char* moe_last_error(void);
  * Labels: route_gemm, select_topk, send_rank, send_scan, ragged_offsets, pack, recv_rank,
  * recv_scan, recv_final, recv_place, wave_gather, expert_gate_up, expert_down,
  * zero_dropped, combine, shared_gate_up, up_shared_down, and the tail-split
- * fixups route_fixup, gate_up_fixup, down_fixup, up_fixup. */
+ * fixups route_fixup, gate_up_fixup, down_fixup, up_fixup; mx_quantize,
+ * mx_dequantize, mx_gemm, mx_gather, mx_gate_up, mx_down;
+ * few_project, few_select, few_gate_up, few_down, few_sum, few_up. */
 typedef struct moe_kernel_time {
   char name[32];    /* kernel label */
   int32_t launches; /* launches recorded since the last moe_timing_read */
@@ -315,6 +317,119 @@ int moe_timing_enable(int32_t on);
  * recorded, and clear the record.  MOE_EINVAL for NULL or negative
  * arguments; MOE_EHIP if an event cannot be read. */
 int moe_timing_read(moe_kernel_time* out, int32_t max_entries, int32_t* n_entries);
+
+/* ------------------------------------------------------------ MX-FP4 rows
+ * Rows of 4-bit floating point values with one power-of-two scale for every
+ * 32 consecutive values (the OCP microscaling format with E2M1 elements and
+ * E8M0 scales).  A row of `cols` values (a multiple of 32) is
+ *   codes   cols / 2 bytes: value 2i in the low half of byte i, value 2i + 1
+ *           in the high half; bit 3 of a code is the sign, bits 0..2 stand for
+ *           0, 0.5, 1, 1.5, 2, 3, 4, 6
+ *   scales  cols / 32 bytes, padded to a multiple of 16: byte b is the scale
+ *           2^(b - 127) of its 32 values, 255 stands for NaN (every value of
+ *           the block is NaN)
+ * Rows start 16-byte aligned: code and scale strides are multiples of 16, a
+ * code stride at least cols / 2 and a scale stride at least cols / 32 rounded
+ * up to 16.  What a padding byte holds does not matter. */
+
+/* Smallest strides of a row of `cols` values (host only).  Any output may be
+ * NULL.  MOE_EINVAL unless cols is a positive multiple of 32, at most 2^24. */
+int moe_mx_strides(int64_t cols, int64_t* code_stride_bytes, int64_t* scale_stride_bytes);
+
+/* Rows to MX-FP4.  For a block with m = max |x|: e = floor(log2 m) - 2 kept
+ * within [-127, 127] (m = 0: -127), the scale is 2^e and a value becomes
+ * x * 2^-e rounded to the nearest code (ties to the even code), at most 6 in
+ * magnitude.  A block that holds a NaN or an infinity gets scale byte 255 and
+ * codes 0.  Scale padding bytes (up to a multiple of 16) are set to 0.
+ *   x       [rows][cols] act at x_stride_bytes a row (a multiple of 16)
+ *   codes, scales  outputs, rows at their strides; rows * cols <= 2^40 */
+int moe_mx_quantize(int32_t act_dtype, int64_t rows, int64_t cols, const void* x, int64_t x_stride_bytes,
+                    void* codes, int64_t code_stride_bytes, void* scales, int64_t scale_stride_bytes,
+                    void* stream);
+
+/* MX-FP4 rows back to activations, each the value it stands for rounded to
+ * act (exact, but for bf16 or fp32 overflow and underflow of the extreme
+ * scales).  Arguments as for moe_mx_quantize, with `out` in the place of x. */
+int moe_mx_dequantize(int32_t act_dtype, int64_t rows, int64_t cols, const void* codes,
+                      int64_t code_stride_bytes, const void* scales, int64_t scale_stride_bytes, void* out,
+                      int64_t out_stride_bytes, void* stream);
+
+/* Rows of an MX-FP4 operand: row r at codes + r * code_stride_bytes and
+ * scales + r * scale_stride_bytes. */
+typedef struct moe_mx_rows {
+  const void* codes;
+  const void* scales;
+  int64_t code_stride_bytes, scale_stride_bytes;
+} moe_mx_rows;
+
+/* Grouped product of MX-FP4 rows, the product of moe_mx_expert_gemm on its
+ * own: for every group g < groups, row m < counts[g] and column i < n
+ *   out[g][m][i] = act(sum_j A[g * max_rows + m][j] * B[g * n + i][j])
+ * over j < k, accumulated in fp32 (a NaN scale gives NaN).
+ *   a        groups * max_rows rows of k values, group by group
+ *   counts   [groups] int32 rows of each group (at most max_rows are used, a
+ *            negative count is 0), or NULL: max_rows each
+ *   b        groups * n rows of k values
+ *   out      output row (g, m) at out + (g * max_rows + m) * out_stride_bytes,
+ *            n values of out_dtype (MOE_ACT_BF16 / MOE_ACT_F32); a stride is
+ *            a multiple of the value's size, at least n values; rows past a
+ *            group's count are left as they were
+ * k is a multiple of 32; k and n at most 2^24, max_rows at most 2^24, groups
+ * at most 4096, groups * max_rows and groups * n at most 2^30.  A product
+ * with no rows or no groups does nothing. */
+int moe_mx_gemm(int32_t out_dtype, int32_t groups, int64_t max_rows, int64_t n, int64_t k,
+                const moe_mx_rows* a, const int32_t* counts, const moe_mx_rows* b, void* out,
+                int64_t out_stride_bytes, void* stream);
+
+/* Device bytes moe_mx_expert_gemm needs beside the layer's workspace (host
+ * only): the MX-FP4 rows of live_waves waves.  Needs latent and
+ * expert_hidden to be multiples of 32. */
+int moe_mx_workspace_size(const moe_dims* dims, size_t* bytes);
+
+/* moe_expert_gemm with MX-FP4 experts: for each expert j of the wave and each
+ * kept row r, q = mx(r), h = mx(silu(a)*b) with a = q . W_gate^T and
+ * b = q . W_up^T (fp32, quantised without a rounding in between), and
+ * y = act(h . W2^T) is written to the return row.  Arguments as for
+ * moe_expert_gemm, with
+ *   w13      MX-FP4 rows [X][2H] of L values: per local expert, H gate rows
+ *            then H up rows
+ *   w2       MX-FP4 rows [X][L] of H values
+ *   ws_mx    moe_mx_workspace_size() bytes; block w mod live_waves serves
+ *            wave w, as in `ws` */
+int moe_mx_expert_gemm(const moe_dims* dims, int32_t wave, const void* wave_buf, const void* recv_pools,
+                       int64_t src_stride_bytes, const int32_t* row_src, const int32_t* wave_count,
+                       const moe_mx_rows* w13, const moe_mx_rows* w2, void* ret_pools,
+                       int64_t ret_src_stride_bytes, void* ws, void* ws_mx, void* stream);
+
+/* --------------------------------------------------------- few-token layer
+ * A whole layer for a few tokens (a decode step): dims.tokens <= 64.  No
+ * exchange and no capacity: the tokens' own rank holds the experts of
+ * dims.my_rank (all of them with n_ranks = 1) and computes
+ *   logits = x . W_r^T + bias, the top-k and its softmax as moe_route,
+ *   z = x . W_down^T, h = silu(z . W_gate^T) * (z . W_up^T) per chosen expert,
+ *   c = sum_i topk_w[i] * (h_i . W2^T) over the chosen experts held here,
+ *   out = act(c . U^T + sum_j h_s[j] . W2_j^T), h_s as moe_shared_experts,
+ * with nothing rounded below fp32 before `out` (products with bf16 weights
+ * take the fp32 activations as two bf16 parts, 2^-17 off at most).  With
+ * n_ranks > 1 and the tokens on every rank, the ranks' outputs add up to the
+ * layer's if one of them passes the shared experts and the others
+ * shared_experts = 0.  Capacity factors, waves and the wave fields of dims
+ * play no part and are not looked at, and any number of experts may be held
+ * here; fp32 layers take any widths.  T * k <= 2048 follows; the products of
+ * the chosen experts are limited to 2^30 groups of 16 hidden units.
+ *   x, w_router, w_down, bias, bias_row_tokens, w_up, ws13, ws2: as for
+ *            moe_route, moe_shared_experts and moe_combine
+ *   w13, w2  [X][2H][L] and [X][L][H] act, or their MX-FP4 codes (bf16 layers
+ *            with L and H multiples of 32) with w13_scales and w2_scales set,
+ *            rows at the smallest strides (moe_mx_strides)
+ *   topk_idx [T][k] int32, topk_w [T][k] fp32, out [T][D] act: outputs
+ *   ws       moe_few_workspace_size() bytes, used by one call at a time */
+#define MOE_FEW_TOKENS_MAX 64
+int moe_few_workspace_size(const moe_dims* dims, size_t* bytes);
+int moe_few_tokens(const moe_dims* dims, const void* x, const void* w_router, const void* w_down,
+                   const float* bias, int32_t bias_row_tokens, const void* w13, const void* w13_scales,
+                   const void* w2, const void* w2_scales, const void* w_up, const void* ws13,
+                   const void* ws2, int32_t* topk_idx, float* topk_w, void* out, void* ws, void* stream);
 
 #ifdef __cplusplus
 }
