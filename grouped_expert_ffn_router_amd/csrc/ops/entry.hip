@@ -156,7 +156,7 @@ int moe_mx_gemm(int32_t out_dtype, int32_t groups, int64_t max_rows, int64_t n, 
   int rc = mx_cols(k, "k");
   if (rc) return rc;
   if (groups > 4096 || max_rows > (1 << 24) || groups * max_rows > (1ll << 30) || groups * n > (1ll << 30) ||
-      groups * ceil_div(max_rows, 256) * ceil_div(n, 256) > (1ll << 30))
+      groups * ceil_div(max_rows, 256) * ceil_div(n, 256) > (1ll << 28))
     return fail(MOE_EINVAL, "groups, max_rows or n exceed the kernels' index range");
   if (groups == 0 || max_rows == 0) return MOE_OK;
   if ((rc = mx_rows_ok(a, k, "a")) || (rc = mx_rows_ok(b, k, "b"))) return rc;

@@ -227,6 +227,30 @@ struct MxARows {  // rows of group g: bank rows g * group_rows .., or end to end
   }
 };
 
+// Tile of workgroup `bid`: the tiles of the rows that exist, group by group and
+// 4 tile rows at a time inside a group, in 8 contiguous ranges, one for each
+// XCD (workgroups go round-robin to the XCDs), so that an XCD's L2 sees
+// neighbouring tiles.  False: none is left.
+template <int BM>
+__device__ __forceinline__ bool mx_tile_of(const MxARows& a, int groups, int tiles_n, int bid, int& g, int& tm, int& tn) {
+  int total = 0;
+  for (int i = 0; i < groups; ++i) total += (a.rows(i) + BM - 1) / BM * tiles_n;
+  const int xcd = bid & 7, idx = bid >> 3, per = total >> 3, rem = total & 7;
+  if (idx >= per + (xcd < rem ? 1 : 0)) return false;
+  int t = xcd * per + min(xcd, rem) + idx, mt = 0;
+  for (g = 0; g < groups; ++g) {
+    mt = (a.rows(g) + BM - 1) / BM;
+    if (t < mt * tiles_n) break;
+    t -= mt * tiles_n;
+  }
+  constexpr int GROUP_M = 4;
+  const int gid = t / (GROUP_M * tiles_n), first = gid * GROUP_M, size = min(mt - first, GROUP_M);
+  const int rest = t - gid * GROUP_M * tiles_n;
+  tm = first + rest % size;
+  tn = rest / size;
+  return true;
+}
+
 struct MxBRows {
   MxView v;
   int n;
@@ -252,10 +276,9 @@ struct EMxOut {
   char* out;
   int64_t ldo;  // bytes
   int64_t group_rows;
-  bool vec, wide;  // rows aligned to 4 values; to 16 bytes with n a multiple of 8 (the staged epilogue)
+  bool vec, wide;  // rows aligned to 4 values; to 16 bytes with n a multiple of 8
   struct Row { T* p; };
   __device__ Row row(int g, int m) const { return {(T*)(out + (g * group_rows + m) * ldo)}; }
-  __device__ bool staged_tile(int) const { return wide; }
   __device__ int64_t row_key(int g, int m) const { return g * group_rows + m; }
   __device__ T* key_dst(int64_t key) const { return (T*)(out + key * ldo); }
   __device__ void store4(const Row& r, int n, int N, const float* v) const {
@@ -274,18 +297,18 @@ __device__ __forceinline__ i32x8 mx_operand(i32x4 v) { return __builtin_shufflev
 
 // ------------------------------------------------------------ product, few rows
 //
-// A workgroup of 4 waves computes 16 columns (rows of B) for up to 16 * MT
+// A workgroup of NW waves computes 16 columns (rows of B) for up to 16 * MT
 // rows of A, straight from memory: the waves take K in pieces of 512 in turn
 // and their sums meet in LDS.  v_mfma_scale_f32_16x16x128: a lane holds one
 // block of one row (16 bytes of codes) and its scale byte.  The 16 scales of
 // a 512-piece are one 16-byte load, whose dword j holds the scales of MFMA j.
 // The last piece may end early: codes past the row are read from its last
 // block, and their scales are 0 on both sides (2^-254: nothing in fp32).
-template <int MT, class T>
-__global__ void __launch_bounds__(256)
+template <int MT, int NW, class T>
+__global__ void __launch_bounds__(NW * 64)
 mx_gemm_rows(MxARows a, MxBRows b, EMxOut<T> e, int N, int K) {
-  const int g = blockIdx.z, M = a.rows(g), m0 = blockIdx.y * 16 * MT, n0 = blockIdx.x * 16;
-  if (m0 >= M) return;
+  const int g = blockIdx.y, M = a.rows(g), n0 = blockIdx.x * 16;
+  if (M <= 0) return;
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, r16 = lane & 15, grp = lane >> 4;
   const int nb = K / MX_BLOCK, pieces = (nb + 15) / 16;
   const int64_t br = b.index(g, min(n0 + r16, N - 1));
@@ -294,14 +317,14 @@ mx_gemm_rows(MxARows a, MxBRows b, EMxOut<T> e, int N, int K) {
   const uint8_t *ac[MT], *as[MT];
 #pragma unroll
   for (int t = 0; t < MT; ++t) {
-    const int64_t ar = a.index(g, min(m0 + t * 16 + r16, M - 1));
+    const int64_t ar = a.index(g, min(t * 16 + r16, M - 1));
     ac[t] = a.v.codes + ar * a.v.ldc;
     as[t] = a.v.scales + ar * a.v.lds;
   }
   f32x4 acc[MT];
 #pragma unroll
   for (int t = 0; t < MT; ++t) acc[t] = f32x4{0.f, 0.f, 0.f, 0.f};
-  for (int p = wave; p < pieces; p += 4) {
+  for (int p = wave; p < pieces; p += NW) {
     int64_t off[4];
     uint32_t keep[4];
 #pragma unroll
@@ -332,14 +355,17 @@ mx_gemm_rows(MxARows a, MxBRows b, EMxOut<T> e, int N, int K) {
       }
     }
   }
-  // lane: row m0 + 16 t + lane % 16, columns n0 + 4 (lane / 16) ..
-  __shared__ f32x4 part[4][MT][64];
+  // lane: row 16 t + lane % 16, columns n0 + 4 (lane / 16) ..
+  __shared__ f32x4 part[NW][MT][64];
 #pragma unroll
   for (int t = 0; t < MT; ++t) part[wave][t][lane] = acc[t];
   __syncthreads();
-  for (int t = wave; t < MT; t += 4) {
-    const f32x4 s = part[0][t][lane] + part[1][t][lane] + part[2][t][lane] + part[3][t][lane];
-    const int m = m0 + t * 16 + r16, n = n0 + grp * 4;
+  if (wave < MT) {
+    const int t = wave;
+    f32x4 s = part[0][t][lane];
+#pragma unroll
+    for (int w = 1; w < NW; ++w) s += part[w][t][lane];
+    const int m = t * 16 + r16, n = n0 + grp * 4;
     if (m < M && n < N) {
       const float v[4] = {s[0], s[1], s[2], s[3]};
       e.store4(e.row(g, m), n, N, v);
@@ -354,27 +380,35 @@ mx_gemm_rows(MxARows a, MxBRows b, EMxOut<T> e, int N, int K) {
 // row pieces (256 values here) with the same chunk swizzle, one 16-byte chunk
 // a lane and fragment: v_mfma_scale_f32_32x32x64_f8f6f4 takes a block of 32
 // values of one row from each lane, four times the bf16 instruction's work for
-// the same LDS bytes and the same number of cycles.  Lane (row, half) of
-// fragment step ks holds block 2 ks + half of the step's eight.
+// the same LDS bytes and the same 32 cycles.  Lane (row, half) of fragment step
+// ks holds block 2 ks + half of the step's eight.
 //
 // Scales: a row's 16 scale bytes of two K steps are one 16-byte piece, so one
-// more global->LDS load a thread every second step brings in those of all 512
-// rows (two buffers of 8 KB).  A lane reads the 4 bytes of a row and half a
-// step, shifts its half's bytes down once, and the MFMA picks byte 0 or 2.
+// more global->LDS load a thread every second step brings in those of all
+// rows (two buffers).  A lane reads the 4 bytes of a row and half a step,
+// shifts its half's bytes down once, and the MFMA picks byte 0 or 2.
 //
 // A last step that reaches past K reads the row's last block again in the
 // place of what is missing, and clears the scales of those blocks on both
 // sides: 2^-254 times at most 36 adds nothing to an fp32 sum.
+//
+// A tile of 128 x 128 by 4 waves (2 x 2, 64 x 64 each) has the same layout;
+// two such workgroups share a CU.
+template <int B_>
 struct MxTile {
-  static constexpr int BM = 256, BN = 256, NT = 512, WTM = 128, WTN = 64, FM = 4, FN = 2, NF = FM + FN;
+  static_assert(B_ == 256 || B_ == 128, "a wave loads 32 rows of each operand");
+  static constexpr int BM = B_, BN = B_, NW = B_ / 32, NT = NW * 64;
+  static constexpr int WN = NW / 2, WTM = BM / 2, WTN = 64;  // waves along n; a wave's part of the tile
+  static constexpr int FM = WTM / 32, FN = 2, NF = FM + FN;
   static constexpr int ROW = 128, STAGE = (BM + BN) * ROW;  // bytes of an LDS row and of one buffer
   static constexpr int RPW = 32, WBYTES = RPW * ROW;        // rows of each operand that one wave loads
   static constexpr int SCALES = (BM + BN) * 16;             // bytes of one scale buffer
   static constexpr int STEP = 8;                            // 32-value blocks of one K step
 };
 
+template <int FM>
 struct MxFrags {
-  i32x4 a[MxTile::FM], b[MxTile::FN];
+  i32x4 a[FM], b[2];
 };
 
 __device__ __forceinline__ void mx_read16(i32x4& v, uint32_t addr) {
@@ -385,17 +419,82 @@ __device__ __forceinline__ void mx_read4(int& v, uint32_t addr) {
 }
 // Every LDS read so far has landed; the registers pass through, so that their
 // consumers stay behind it.
-__device__ __forceinline__ void mx_wait(MxFrags& f) {
+__device__ __forceinline__ void mx_wait(MxFrags<4>& f) {
   asm volatile("s_waitcnt lgkmcnt(0)"
                : "+v"(f.a[0]), "+v"(f.a[1]), "+v"(f.a[2]), "+v"(f.a[3]), "+v"(f.b[0]), "+v"(f.b[1])::"memory");
 }
-__device__ __forceinline__ void mx_wait(MxFrags& f, int (&s)[MxTile::NF]) {
+__device__ __forceinline__ void mx_wait(MxFrags<4>& f, int (&s)[6]) {
   asm volatile("s_waitcnt lgkmcnt(0)"
                : "+v"(f.a[0]), "+v"(f.a[1]), "+v"(f.a[2]), "+v"(f.a[3]), "+v"(f.b[0]), "+v"(f.b[1]), "+v"(s[0]),
                  "+v"(s[1]), "+v"(s[2]), "+v"(s[3]), "+v"(s[4]), "+v"(s[5])::"memory");
 }
+__device__ __forceinline__ void mx_wait(MxFrags<2>& f) {
+  asm volatile("s_waitcnt lgkmcnt(0)" : "+v"(f.a[0]), "+v"(f.a[1]), "+v"(f.b[0]), "+v"(f.b[1])::"memory");
+}
+__device__ __forceinline__ void mx_wait(MxFrags<2>& f, int (&s)[4]) {
+  asm volatile("s_waitcnt lgkmcnt(0)"
+               : "+v"(f.a[0]), "+v"(f.a[1]), "+v"(f.b[0]), "+v"(f.b[1]), "+v"(s[0]), "+v"(s[1]), "+v"(s[2]), "+v"(s[3])
+               ::"memory");
+}
 
-// Hidden rows out of a gate / up tile: a wave's 64 columns are the 32 gate and
+// A bf16 tile by way of LDS (free of operands by now), whole row pieces at a
+// time: the accumulators' own stores would write 8 bytes (2 where a row is not
+// aligned) of 32 different rows each.  16-byte chunks are swizzled by row.
+template <class C, class E>
+__device__ __forceinline__ void mx_staged(const E& e, int m0, int n0, int M, int N, char* smem, const int64_t* keys,
+                                          const f32x16 (&acc)[C::FM][C::FN]) {
+  constexpr int RB = C::BN * 2, CH = RB / 16;
+  static_assert(C::BM * RB <= 2 * C::STAGE, "the staged tile fits the operand buffers");
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int wm = wave / C::WN, wn = wave % C::WN, frow = lane & 31, half = lane >> 5;
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < C::FM; ++i) {
+    const int row = wm * C::WTM + i * 32 + frow;
+#pragma unroll
+    for (int j = 0; j < C::FN; ++j)
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const int byte = (wn * C::WTN + j * 32 + q * 8 + half * 4) * 2;
+        const float v[4] = {acc[i][j][q * 4], acc[i][j][q * 4 + 1], acc[i][j][q * 4 + 2], acc[i][j][q * 4 + 3]};
+        *(uint2*)(smem + row * RB + (((byte >> 4) ^ (row & (CH - 1))) << 4) + (byte & 15)) = pack_bf16x4(v);
+      }
+  }
+  __syncthreads();
+  if (e.wide) {
+    constexpr int RPI = 64 / CH;  // rows a store instruction covers
+    const int c = lane % CH;
+#pragma unroll 4
+    for (int it = 0; it < C::RPW / RPI; ++it) {
+      const int row = wave * C::RPW + it * RPI + lane / CH;
+      if (m0 + row < M && n0 + c * 8 < N)
+        *(uint4*)(e.key_dst(keys[row]) + n0 + c * 8) = *(const uint4*)(smem + row * RB + ((c ^ (row & (CH - 1))) << 4));
+    }
+  } else {
+    constexpr int R = 8, X = C::BN / 64;  // rows in flight, 64-column pieces of a row
+    for (int r0 = 0; r0 < C::RPW; r0 += R) {
+      bf16_t v[R][X];
+#pragma unroll
+      for (int r = 0; r < R; ++r)
+#pragma unroll
+        for (int x = 0; x < X; ++x) {
+          const int row = wave * C::RPW + r0 + r, col = x * 64 + lane;
+          v[r][x] = *(const bf16_t*)(smem + row * RB + (((col >> 3) ^ (row & (CH - 1))) << 4) + (col & 7) * 2);
+        }
+#pragma unroll
+      for (int r = 0; r < R; ++r) {
+        const int row = wave * C::RPW + r0 + r;
+        if (m0 + row >= M) return;
+        bf16_t* dst = e.key_dst(keys[row]) + n0;
+#pragma unroll
+        for (int x = 0; x < X; ++x)
+          if (n0 + x * 64 + lane < N) dst[x * 64 + lane] = v[r][x];
+      }
+    }
+  }
+}
+
+// Hidden rows out of a gate / up tile: 64 columns of a wave are the 32 gate and
 // the 32 up columns of one block of hidden units, 16 of them in this lane and
 // 16 in lane ^ 32, so silu(gate) * up is quantised where it is: one exchange
 // for the block's maximum and one that pairs the halves' codes.
@@ -433,42 +532,35 @@ struct EMxHidden {
   }
 };
 
-// grid: gemm_grid(groups * ceil(max_rows / 256) * tiles_n, P); block: 512.
-template <bool GATEUP, class B, class E>
-__global__ void __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(2, 2)))
-mx_gemm_tile(MxARows a, B b, E e, int N, int K, int groups, int tiles_n, int P) {
-  using C = MxTile;
-  constexpr int FM = C::FM, FN = C::FN, NF = C::NF;
+// grid: gemm_grid of the tiles; block: C::NT.
+template <class C, bool GATEUP, class B, class E>
+__global__ void __launch_bounds__(C::NT) __attribute__((amdgpu_waves_per_eu(2, 2)))
+mx_gemm_tile(MxARows a, B b, E e, int N, int K, int groups, int tiles_n) {
+  constexpr int FM = C::FM, FN = C::FN, NF = C::NF, NMMA = FM * FN;
   __shared__ __attribute__((aligned(1024))) char smem[2 * C::STAGE + 2 * C::SCALES];
   const int nch = K / MX_BLOCK, nk = (nch + C::STEP - 1) / C::STEP;
-  const TailPlan plan = tail_plan(a, groups, tiles_n, nk, P, false);
-  int t, kb, ke, slot;
-  if (!block_work(plan, nk, blockIdx.x, t, kb, ke, slot)) return;
   int g, tm, tn;
-  tile_coords(a, groups, tiles_n, t, g, tm, tn);
+  if (!mx_tile_of<C::BM>(a, groups, tiles_n, blockIdx.x, g, tm, tn)) return;
   const int M = a.rows(g);
   const int m0 = tm * C::BM, n0 = tn * C::BN;
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-  const int wm = wave >> 2, wn = wave & 3;
+  const int wm = wave / C::WN, wn = wave % C::WN;
   __shared__ int64_t keys[E::STAGED ? C::BM : 1];
-  int64_t my_key = -1;
-  bool staged = false;
-  if constexpr (E::STAGED) {
-    staged = e.staged_tile(n0);
-    if (staged && tid < C::BM && m0 + tid < M) my_key = e.row_key(g, m0 + tid);
-  }
+  if constexpr (E::STAGED)  // where the tile's rows go, looked up while the first loads are under way
+    if (tid < C::BM && m0 + tid < M) keys[tid] = e.row_key(g, m0 + tid);
 
-  // codes: slot d of a wave holds rows 32 wave + 8 d + lane / 8; the load's
+  // codes: load d of a wave brings in rows 32 wave + 8 d + lane / 8; its
   // immediate offset moves both addresses by 1024 d, taken off the row pointer
   const int lrow = lane >> 3, lcol = lane & 7;
   const int gcol = lcol ^ swz(wave * C::RPW + lrow);  // rows 8 further: ^ 4
   const uint8_t *pa[4], *pb[4];
 #pragma unroll
   for (int d = 0; d < 4; ++d) {
-    pa[d] = a.v.codes + a.index(g, min(m0 + wave * C::RPW + d * 8 + lrow, M - 1)) * a.v.ldc - 1024 * d;
-    pb[d] = b.v.codes + b.index(g, min(n0 + wave * C::RPW + d * 8 + lrow, N - 1)) * b.v.ldc - 1024 * d;
+    const int row = wave * C::RPW + d * 8 + lrow;
+    pa[d] = a.v.codes + a.index(g, min(m0 + row, M - 1)) * a.v.ldc - 1024 * d;
+    pb[d] = b.v.codes + b.index(g, min(n0 + row, N - 1)) * b.v.ldc - 1024 * d;
   }
-  // scales: thread tid brings in row tid of A (below 256) or of B
+  // scales: thread tid brings in row tid of A (below BM) or of B
   const uint8_t* ps = tid < C::BM ? a.v.scales + a.index(g, min(m0 + tid, M - 1)) * a.v.lds
                                   : b.v.scales + b.index(g, min(n0 + tid - C::BM, N - 1)) * b.v.lds;
 
@@ -486,8 +578,9 @@ mx_gemm_tile(MxARows a, B b, E e, int N, int K, int groups, int tiles_n, int P) 
 #pragma unroll
       for (int v = 0; v < 16; ++v) acc[i][j][v] = 0.f;
 
+  MxFrags<FM> F[2];
   int sc[2][NF];  // the scale bytes of substeps 2 w and 2 w + 1 (bytes 0 and 2)
-  auto read_codes = [&](MxFrags& f, int kt, int ks, int q) {
+  auto read_codes = [&](MxFrags<FM>& f, int kt, int ks, int q) {
     const uint32_t st = (uint32_t)((kt & 1) * C::STAGE) + (uint32_t)(((ks * 2 + half) ^ fswz) << 4);
     if (q < FM) mx_read16(f.a[q], fa_base + st + q * 32 * C::ROW);
     else mx_read16(f.b[q - FM], fb_base + st + (q - FM) * 32 * C::ROW);
@@ -513,7 +606,6 @@ mx_gemm_tile(MxARows a, B b, E e, int N, int K, int groups, int tiles_n, int P) 
     auto lp = (__attribute__((address_space(3))) void*)(smem + 2 * C::STAGE + (pair & 1) * C::SCALES + wave * 1024);
     __builtin_amdgcn_global_load_lds((const void*)(ps + (int64_t)pair * 16), lp, 16, 0, 0);
   };
-
   // Scale dwords are read one half step ahead, where their registers are
   // free: those of substeps 0 and 1 in the last substep of the step before,
   // those of 2 and 3 in the first of their own.
@@ -521,21 +613,20 @@ mx_gemm_tile(MxARows a, B b, E e, int N, int K, int groups, int tiles_n, int P) 
 #pragma unroll
     for (int q = 0; q < NF; ++q) sc[w][q] = (int)(((uint32_t)sc[w][q] >> (8 * half)) & keep);
   };
-  MxFrags F[2];
   // MODE 0: issues the loads of step kt + 2; 1: no new loads; 2: the last
   // step.  HALF: loads 4..7 of step kt + 1 were left to this step's start.
   auto substep = [&](int kt, auto ks_tag, auto mode_tag, auto half_tag) {
     constexpr int ks = decltype(ks_tag)::value, MODE = decltype(mode_tag)::value;
     constexpr bool HALF = decltype(half_tag)::value;
     constexpr int SEL = (ks & 1) * 2;
-    MxFrags& cur = F[ks & 1];
-    MxFrags& nxt = F[(ks + 1) & 1];
+    MxFrags<FM>& cur = F[ks & 1];
+    MxFrags<FM>& nxt = F[(ks + 1) & 1];
     if constexpr (ks == 3 && MODE != 2) {
       vm_wait<0>();   // step kt + 1's codes and scales (this lane's part)
       lds_barrier();  // ... every lane's; every wave is done with step kt's buffers
     }
 #pragma unroll
-    for (int q = 0; q < FM * FN; ++q) {
+    for (int q = 0; q < NMMA; ++q) {
       const int j = q / FM, i = q % FM;
       acc[i][j] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(mx_operand(cur.b[j]), mx_operand(cur.a[i]), acc[i][j],
                                                                   4, 4, SEL, sc[ks >> 1][FM + j], SEL, sc[ks >> 1][i]);
@@ -545,7 +636,7 @@ mx_gemm_tile(MxARows a, B b, E e, int N, int K, int groups, int tiles_n, int P) 
           if (q < NF) read_scales(kt, 1, q);
           if (HALF && q < 4) load_codes(kt + 1, 4 + q);
           // the scales of the next pair of steps, into the buffer that step kt - 1 was the last to use
-          if (q == 4 && MODE == 0 && !(kt & 1)) load_scales(kt / 2 + 1);
+          if (q == NMMA - 1 && MODE == 0 && !(kt & 1)) load_scales(kt / 2 + 1);
         }
       } else if constexpr (MODE != 2) {
         if (q < NF) {
@@ -605,30 +696,47 @@ mx_gemm_tile(MxARows a, B b, E e, int N, int K, int groups, int tiles_n, int P) 
   }
 
   if constexpr (GATEUP) {
-    const int n = n0 + wn * C::WTN;
 #pragma unroll
-    for (int i = 0; i < FM; ++i)
-      e.store(g, m0 + wm * C::WTM + i * 32 + frow, M, n >> 6, n < N, half, acc[i][0], acc[i][1]);
+    for (int j = 0; j < FN; j += 2) {
+      const int n = n0 + wn * C::WTN + j * 32;
+#pragma unroll
+      for (int i = 0; i < FM; ++i)
+        e.store(g, m0 + wm * C::WTM + i * 32 + frow, M, n >> 6, n < N, half, acc[i][j], acc[i][j + 1]);
+    }
   } else {
     if constexpr (E::STAGED) {
-      if (staged) {  // uniform per workgroup
-        staged_epilogue<TileCfg<256, 256>, false>(e, m0, n0, M, N, smem, keys, my_key, acc);
-        return;
-      }
-    }
+      mx_staged<C>(e, m0, n0, M, N, smem, keys, acc);
+    } else {
 #pragma unroll
-    for (int i = 0; i < FM; ++i)
-      epilogue_row<false, FN>(e, g, m0 + wm * C::WTM + i * 32 + frow, M, n0 + wn * C::WTN, N, half, acc[i]);
+      for (int i = 0; i < FM; ++i)
+        epilogue_row<false, FN>(e, g, m0 + wm * C::WTM + i * 32 + frow, M, n0 + wn * C::WTN, N, half, acc[i]);
+    }
   }
 }
 
+template <class C, bool GATEUP, class B, class E>
+hipError_t run_mx_tiles(const MxARows& a, const B& b, const E& e, int N, int K, int groups, hipStream_t st) {
+  const int64_t tiles_n = (N + C::BN - 1) / C::BN, tiles = groups * (((int64_t)a.max_rows + C::BM - 1) / C::BM) * tiles_n;
+  if (tiles <= 0) return hipSuccess;
+  launch((mx_gemm_tile<C, GATEUP, B, E>), dim3((unsigned)(8 * ((tiles + 7) / 8))), dim3(C::NT), 0, st, a, b, e, N, K,
+         groups, (int)tiles_n);
+  return hipGetLastError();
+}
+
+// Rounds of the card's CUs that the tiles take: one workgroup of 256 x 256 a
+// CU, or two of 128 x 128, which together take MX_SMALL_ROUND of a large
+// tile's time for half of its work.
+constexpr double MX_SMALL_ROUND = 0.65;
+
 template <bool GATEUP, class B, class E>
 hipError_t run_mx_tile(const MxARows& a, const B& b, const E& e, int N, int K, int groups, int cus, hipStream_t st) {
-  const int64_t tiles_n = (N + 255) / 256, tiles = groups * ((a.max_rows + 255) / 256) * tiles_n;
-  if (tiles <= 0) return hipSuccess;
-  launch((mx_gemm_tile<GATEUP, B, E>), dim3((unsigned)gemm_grid(tiles, cus)), dim3(512), 0, st, a, b, e, N, K, groups,
-         (int)tiles_n, cus);
-  return hipGetLastError();
+  auto rounds = [&](int64_t tile, int64_t at_once) {
+    const int64_t tiles = groups * ((a.max_rows + tile - 1) / tile) * ((N + tile - 1) / tile);
+    return (double)((tiles + at_once - 1) / at_once);
+  };
+  if (rounds(128, 2 * cus) * MX_SMALL_ROUND < rounds(256, cus))
+    return run_mx_tiles<MxTile<128>, GATEUP>(a, b, e, N, K, groups, st);
+  return run_mx_tiles<MxTile<256>, GATEUP>(a, b, e, N, K, groups, st);
 }
 
 template <class T>
@@ -637,15 +745,19 @@ hipError_t run_mx_gemm(const MxGemmArgs& q, int cus, hipStream_t st) {
   const MxBRows b{q.b, q.n};
   const uintptr_t at = (uintptr_t)q.out | (uintptr_t)q.ldo;
   const EMxOut<T> e{(char*)q.out, q.ldo, q.max_rows, at % (4 * sizeof(T)) == 0, at % 16 == 0 && q.n % 8 == 0};
-  const dim3 grid((unsigned)((q.n + 15) / 16), 1, (unsigned)q.groups);
-  if (q.max_rows <= 16)
-    launch((mx_gemm_rows<1, T>), grid, dim3(256), 0, st, a, b, e, q.n, q.k);
-  else if (q.max_rows <= 32)
-    launch((mx_gemm_rows<2, T>), grid, dim3(256), 0, st, a, b, e, q.n, q.k);
-  else if (q.max_rows <= 64)
-    launch((mx_gemm_rows<4, T>), grid, dim3(256), 0, st, a, b, e, q.n, q.k);
-  else
-    return run_mx_tile<false>(a, b, e, q.n, q.k, q.groups, cus, st);
+  if (q.max_rows > 64) return run_mx_tile<false>(a, b, e, q.n, q.k, q.groups, cus, st);
+  // one wave for each 512-piece of K, as far as a workgroup goes
+  const dim3 grid((unsigned)((q.n + 15) / 16), (unsigned)q.groups);
+  const int pieces = (q.k + 511) / 512;
+  auto rows = [&](auto mt) {
+    constexpr int MT = decltype(mt)::value;
+    if (pieces <= 4) launch((mx_gemm_rows<MT, 4, T>), grid, dim3(256), 0, st, a, b, e, q.n, q.k);
+    else if (pieces <= 8) launch((mx_gemm_rows<MT, 8, T>), grid, dim3(512), 0, st, a, b, e, q.n, q.k);
+    else launch((mx_gemm_rows<MT, 16, T>), grid, dim3(1024), 0, st, a, b, e, q.n, q.k);
+  };
+  if (q.max_rows <= 16) rows(std::integral_constant<int, 1>());
+  else if (q.max_rows <= 32) rows(std::integral_constant<int, 2>());
+  else rows(std::integral_constant<int, 4>());
   return hipGetLastError();
 }
 
@@ -663,6 +775,7 @@ hipError_t launch_mx_gate_up(const MxExpertArgs& g, int cus, hipStream_t st) {
 template <class T>
 struct EMxReturn : EScatter<T> {
   static constexpr bool STAGED = sizeof(T) == 2;  // the staged copy of a tile is bf16
+  static constexpr bool wide = true;              // latent is a multiple of 64 in bf16 layers
 };
 
 template <class T>

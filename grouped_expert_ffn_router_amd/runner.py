@@ -18,6 +18,8 @@ are provided:
   view: zero copies.
 """
 
+import contextlib
+
 import numpy as np
 import torch
 
@@ -674,19 +676,34 @@ class RaggedAllRanksLayer:
 _DTYPE = {torch.bfloat16: B.MOE_ACT_BF16, torch.float32: B.MOE_ACT_F32}
 
 
+_HERE = contextlib.nullcontext()
+
+
 def _on(t):
     """(stream handle, device guard) for work on tensor t: its device's current stream."""
     if not t.is_cuda:
         raise ValueError("the library works on GPU tensors")
-    return torch.cuda.current_stream(t.device).cuda_stream, torch.cuda.device(t.device)
+    index = t.device.index
+    stream = torch.cuda.current_stream(index).cuda_stream
+    # a guard costs as much as a launch: only where the device is not the current one
+    return stream, _HERE if index == torch.cuda.current_device() else torch.cuda.device(index)
+
+
+def _mx_strides(cols):
+    """B.mx_strides without the call (it also refuses what that refuses)."""
+    if cols <= 0 or cols % 32 or cols > 1 << 24:
+        return B.mx_strides(cols)
+    return cols // 2, (cols // 32 + 15) // 16 * 16
 
 
 def _row_stride(t, what):
     """Elements from row to row of t [..., rows, cols], whose rows must be evenly spaced and contiguous."""
+    if t.dim() >= 2 and t.is_contiguous():
+        return max(t.shape[-1], 1)
     if t.dim() < 2 or t.stride(-1) != 1 and t.shape[-1] > 1:
         raise ValueError(f"{what}: rows of contiguous values are needed")
-    if t.numel() == 0:
-        return max(t.shape[-1], 1)
+    if t.dim() == 2:
+        return t.stride(0)
     stride = None
     rows = 1
     for size, st in zip(reversed(t.shape[:-1]), reversed(t.stride()[:-1])):
@@ -706,7 +723,7 @@ class MxRows:
     codes [..., rows, cols / 2] and scales [..., rows, cols / 32 rounded up to 16], uint8."""
 
     def __init__(self, codes, scales, cols):
-        cb, sb = B.mx_strides(cols)
+        cb, sb = _mx_strides(cols)
         if codes.dtype != torch.uint8 or scales.dtype != torch.uint8:
             raise TypeError("codes and scales are uint8")
         if codes.shape[:-1] != scales.shape[:-1] or codes.shape[-1] != cb or scales.shape[-1] < sb:
@@ -714,7 +731,23 @@ class MxRows:
         if codes.device != scales.device:
             raise ValueError("codes and scales are on different devices")
         self.codes, self.scales, self.cols = codes, scales, cols
-        self.arg = B.mx_rows(codes, scales, _row_stride(codes, "codes"), _row_stride(scales, "scales"))
+        self.code_stride, self.scale_stride = _row_stride(codes, "codes"), _row_stride(scales, "scales")
+        self._arg = None
+
+    @classmethod
+    def _made(cls, codes, scales, cols, code_stride, scale_stride):
+        """From contiguous tensors made here."""
+        q = cls.__new__(cls)
+        q.codes, q.scales, q.cols = codes, scales, cols
+        q.code_stride, q.scale_stride, q._arg = code_stride, scale_stride, None
+        return q
+
+    @property
+    def arg(self):
+        """moe_mx_rows of these tensors."""
+        if self._arg is None:
+            self._arg = B.mx_rows(self.codes, self.scales, self.code_stride, self.scale_stride)
+        return self._arg
 
     @property
     def shape(self):
@@ -734,28 +767,30 @@ class MxRows:
 
 def mx_quantize(x):
     """x [..., rows, cols] (bf16 or fp32, evenly spaced rows) as MxRows."""
-    if x.dtype not in _DTYPE:
+    code = _DTYPE.get(x.dtype)
+    if code is None:
         raise TypeError(f"mx_quantize takes bf16 or fp32, not {x.dtype}")
     st, dev = _on(x)
     ld = _row_stride(x, "x")
-    cols = x.shape[-1]
-    cb, sb = B.mx_strides(cols)
+    lead, cols = x.shape[:-1], x.shape[-1]
+    cb, sb = _mx_strides(cols)
     with dev:
-        codes = torch.empty(x.shape[:-1] + (cb,), dtype=torch.uint8, device=x.device)
-        scales = torch.empty(x.shape[:-1] + (sb,), dtype=torch.uint8, device=x.device)
-        B.mx_quantize(_DTYPE[x.dtype], x.numel() // cols, cols, x, ld * x.element_size(), codes, cb, scales, sb, st)
-    return MxRows(codes, scales, cols)
+        codes = torch.empty(lead + (cb,), dtype=torch.uint8, device=x.device)
+        scales = torch.empty(lead + (sb,), dtype=torch.uint8, device=x.device)
+        B.mx_quantize(code, x.numel() // cols, cols, x, ld * x.element_size(), codes, cb, scales, sb, st)
+    return MxRows._made(codes, scales, cols, cb, sb)
 
 
 def mx_dequantize(q, dtype=torch.bfloat16):
     """The values of MxRows q as a bf16 or fp32 tensor."""
-    if dtype not in _DTYPE:
+    code = _DTYPE.get(dtype)
+    if code is None:
         raise TypeError(f"mx_dequantize gives bf16 or fp32, not {dtype}")
     st, dev = _on(q.codes)
     with dev:
-        out = torch.empty(q.shape, dtype=dtype, device=q.codes.device)
-        B.mx_dequantize(_DTYPE[dtype], q.rows, q.cols, q.codes, q.arg.code_stride_bytes, q.scales,
-                        q.arg.scale_stride_bytes, out, q.cols * out.element_size(), st)
+        out = torch.empty(q.codes.shape[:-1] + (q.cols,), dtype=dtype, device=q.codes.device)
+        B.mx_dequantize(code, out.numel() // q.cols, q.cols, q.codes, q.code_stride, q.scales, q.scale_stride, out,
+                        q.cols * out.element_size(), st)
     return out
 
 
@@ -763,24 +798,25 @@ def mx_gemm(a, b, counts=None, out=None, dtype=torch.bfloat16):
     """out[g] = a[g] . b[g]^T of MxRows a [G, M, K] and b [G, N, K] (or [M, K] and
     [N, K]) as bf16 or fp32.  counts: int32 [G] rows of each group (the rows of
     `out` behind them are left as they were)."""
-    if len(a.shape) != len(b.shape) or len(a.shape) not in (2, 3) or a.cols != b.cols or a.shape[:-2] != b.shape[:-2]:
+    ca, cb = a.codes, b.codes
+    sa, sb = ca.shape, cb.shape
+    if len(sa) != len(sb) or len(sa) not in (2, 3) or a.cols != b.cols or sa[:-2] != sb[:-2]:
         raise ValueError(f"mx_gemm of rows {a.shape} and {b.shape}")
-    G = a.shape[0] if len(a.shape) == 3 else 1
-    M, N = a.shape[-2], b.shape[-2]
-    st, dev = _on(a.codes)
-    shape = a.shape[:-1] + (N,)
+    G = sa[0] if len(sa) == 3 else 1
+    M, N = sa[-2], sb[-2]
+    st, dev = _on(ca)
+    shape = sa[:-1] + (N,)
     with dev:
         if out is None:
-            out = (torch.empty if counts is None else torch.zeros)(shape, dtype=dtype, device=a.codes.device)
-        if tuple(out.shape) != shape or out.dtype not in _DTYPE:
-            raise ValueError(f"out {tuple(out.shape)} {out.dtype}, expected {shape} bf16 or fp32")
-        if counts is not None and (counts.dtype != torch.int32 or tuple(counts.shape) != (G,) or not counts.is_contiguous()):
+            out = (torch.empty if counts is None else torch.zeros)(shape, dtype=dtype, device=ca.device)
+        code = _DTYPE.get(out.dtype)
+        if out.shape != shape or code is None:
+            raise ValueError(f"out {tuple(out.shape)} {out.dtype}, expected {tuple(shape)} bf16 or fp32")
+        if counts is not None and (counts.dtype != torch.int32 or counts.shape != (G,) or not counts.is_contiguous()):
             raise ValueError("counts is a contiguous int32 tensor with one value a group")
-        for t in (b.codes, out) + (() if counts is None else (counts,)):
-            if t.device != a.codes.device:
-                raise ValueError("mx_gemm: tensors on different devices")
-        B.mx_gemm(_DTYPE[out.dtype], G, M, N, a.cols, a.arg, counts, b.arg, out,
-                  _row_stride(out, "out") * out.element_size(), st)
+        if cb.device != ca.device or out.device != ca.device or counts is not None and counts.device != ca.device:
+            raise ValueError("mx_gemm: tensors on different devices")
+        B.mx_gemm(code, G, M, N, a.cols, a.arg, counts, b.arg, out, _row_stride(out, "out") * out.element_size(), st)
     return out
 
 

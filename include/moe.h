@@ -375,8 +375,9 @@ typedef struct moe_mx_rows {
  *            a multiple of the value's size, at least n values; rows past a
  *            group's count are left as they were
  * k is a multiple of 32; k and n at most 2^24, max_rows at most 2^24, groups
- * at most 4096, groups * max_rows and groups * n at most 2^30.  A product
- * with no rows or no groups does nothing. */
+ * at most 4096, groups * max_rows and groups * n at most 2^30, and the output
+ * at most 2^28 tiles of 256 x 256.  A product with no rows or no groups does
+ * nothing. */
 int moe_mx_gemm(int32_t out_dtype, int32_t groups, int64_t max_rows, int64_t n, int64_t k,
                 const moe_mx_rows* a, const int32_t* counts, const moe_mx_rows* b, void* out,
                 int64_t out_stride_bytes, void* stream);

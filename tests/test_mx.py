@@ -92,6 +92,7 @@ def _gemm_args(**kw):
     (dict(max_rows=(1 << 24) + 1), B.MOE_EINVAL, "range"),
     (dict(groups=4096, max_rows=1 << 20), B.MOE_EINVAL, "range"),
     (dict(groups=4096, n=1 << 20), B.MOE_EINVAL, "range"),
+    (dict(groups=1, max_rows=1 << 24, n=1 << 21, out_stride_bytes=1 << 22), B.MOE_EINVAL, "range"),
     (dict(a=None), B.MOE_EINVAL, "a is NULL"),
     (dict(b=None), B.MOE_EINVAL, "b is NULL"),
     (dict(a=B.mx_rows(None, 256, 32, 16)), B.MOE_EINVAL, "a is NULL"),
@@ -300,6 +301,8 @@ def _gemm_case(G, M, N, K, act, kind, counts, seed=0, ldpad=0, offset=0):
     (1, 1, 1, 32, None), (1, 1, 16, 128, None), (1, 3, 17, 96, None), (1, 16, 64, 512, None), (1, 17, 33, 544, None),
     (1, 33, 100, 1056, None), (2, 64, 48, 2080, None), (3, 40, 20, 256, [0, 40, 7]), (4, 9, 5, 64, [-3, 100, 1, 0]),
     (1, 65, 64, 128, None), (1, 256, 256, 256, None), (1, 257, 255, 288, None), (1, 300, 520, 544, None),
+    # max_rows large enough for 256 x 256 tiles, whatever the counts
+    (1, 60000, 260, 800, [700]), (2, 30000, 250, 544, [257, 1]), (1, 33000, 512, 32, [300]), (1, 33000, 512, 512, [513]),
     (2, 511, 77, 1024, [511, 1]), (3, 300, 260, 800, [0, 299, 257]), (5, 130, 130, 2080, [128, 129, 0, 1, 130]),
 ])
 def test_gemm(G, M, N, K, counts, act):

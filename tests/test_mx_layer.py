@@ -127,7 +127,10 @@ def _check_returned_rows(lay, sh, r, w13, w2, pool_of, ret_of):
 
 
 def _layer(cls, name, gather, **kw):
+    from dataclasses import replace
     sh = configs.get(name)
+    if "recv_num" in kw:
+        sh = replace(sh, recv_num=kw.pop("recv_num"))
     inp = gen.generate(sh, seed=11)
     lay = cls(sh, inp, experts="mx", gather=gather, **kw)
     lay.run()
@@ -137,12 +140,14 @@ def _layer(cls, name, gather, **kw):
 
 
 @pytest.mark.gpu
-@pytest.mark.parametrize("name,gather", [("mini_bf16", "fused"), ("mini_bf16", "buffer"), ("mini_bf16_skew", "fused"),
-                                         ("mini_bf16_seg", "fused"), ("mini_bf16_longk", "buffer"), (1, "fused"),
-                                         (1, "buffer")])
-def test_returned_rows_of_every_rank(name, gather):
+@pytest.mark.parametrize("name,gather,recv_num", [
+    ("mini_bf16", "fused", 115), ("mini_bf16", "buffer", 115), ("mini_bf16_skew", "fused", 115), ("mini_bf16_seg", "fused", 115),
+    ("mini_bf16_longk", "buffer", 115), (1, "fused", 115), (1, "buffer", 115),
+    # a receive cap of many times the load: the products take their large tiles
+    ("mini_bf16", "fused", 10000), (1, "fused", 20000)])
+def test_returned_rows_of_every_rank(name, gather, recv_num):
     from grouped_expert_ffn_router_amd import runner
-    sh, inp, lay, w13, w2 = _layer(runner.AllRanksLayer, name, gather)
+    sh, inp, lay, w13, w2 = _layer(runner.AllRanksLayer, name, gather, recv_num=recv_num)
     act = torch.bfloat16 if sh.act == "bf16" else torch.float32
     L = sh.latent
     pools = lay.pools[..., :L * (2 if sh.act == "bf16" else 4)].contiguous().view(act).double().cpu().numpy()
