@@ -232,7 +232,13 @@ int moe_few_workspace_size(const moe_dims* dims, size_t* bytes) {
   const int rc = few_dims(dims, &f);
   if (rc) return rc;
   if (!bytes) return fail(MOE_EINVAL, "bytes is NULL");
-  *bytes = few_layout(f).total;
+  // enough for every smaller batch too (the shares of the down product depend on the tokens)
+  size_t most = 0;
+  for (; f.T > 0; --f.T) {
+    const size_t n = few_layout(f).total;
+    if (n > most) most = n;
+  }
+  *bytes = most;
   return MOE_OK;
 }
 
@@ -272,13 +278,13 @@ int moe_few_tokens(const moe_dims* dims, const void* x, const void* w_router, co
   a.h = {at<char>(ws, w.h), at<char>(ws, w.h_lo)};
   a.c = {at<char>(ws, w.c), at<char>(ws, w.c_lo)};
   a.part = at<float>(ws, w.part);
-  a.parts = w.parts;
+  a.arrived = at<int32_t>(ws, w.arrived);
+  a.parts = w.parts; a.tiles = w.tiles; a.down_rt = w.down_rt;
   hipStream_t st = (hipStream_t)stream;
   LAUNCH("few_project", launch_few_project(a, st), "moe_few_tokens project");
   LAUNCH("few_select", launch_few_select(a, st), "moe_few_tokens select");
   LAUNCH("few_gate_up", launch_few_gate_up(a, st), "moe_few_tokens gate/up");
   LAUNCH("few_down", launch_few_down(a, st), "moe_few_tokens down");
-  LAUNCH("few_sum", launch_few_sum(a, st), "moe_few_tokens sum");
   LAUNCH("few_up", launch_few_up(a, st), "moe_few_tokens up");
   return MOE_OK;
 }

@@ -21,8 +21,8 @@ struct FewAct {
 };
 
 struct FewWs {  // byte offsets
-  size_t logits, mask, active, first, count, gate, z, z_lo, hs, hs_lo, h, h_lo, part, c, c_lo, total;
-  int parts;  // fp32 partial sums of the combined rows
+  size_t logits, mask, active, first, count, gate, z, z_lo, hs, hs_lo, h, h_lo, part, c, c_lo, arrived, total;
+  int parts, tiles, down_rt;  // the down product: shares, row tiles, 16-row groups of a tile
 };
 FewWs few_layout(const FewDims& d);
 
@@ -43,14 +43,14 @@ struct FewArgs {
   int32_t* count;     // [0]: chosen experts
   float* gate;        // [T][X] routing weights of the chosen pairs
   FewAct z, hs, h, c; // [T][L], [T][S * HS], [T * k][H], [T][L]
-  float* part;        // [parts][T][L]
-  int parts;
+  float* part;        // [parts][T][L], where parts > 1
+  int32_t* arrived;   // [tiles] shares of a tile that are done
+  int parts, tiles, down_rt;
 };
 hipError_t launch_few_project(const FewArgs& a, hipStream_t st);
 hipError_t launch_few_select(const FewArgs& a, hipStream_t st);
 hipError_t launch_few_gate_up(const FewArgs& a, hipStream_t st);
 hipError_t launch_few_down(const FewArgs& a, hipStream_t st);
-hipError_t launch_few_sum(const FewArgs& a, hipStream_t st);
 hipError_t launch_few_up(const FewArgs& a, hipStream_t st);
 
 }  // namespace moe

@@ -190,10 +190,12 @@ __device__ __forceinline__ int64_t lo_offset(const FewAct& a) { return (const T*
 
 // ------------------------------------------------------------ phases
 
-// Sums of the waves' accumulators, in wave order; f(r, t, sum) gets the sums
-// of row tile r and token tile t (4 weight rows 4 g .. of token r16).
-template <int RT, int NT, class F>
+// Sums of the waves' accumulators, in wave order, G row tiles at a time (a
+// gate tile and its up tile together): f(group, t, sums) gets those of token
+// tile t, each 4 weight rows 4 g .. of token r16.
+template <int G, int RT, int NT, class F>
 __device__ __forceinline__ void reduce(f32x4 (&acc)[RT][NT], f32x4* lds, F f) {
+  static_assert(RT % G == 0, "whole groups");
   const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
   __syncthreads();
 #pragma unroll
@@ -201,14 +203,16 @@ __device__ __forceinline__ void reduce(f32x4 (&acc)[RT][NT], f32x4* lds, F f) {
 #pragma unroll
     for (int t = 0; t < NT; ++t) lds[((wave * RT + r) * NT + t) * 64 + lane] = acc[r][t];
   __syncthreads();
-  if (wave < NT) {  // wave t finishes token tile t
-    f32x4 s[RT];
+  for (int p = wave; p < RT / G * NT; p += NW) {
+    const int grp = p / NT, t = p % NT;
+    f32x4 s[G];
 #pragma unroll
-    for (int r = 0; r < RT; ++r) {
-      s[r] = lds[(r * NT + wave) * 64 + lane];
-      for (int w = 1; w < NW; ++w) s[r] += lds[((w * RT + r) * NT + wave) * 64 + lane];
+    for (int i = 0; i < G; ++i) {
+      s[i] = lds[((grp * G + i) * NT + t) * 64 + lane];
+#pragma unroll
+      for (int w = 1; w < NW; ++w) s[i] += lds[((w * RT + grp * G + i) * NT + t) * 64 + lane];
     }
-    f(wave, s);
+    f(grp, t, s);
   }
 }
 
@@ -223,33 +227,39 @@ __device__ __forceinline__ void zero(f32x4 (&acc)[RT][NT]) {
     for (int t = 0; t < NT; ++t) acc[r][t] = f32x4{0.f, 0.f, 0.f, 0.f};
 }
 
-// Items: 16 router rows, then 16 rows of W_down, then 16 hidden units of a shared expert.
+// Items: 16 RT router rows, then 16 RT rows of W_down, then 16 RT hidden units
+// of a shared expert (their gate and up rows).
+__host__ __device__ __forceinline__ int tiles_of(int n, int rows) { return (n + rows - 1) / rows; }
+template <int RT>
 __host__ __device__ __forceinline__ int project_items(const FewDims& d) {
-  return (d.E + 15) / 16 + (d.L + 15) / 16 + d.S * ((d.HS + 15) / 16);
+  return tiles_of(d.E, 16 * RT) + tiles_of(d.L, 16 * RT) + d.S * tiles_of(d.HS, 16 * RT);
 }
 
-template <class T, int NT>
-__device__ void project(const FewArgs& a, int item, f32x4* lds) {
+template <class T, int RT, int NT>
+__device__ __forceinline__ void project(const FewArgs& a, int item, f32x4* lds) {
   const FewDims& d = a.d;
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, r16 = lane & 15, g = lane >> 4;
   using W = typename Weights<T>::type;
   const T* hi[NT];
 #pragma unroll
   for (int t = 0; t < NT; ++t) hi[t] = (const T*)a.x + (int64_t)min(t * 16 + r16, d.T - 1) * d.D;
-  const int nr = (d.E + 15) / 16, nd = (d.L + 15) / 16;
+  const int nr = tiles_of(d.E, 16 * RT), nd = tiles_of(d.L, 16 * RT);
   if (item < nr + nd) {
     const bool router = item < nr;
-    const int n0 = (router ? item : item - nr) * 16, N = router ? d.E : d.L;
-    const W w[1] = {{(const T*)(router ? a.w_router : a.w_down) + (int64_t)min(n0 + r16, N - 1) * d.D}};
-    f32x4 acc[1][NT];
+    const int n0 = (router ? item : item - nr) * 16 * RT, N = router ? d.E : d.L;
+    W w[RT];
+#pragma unroll
+    for (int r = 0; r < RT; ++r)
+      w[r] = W{(const T*)(router ? a.w_router : a.w_down) + (int64_t)min(n0 + r * 16 + r16, N - 1) * d.D};
+    f32x4 acc[RT][NT];
     zero(acc);
-    dot<W, false, 1, NT>(acc, w, hi, 0, d.D, wave, NW);
-    reduce<1, NT>(acc, lds, [&](int t, const f32x4 (&s)[1]) {
+    dot<W, false, RT, NT>(acc, w, hi, 0, d.D, wave, NW);
+    reduce<1, RT, NT>(acc, lds, [&](int r, int t, const f32x4 (&s)[1]) {
       const int m = t * 16 + r16;
       if (m >= d.T) return;
 #pragma unroll
       for (int v = 0; v < 4; ++v) {
-        const int n = n0 + g * 4 + v;
+        const int n = n0 + r * 16 + g * 4 + v;
         if (n >= N) break;
         if (router) {
           float b = 0.f;
@@ -262,18 +272,23 @@ __device__ void project(const FewArgs& a, int item, f32x4* lds) {
     });
     return;
   }
-  const int ns = (d.HS + 15) / 16, i = item - nr - nd, j = i / ns, u0 = (i - j * ns) * 16;
-  const T* base = (const T*)a.ws13 + (int64_t)j * 2 * d.HS * d.D + (int64_t)min(u0 + r16, d.HS - 1) * d.D;
-  const W w[2] = {{base}, {base + (int64_t)d.HS * d.D}};
-  f32x4 acc[2][NT];
+  const int ns = tiles_of(d.HS, 16 * RT), i = item - nr - nd, j = i / ns, u0 = (i - j * ns) * 16 * RT;
+  W w[2 * RT];
+#pragma unroll
+  for (int r = 0; r < RT; ++r) {
+    const T* base = (const T*)a.ws13 + ((int64_t)j * 2 * d.HS + min(u0 + r * 16 + r16, d.HS - 1)) * d.D;
+    w[2 * r] = W{base};
+    w[2 * r + 1] = W{base + (int64_t)d.HS * d.D};
+  }
+  f32x4 acc[2 * RT][NT];
   zero(acc);
-  dot<W, false, 2, NT>(acc, w, hi, 0, d.D, wave, NW);
-  reduce<2, NT>(acc, lds, [&](int t, const f32x4 (&s)[2]) {
+  dot<W, false, 2 * RT, NT>(acc, w, hi, 0, d.D, wave, NW);
+  reduce<2, 2 * RT, NT>(acc, lds, [&](int r, int t, const f32x4 (&s)[2]) {
     const int m = t * 16 + r16;
     if (m >= d.T) return;
 #pragma unroll
     for (int v = 0; v < 4; ++v) {
-      const int u = u0 + g * 4 + v;
+      const int u = u0 + r * 16 + g * 4 + v;
       if (u < d.HS) put_act(a.hs, (T*)nullptr, ((int64_t)m * d.S + j) * d.HS + u, silu_exact(s[0][v]) * s[1][v]);
     }
   });
@@ -299,41 +314,47 @@ template <> __device__ __forceinline__ WMx Bank<WMx>::row(int64_t r, int K) cons
   return {(const uint8_t*)codes + r * (K / 2), scales + r * mx_scale_bytes(K)};
 }
 
-// Item: 16 hidden units of a chosen expert.
-template <class T, class W, int NT>
-__device__ void gate_up(const FewArgs& a, int i, int u0, const int* list, int n, f32x4* lds) {
+// Item: 16 RT hidden units of a chosen expert.
+template <class T, class W, int RT, int NT>
+__device__ __forceinline__ void gate_up(const FewArgs& a, int i, int u0, const int* list, int n, f32x4* lds) {
   const FewDims& d = a.d;
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, r16 = lane & 15, g = lane >> 4;
   const T* hi[NT];
 #pragma unroll
   for (int t = 0; t < NT; ++t) hi[t] = (const T*)a.z.hi + (int64_t)list[min(t * 16 + r16, n - 1)] * d.L;
   const Bank<W> bank{a.w13, a.w13_scales};
-  const int64_t row = (int64_t)a.active[i] * 2 * d.H + min(u0 + r16, d.H - 1);
-  const W w[2] = {bank.row(row, d.L), bank.row(row + d.H, d.L)};
-  f32x4 acc[2][NT];
+  W w[2 * RT];
+#pragma unroll
+  for (int r = 0; r < RT; ++r) {
+    const int64_t row = (int64_t)a.active[i] * 2 * d.H + min(u0 + r * 16 + r16, d.H - 1);
+    w[2 * r] = bank.row(row, d.L);
+    w[2 * r + 1] = bank.row(row + d.H, d.L);
+  }
+  f32x4 acc[2 * RT][NT];
   zero(acc);
-  dot<W, sizeof(T) == 2, 2, NT>(acc, w, hi, lo_offset<T>(a.z), d.L, wave, NW);
+  dot<W, sizeof(T) == 2, 2 * RT, NT>(acc, w, hi, lo_offset<T>(a.z), d.L, wave, NW);
   const int64_t first = a.first[i];
-  reduce<2, NT>(acc, lds, [&](int t, const f32x4 (&s)[2]) {
+  reduce<2, 2 * RT, NT>(acc, lds, [&](int r, int t, const f32x4 (&s)[2]) {
     const int m = t * 16 + r16;
     if (m >= n) return;
 #pragma unroll
     for (int v = 0; v < 4; ++v) {
-      const int u = u0 + g * 4 + v;
+      const int u = u0 + r * 16 + g * 4 + v;
       if (u < d.H) put_act(a.h, (T*)nullptr, (first + m) * d.H + u, silu_exact(s[0][v]) * s[1][v]);
     }
   });
 }
 
-// Item: 16 rows of the latent width and one of `parts` shares of the chosen
+// Item: 16 RT rows of the latent width and one of `parts` shares of the chosen
 // experts' hidden units.  A wave takes pieces (expert, DOWN_K hidden units) in
 // turn, weighs each piece's sums with the tokens' routing weights and adds
-// them to its own rows in LDS; the waves' rows are added in wave order.
+// them to its own rows in LDS; the waves' rows are added in wave order, and
+// the last of a tile's shares to finish adds the shares in their order.
 constexpr int DOWN_K = 512;
 
-template <class T, class W, int NT>
-__device__ __forceinline__ void down_piece(const FewArgs& a, int i, int k0, int l0, uint64_t mask, float* rows) {
-  const FewDims& d = a.d;
+template <class T, class W, int RT, int NT>
+__device__ __forceinline__ void down_piece(const FewArgs& a, int i, int k0, int l0, uint64_t mask, int m0, float* rows) {
+  const FewDims& d = a.d;  // the expert's tokens m0 .. m0 + 16 NT - 1
   const int lane = threadIdx.x & 63, r16 = lane & 15, g = lane >> 4, n = __popcll(mask);
   const int K = min(DOWN_K, d.H - k0);
   const int64_t first = a.first[i], e = a.active[i];
@@ -342,7 +363,7 @@ __device__ __forceinline__ void down_piece(const FewArgs& a, int i, int k0, int 
   float gate[NT];
 #pragma unroll
   for (int t = 0; t < NT; ++t) {
-    const int m = min(t * 16 + r16, n - 1);
+    const int m = min(m0 + t * 16 + r16, n - 1);
     hi[t] = (const T*)a.h.hi + (first + m) * d.H + k0;
     uint64_t rest = mask;  // the m-th set bit
     for (int s = 0; s < m; ++s) rest &= rest - 1;
@@ -350,80 +371,117 @@ __device__ __forceinline__ void down_piece(const FewArgs& a, int i, int k0, int 
     gate[t] = a.gate[(int64_t)tok[t] * d.X + e];
   }
   const Bank<W> bank{a.w2, a.w2_scales};
-  W w[1] = {bank.row(e * d.L + min(l0 + r16, d.L - 1), d.H)};
-  if constexpr (W::KSTEP == 128) {
-    w[0].p += k0 / 2;
-    w[0].s += k0 / 32;
-  } else {
-    w[0].p += k0;
+  W w[RT];
+#pragma unroll
+  for (int r = 0; r < RT; ++r) {
+    w[r] = bank.row(e * d.L + min(l0 + r * 16 + r16, d.L - 1), d.H);
+    if constexpr (W::KSTEP == 128) {
+      w[r].p += k0 / 2;
+      w[r].s += k0 / 32;
+    } else {
+      w[r].p += k0;
+    }
   }
-  f32x4 acc[1][NT];
+  f32x4 acc[RT][NT];
   zero(acc);
-  dot<W, sizeof(T) == 2, 1, NT>(acc, w, hi, lo_offset<T>(a.h), K, 0, 1);
+  dot<W, sizeof(T) == 2, RT, NT>(acc, w, hi, lo_offset<T>(a.h), K, 0, 1);
 #pragma unroll
   for (int t = 0; t < NT; ++t)
-    if (t * 16 + r16 < n) {
-      f32x4* p = (f32x4*)(rows + tok[t] * 16 + g * 4);
-      f32x4 v = *p;
+    if (m0 + t * 16 + r16 < n) {
 #pragma unroll
-      for (int q = 0; q < 4; ++q) v[q] = fmaf(gate[t], acc[0][t][q], v[q]);
-      *p = v;
+      for (int r = 0; r < RT; ++r) {
+        f32x4* p = (f32x4*)(rows + (tok[t] * RT + r) * 16 + g * 4);
+        f32x4 v = *p;
+#pragma unroll
+        for (int q = 0; q < 4; ++q) v[q] = fmaf(gate[t], acc[r][t][q], v[q]);
+        *p = v;
+      }
     }
 }
 
-template <class T, class W>
-__device__ void down(const FewArgs& a, int part, int l0, float* lds) {  // lds: [NW][T][16]
+template <class T, class W, int RT, int NTMAX>
+__device__ __forceinline__ void down(const FewArgs& a, int part, int tile, float* lds) {  // lds: [NW][T][16 RT]
   const FewDims& d = a.d;
-  const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
-  float* rows = lds + wave * d.T * 16;
-  for (int i = lane; i < d.T * 16; i += 64) rows[i] = 0.f;
+  constexpr int R = 16 * RT;
+  const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63, l0 = tile * R;
+  float* rows = lds + wave * d.T * R;
+  for (int i = lane; i < d.T * R; i += 64) rows[i] = 0.f;
   const int active = a.count[0], chunks = (d.H + DOWN_K - 1) / DOWN_K, pieces = active * chunks;
   for (int p = part * NW + wave; p < pieces; p += a.parts * NW) {
     const int i = p / chunks, k0 = (p - i * chunks) * DOWN_K;
     const uint64_t mask = a.mask[i];
     const int n = __popcll(mask);
-    if (n <= 16) down_piece<T, W, 1>(a, i, k0, l0, mask, rows);
-    else if (n <= 32) down_piece<T, W, 2>(a, i, k0, l0, mask, rows);
-    else down_piece<T, W, 4>(a, i, k0, l0, mask, rows);
+    if (NTMAX == 1 || n <= 16) down_piece<T, W, RT, 1>(a, i, k0, l0, mask, 0, rows);
+    else  // more than 32 tokens read the expert's piece twice
+      for (int m0 = 0; m0 < n; m0 += 32) down_piece<T, W, RT, NTMAX>(a, i, k0, l0, mask, m0, rows);
   }
   __syncthreads();
-  for (int i = threadIdx.x; i < d.T * 16; i += NTHREADS) {
+  const int64_t n = (int64_t)d.T * d.L;
+  for (int i = threadIdx.x; i < d.T * R; i += NTHREADS) {
     float s = lds[i];
-    for (int w = 1; w < NW; ++w) s += lds[w * d.T * 16 + i];
-    const int t = i >> 4, l = l0 + (i & 15);
-    if (l < d.L) a.part[((int64_t)part * d.T + t) * d.L + l] = s;
+    for (int w = 1; w < NW; ++w) s += lds[w * d.T * R + i];
+    const int t = i / R, l = l0 + i % R;
+    if (l >= d.L) continue;
+    if (a.parts == 1) put_act(a.c, (T*)nullptr, (int64_t)t * d.L + l, s);
+    else __hip_atomic_store(&a.part[part * n + (int64_t)t * d.L + l], s, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+  }
+  if (a.parts == 1) return;
+  // The shares of a tile meet: the last workgroup to arrive adds them.  The
+  // shares were stored, and are read, with device scope (through the L2 of the
+  // XCD, which others do not see), so waiting for the stores is all the
+  // release that is needed; a device-wide fence writes back the whole L2,
+  // which took 100 us here.
+  __shared__ int last;
+  vm_wait<0>();
+  __syncthreads();
+  if (threadIdx.x == 0)
+    last = __hip_atomic_fetch_add(&a.arrived[tile], 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) == a.parts - 1;
+  __syncthreads();
+  if (!last) return;
+  for (int i = threadIdx.x; i < d.T * R; i += NTHREADS) {
+    const int t = i / R, l = l0 + i % R;
+    if (l >= d.L) continue;
+    const float* p = a.part + (int64_t)t * d.L + l;
+    float s = __hip_atomic_load(p, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    for (int q = 1; q < a.parts; ++q) s += __hip_atomic_load(p + q * n, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    put_act(a.c, (T*)nullptr, (int64_t)t * d.L + l, s);
   }
 }
 
-// Item: 16 output columns.
-template <class T, int NT>
-__device__ void up(const FewArgs& a, int n0, f32x4* lds) {
+// Item: 16 RT output columns.
+template <class T, int RT, int NT>
+__device__ __forceinline__ void up(const FewArgs& a, int n0, f32x4* lds) {
   const FewDims& d = a.d;
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, r16 = lane & 15, g = lane >> 4;
   using W = typename Weights<T>::type;
-  const int64_t row = min(n0 + r16, d.D - 1);
-  f32x4 acc[1][NT];
+  int64_t row[RT];
+#pragma unroll
+  for (int r = 0; r < RT; ++r) row[r] = min(n0 + r * 16 + r16, d.D - 1);
+  f32x4 acc[RT][NT];
   zero(acc);
   const T* hi[NT];
-  {
-    const W w[1] = {{(const T*)a.w_up + row * d.L}};
+  W w[RT];
 #pragma unroll
-    for (int t = 0; t < NT; ++t) hi[t] = (const T*)a.c.hi + (int64_t)min(t * 16 + r16, d.T - 1) * d.L;
-    dot<W, sizeof(T) == 2, 1, NT>(acc, w, hi, lo_offset<T>(a.c), d.L, wave, NW);
-  }
+  for (int r = 0; r < RT; ++r) w[r] = W{(const T*)a.w_up + row[r] * d.L};
+#pragma unroll
+  for (int t = 0; t < NT; ++t) hi[t] = (const T*)a.c.hi + (int64_t)min(t * 16 + r16, d.T - 1) * d.L;
+  dot<W, sizeof(T) == 2, RT, NT>(acc, w, hi, lo_offset<T>(a.c), d.L, wave, NW);
   for (int j = 0; j < d.S; ++j) {
-    const W w[1] = {{(const T*)a.ws2 + ((int64_t)j * d.D + row) * d.HS}};
+#pragma unroll
+    for (int r = 0; r < RT; ++r) w[r] = W{(const T*)a.ws2 + ((int64_t)j * d.D + row[r]) * d.HS};
 #pragma unroll
     for (int t = 0; t < NT; ++t)
       hi[t] = (const T*)a.hs.hi + ((int64_t)min(t * 16 + r16, d.T - 1) * d.S + j) * d.HS;
-    dot<W, sizeof(T) == 2, 1, NT>(acc, w, hi, lo_offset<T>(a.hs), d.HS, wave, NW);
+    dot<W, sizeof(T) == 2, RT, NT>(acc, w, hi, lo_offset<T>(a.hs), d.HS, wave, NW);
   }
-  reduce<1, NT>(acc, lds, [&](int t, const f32x4 (&s)[1]) {
+  reduce<1, RT, NT>(acc, lds, [&](int r, int t, const f32x4 (&s)[1]) {
     const int m = t * 16 + r16;
     if (m >= d.T) return;
 #pragma unroll
-    for (int v = 0; v < 4; ++v)
-      if (n0 + g * 4 + v < d.D) ((T*)a.out)[(int64_t)m * d.D + n0 + g * 4 + v] = Act<T>::store(s[0][v]);
+    for (int v = 0; v < 4; ++v) {
+      const int n = n0 + r * 16 + g * 4 + v;
+      if (n < d.D) ((T*)a.out)[(int64_t)m * d.D + n] = Act<T>::store(s[0][v]);
+    }
   });
 }
 
@@ -431,29 +489,52 @@ __device__ void up(const FewArgs& a, int n0, f32x4* lds) {
 
 // ------------------------------------------------------------ kernels
 
-template <class T, int NT>
+template <class T, int RT, int NT>
 __global__ void __launch_bounds__(NTHREADS) few_project(FewArgs a) {
-  __shared__ f32x4 lds[NW * 2 * NT * 64];
-  project<T, NT>(a, blockIdx.x, lds);
+  __shared__ f32x4 lds[NW * 2 * RT * NT * 64];
+  project<T, RT, NT>(a, blockIdx.x, lds);
+}
+
+// Largest key of the wave, in every lane: rotations inside each row of 16
+// lanes (DPP row_ror by 8, 4, 2, 1), then the four rows' maxima.
+template <int CTRL>
+__device__ __forceinline__ uint64_t ror_max(uint64_t k) {
+  const uint64_t o = ((uint64_t)(uint32_t)__builtin_amdgcn_update_dpp(0, (int)(k >> 32), CTRL, 0xf, 0xf, false) << 32) |
+                     (uint32_t)__builtin_amdgcn_update_dpp(0, (int)(uint32_t)k, CTRL, 0xf, 0xf, false);
+  return o > k ? o : k;
+}
+__device__ __forceinline__ uint64_t key_at(uint64_t k, int lane) {
+  return ((uint64_t)(uint32_t)__builtin_amdgcn_readlane((int)(k >> 32), lane) << 32) |
+         (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)k, lane);
+}
+__device__ __forceinline__ uint64_t max_key(uint64_t k) {
+  k = ror_max<0x121>(ror_max<0x122>(ror_max<0x124>(ror_max<0x128>(k))));
+  const uint64_t a = key_at(k, 0), b = key_at(k, 16), c = key_at(k, 32), d = key_at(k, 48);
+  const uint64_t ab = a > b ? a : b, cd = c > d ? c : d;
+  return ab > cd ? ab : cd;
 }
 
 // One workgroup: every wave takes tokens in turn, k rounds of a maximum over
-// (logit, lower expert first) keys; then the chosen experts in ascending
-// order with their tokens (a bit each: an expert is chosen once a token).
+// (logit, lower expert first) keys, EPL of them a lane (-0 counts as 0, and a
+// NaN by its bits, so that a token always gets k experts); then the chosen
+// experts in ascending order with their tokens (a bit each: an expert is
+// chosen once a token).  It also clears the counters of the down product.
+template <int EPL>
 __global__ void __launch_bounds__(1024) few_select(FewArgs a) {
   __shared__ unsigned long long mask[2048];
-  __shared__ int scan_n[1024], scan_p[1024];
+  __shared__ int wave_n[16], wave_p[16];
   const FewDims& d = a.d;
   const int tid = threadIdx.x, wave = tid >> 6, lane = tid & 63;
   for (int e = tid; e < d.X; e += 1024) mask[e] = 0;
+  for (int i = tid; i < a.tiles; i += 1024) a.arrived[i] = 0;
   __syncthreads();
   for (int t = wave; t < d.T; t += 16) {
-    uint64_t key[32];
+    uint64_t key[EPL];
 #pragma unroll
-    for (int j = 0; j < 32; ++j) {
+    for (int j = 0; j < EPL; ++j) {
       const int e = lane + 64 * j;
       key[j] = 0;
-      if (64 * j < d.E && e < d.E) {
+      if (e < d.E) {
         uint32_t u = __float_as_uint(a.logits[(int64_t)t * d.E + e]);
         if (u == 0x80000000u) u = 0;
         key[j] = ((uint64_t)((u & 0x80000000u) ? ~u : (u | 0x80000000u)) << 32) | (uint32_t)~(uint32_t)e;
@@ -464,13 +545,8 @@ __global__ void __launch_bounds__(1024) few_select(FewArgs a) {
     for (int r = 0; r < d.k; ++r) {
       uint64_t best = key[0];
 #pragma unroll
-      for (int j = 1; j < 32; ++j)
-        if (64 * j < d.E) best = key[j] > best ? key[j] : best;
-      for (int o = 1; o < 64; o <<= 1) {
-        const uint64_t other = ((uint64_t)(uint32_t)__shfl_xor((int)(best >> 32), o) << 32) |
-                               (uint32_t)__shfl_xor((int)(uint32_t)best, o);
-        best = other > best ? other : best;
-      }
+      for (int j = 1; j < EPL; ++j) best = key[j] > best ? key[j] : best;
+      best = max_key(best);
       const int e = (int)~(uint32_t)best;
       const uint32_t o = (uint32_t)(best >> 32);
       const float v = __uint_as_float((o & 0x80000000u) ? (o & 0x7fffffffu) : ~o);
@@ -480,7 +556,7 @@ __global__ void __launch_bounds__(1024) few_select(FewArgs a) {
         my_e = e;
       }
 #pragma unroll
-      for (int j = 0; j < 32; ++j)
+      for (int j = 0; j < EPL; ++j)
         if (lane + 64 * j == e) key[j] = 0;
     }
     const float ex = lane < d.k ? expf(my_v - v0) : 0.f;
@@ -497,21 +573,28 @@ __global__ void __launch_bounds__(1024) few_select(FewArgs a) {
     }
   }
   __syncthreads();
-  // chosen experts and their pair rows: two experts a thread, scans over the threads
+  // chosen experts and their pair rows: two experts a thread, scans inside the waves and over them
   const int e0 = tid * 2;
   const uint64_t m0 = e0 < d.X ? mask[e0] : 0, m1 = e0 + 1 < d.X ? mask[e0 + 1] : 0;
   const int n = (m0 != 0) + (m1 != 0), p = __popcll(m0) + __popcll(m1);
-  scan_n[tid] = n;
-  scan_p[tid] = p;
-  __syncthreads();
-  for (int o = 1; o < 1024; o <<= 1) {
-    const int an = tid >= o ? scan_n[tid - o] : 0, ap = tid >= o ? scan_p[tid - o] : 0;
-    __syncthreads();
-    scan_n[tid] += an;
-    scan_p[tid] += ap;
-    __syncthreads();
+  int sn = n, sp = p;
+  for (int o = 1; o < 64; o <<= 1) {
+    const int an = __shfl_up(sn, o), ap = __shfl_up(sp, o);
+    if (lane >= o) {
+      sn += an;
+      sp += ap;
+    }
   }
-  int at = scan_n[tid] - n, row = scan_p[tid] - p;
+  if (lane == 63) {
+    wave_n[wave] = sn;
+    wave_p[wave] = sp;
+  }
+  __syncthreads();
+  int at = sn - n, row = sp - p;
+  for (int w = 0; w < wave; ++w) {
+    at += wave_n[w];
+    row += wave_p[w];
+  }
   if (m0) {
     a.active[at] = e0;
     a.mask[at] = m0;
@@ -523,44 +606,35 @@ __global__ void __launch_bounds__(1024) few_select(FewArgs a) {
     a.active[at] = e0 + 1;
     a.mask[at] = m1;
     a.first[at] = row;
+    ++at;
   }
-  if (tid == 1023) a.count[0] = scan_n[1023];
+  if (tid == 1023) a.count[0] = at;
 }
 
-template <class T, class W, int NTMAX>
+template <class T, class W, int RT, int NTMAX>
 __global__ void __launch_bounds__(NTHREADS) few_gate_up(FewArgs a) {
-  __shared__ f32x4 lds[NW * 2 * NTMAX * 64];
+  __shared__ f32x4 lds[NW * 2 * RT * NTMAX * 64];
   __shared__ int list[64];
-  const int tiles = (a.d.H + 15) / 16;
-  const int i = blockIdx.x / tiles, u0 = (blockIdx.x - i * tiles) * 16;
+  const int tiles = tiles_of(a.d.H, 16 * RT);
+  const int i = blockIdx.x / tiles, u0 = (blockIdx.x - i * tiles) * 16 * RT;
   if (i >= a.count[0]) return;
   const int n = token_list(a.mask[i], list);
-  if (NTMAX == 1 || n <= 16) gate_up<T, W, 1>(a, i, u0, list, n, lds);
-  else if (NTMAX == 2 || n <= 32) gate_up<T, W, (NTMAX >= 2 ? 2 : 1)>(a, i, u0, list, n, lds);
-  else gate_up<T, W, NTMAX>(a, i, u0, list, n, lds);
+  if (NTMAX == 1 || n <= 16) gate_up<T, W, RT, 1>(a, i, u0, list, n, lds);
+  else if (NTMAX == 2 || n <= 32) gate_up<T, W, RT, (NTMAX >= 2 ? 2 : 1)>(a, i, u0, list, n, lds);
+  else gate_up<T, W, RT, NTMAX>(a, i, u0, list, n, lds);
 }
 
-template <class T, class W>
+template <class T, class W, int RT, int NTMAX>
 __global__ void __launch_bounds__(NTHREADS) few_down(FewArgs a) {
   extern __shared__ float rows[];
-  const int tiles = (a.d.L + 15) / 16;
-  const int part = blockIdx.x / tiles;
-  down<T, W>(a, part, (blockIdx.x - part * tiles) * 16, rows);
+  const int part = blockIdx.x / a.tiles;
+  down<T, W, RT, NTMAX>(a, part, blockIdx.x - part * a.tiles, rows);
 }
 
-template <class T>
-__global__ void __launch_bounds__(256) few_sum(FewArgs a) {
-  const int64_t n = (int64_t)a.d.T * a.d.L, i = (int64_t)blockIdx.x * 256 + threadIdx.x;
-  if (i >= n) return;
-  float s = a.part[i];
-  for (int p = 1; p < a.parts; ++p) s += a.part[p * n + i];
-  put_act(a.c, (T*)nullptr, i, s);
-}
-
-template <class T, int NT>
+template <class T, int RT, int NT>
 __global__ void __launch_bounds__(NTHREADS) few_up(FewArgs a) {
-  __shared__ f32x4 lds[NW * NT * 64];
-  up<T, NT>(a, blockIdx.x * 16, lds);
+  __shared__ f32x4 lds[NW * RT * NT * 64];
+  up<T, RT, NT>(a, blockIdx.x * 16 * RT, lds);
 }
 
 // ------------------------------------------------------------ host
@@ -588,14 +662,19 @@ FewWs few_layout(const FewDims& d) {
   w.h_lo = take((size_t)d.T * d.k * d.H * second);
   w.c = take((size_t)d.T * d.L * es);
   w.c_lo = take((size_t)d.T * d.L * second);
-  // shares of the down product: as many as give every CU two workgroups, and
-  // every wave of a share something to do
-  const int64_t tiles = (d.L + 15) / 16, most = d.X < d.T * d.k ? d.X : d.T * d.k;
-  const int64_t pieces = most * ((d.H + DOWN_K - 1) / DOWN_K);
-  int64_t parts = (2 * FEW_CUS + tiles - 1) / tiles;
-  if (parts > (pieces + NW - 1) / NW) parts = (pieces + NW - 1) / NW;
+  // The down product: row tiles as high as the tokens' rows in LDS allow (the
+  // tokens' hidden values are read once a tile), and shares as many as give
+  // every CU two workgroups and every wave of a share something to do.
+  const int64_t most = d.X < d.T * d.k ? d.X : d.T * d.k;
+  const int64_t pieces = most * ((d.H + DOWN_K - 1) / DOWN_K), most_parts = (pieces + NW - 1) / NW;
+  w.down_rt = d.T <= 16 ? 4 : 2;
+  while (w.down_rt > 1 && tiles_of(d.L, 16 * w.down_rt) * most_parts < 2 * FEW_CUS) w.down_rt /= 2;
+  w.tiles = tiles_of(d.L, 16 * w.down_rt);
+  int64_t parts = (2 * FEW_CUS + w.tiles - 1) / w.tiles;
+  if (parts > most_parts) parts = most_parts;
   w.parts = parts < 1 ? 1 : (int)parts;
-  w.part = take((size_t)w.parts * d.T * d.L * 4);
+  w.part = take((size_t)(w.parts > 1 ? w.parts : 0) * d.T * d.L * 4);
+  w.arrived = take((size_t)w.tiles * 4);
   w.total = off;
   return w;
 }
@@ -614,41 +693,77 @@ hipError_t few_dispatch(const FewDims& d, F f) {
   return hipGetLastError();
 }
 
+// Row tiles of the products with all tokens: two where the tokens' own rows
+// are much of the traffic, one where there are few tokens (more workgroups) or
+// more than 32 (the waves' sums would not fit beside a second workgroup's).
+template <class F>
+void few_row_tiles(const FewDims& d, F f) {
+  if (d.T > 8 && d.T <= 32) f(std::integral_constant<int, 2>());
+  else f(std::integral_constant<int, 1>());
+}
+
 hipError_t launch_few_project(const FewArgs& a, hipStream_t st) {
   return few_dispatch(a.d, [&](auto t, auto, auto nt) {
-    launch((few_project<decltype(t), decltype(nt)::value>), dim3((unsigned)project_items(a.d)), dim3(NTHREADS), 0, st, a);
+    few_row_tiles(a.d, [&](auto rt) {
+      constexpr int RT = decltype(rt)::value, NT = decltype(nt)::value;
+      if constexpr (RT * NT <= 4)
+        launch((few_project<decltype(t), RT, NT>), dim3((unsigned)project_items<RT>(a.d)), dim3(NTHREADS), 0, st, a);
+    });
   });
 }
 
 hipError_t launch_few_select(const FewArgs& a, hipStream_t st) {
-  launch(few_select, dim3(1), dim3(1024), 0, st, a);
+  const int epl = (a.d.E + 63) / 64;
+#define SELECT(N) launch(few_select<N>, dim3(1), dim3(1024), 0, st, a)
+  if (epl <= 1) SELECT(1);
+  else if (epl <= 2) SELECT(2);
+  else if (epl <= 4) SELECT(4);
+  else if (epl <= 8) SELECT(8);
+  else if (epl <= 16) SELECT(16);
+  else SELECT(32);
+#undef SELECT
   return hipGetLastError();
 }
 
 hipError_t launch_few_gate_up(const FewArgs& a, hipStream_t st) {
   const unsigned most = (unsigned)(a.d.X < a.d.T * a.d.k ? a.d.X : a.d.T * a.d.k);
   return few_dispatch(a.d, [&](auto t, auto w, auto nt) {
-    launch((few_gate_up<decltype(t), decltype(w), decltype(nt)::value>), dim3(most * ((a.d.H + 15) / 16)), dim3(NTHREADS),
-           0, st, a);
+    constexpr int NT = decltype(nt)::value;
+    auto go = [&](auto rt) {
+      constexpr int RT = decltype(rt)::value;
+      launch((few_gate_up<decltype(t), decltype(w), RT, NT>), dim3(most * tiles_of(a.d.H, 16 * RT)), dim3(NTHREADS), 0, st, a);
+    };
+    // four times the hidden units a workgroup where that still gives every CU four of them
+    if constexpr (NT <= 1) {
+      if (most * tiles_of(a.d.H, 64) >= 4 * FEW_CUS) return go(std::integral_constant<int, 4>());
+    }
+    go(std::integral_constant<int, 1>());
   });
 }
 
 hipError_t launch_few_down(const FewArgs& a, hipStream_t st) {
-  return few_dispatch(a.d, [&](auto t, auto w, auto) {
-    launch((few_down<decltype(t), decltype(w)>), dim3((unsigned)(a.parts * ((a.d.L + 15) / 16))), dim3(NTHREADS),
-           (uint32_t)(NW * a.d.T * 16 * 4), st, a);
-  });
-}
-
-hipError_t launch_few_sum(const FewArgs& a, hipStream_t st) {
-  return few_dispatch(a.d, [&](auto t, auto, auto) {
-    launch(few_sum<decltype(t)>, dim3((unsigned)(((int64_t)a.d.T * a.d.L + 255) / 256)), dim3(256), 0, st, a);
+  return few_dispatch(a.d, [&](auto t, auto w, auto nt) {
+    constexpr int NT = decltype(nt)::value > 2 ? 2 : decltype(nt)::value;
+    auto go = [&](auto rt) {
+      constexpr int RT = decltype(rt)::value;
+      launch((few_down<decltype(t), decltype(w), RT, NT>), dim3((unsigned)(a.parts * a.tiles)), dim3(NTHREADS),
+             (uint32_t)(NW * a.d.T * 16 * RT * 4), st, a);
+    };
+    if constexpr (NT == 1) {
+      if (a.down_rt == 4) return go(std::integral_constant<int, 4>());
+    }
+    if (a.down_rt == 2) go(std::integral_constant<int, 2>());
+    else go(std::integral_constant<int, 1>());
   });
 }
 
 hipError_t launch_few_up(const FewArgs& a, hipStream_t st) {
   return few_dispatch(a.d, [&](auto t, auto, auto nt) {
-    launch((few_up<decltype(t), decltype(nt)::value>), dim3((unsigned)((a.d.D + 15) / 16)), dim3(NTHREADS), 0, st, a);
+    few_row_tiles(a.d, [&](auto rt) {
+      constexpr int RT = decltype(rt)::value, NT = decltype(nt)::value;
+      if constexpr (RT * NT <= 4)
+        launch((few_up<decltype(t), RT, NT>), dim3((unsigned)tiles_of(a.d.D, 16 * RT)), dim3(NTHREADS), 0, st, a);
+    });
   });
 }
 

@@ -45,8 +45,9 @@ def test_dims_that_only_this_call_takes():
     assert B.few_workspace_size(_dims(n_experts=384, top_k=8)) > 0                # any number of local experts
     assert B.few_workspace_size(_dims(waves=7, send_den=0)) > 0                  # fields it does not look at
     assert B.few_workspace_size(_dims(act_dtype=1, d_model=33, latent=7, expert_hidden=5, shared_hidden=3)) > 0
-    sizes = [B.few_workspace_size(_dims(tokens=t)) for t in range(65)]
-    assert sizes == sorted(sizes)                                                # one for 64 tokens serves fewer
+    for kw in ({}, dict(latent=2048, expert_hidden=1536, n_experts=384, top_k=8), dict(latent=64, expert_hidden=6144)):
+        sizes = [B.few_workspace_size(_dims(tokens=t, **kw)) for t in range(65)]
+        assert sizes == sorted(sizes)                                            # one for 64 tokens serves fewer
 
 
 @pytest.mark.parametrize("kw,code,word", [
