@@ -282,7 +282,7 @@ int moe_few_tokens(const moe_dims* dims, const void* x, const void* w_router, co
   a.parts = w.parts; a.tiles = w.tiles; a.down_rt = w.down_rt;
   hipStream_t st = (hipStream_t)stream;
   LAUNCH("few_project", launch_few_project(a, st), "moe_few_tokens project");
-  LAUNCH("few_select", launch_few_select(a, st), "moe_few_tokens select");
+  LAUNCH("few_select_shared", launch_few_select(a, st), "moe_few_tokens select");
   LAUNCH("few_gate_up", launch_few_gate_up(a, st), "moe_few_tokens gate/up");
   LAUNCH("few_down", launch_few_down(a, st), "moe_few_tokens down");
   LAUNCH("few_up", launch_few_up(a, st), "moe_few_tokens up");

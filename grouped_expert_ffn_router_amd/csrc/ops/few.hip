@@ -135,42 +135,61 @@ __device__ __forceinline__ void dot(f32x4 (&acc)[RT][NT], const W (&w)[RT], cons
   }
 }
 
-// fp32: any K and any alignment, 4 values a lane and step.
+// fp32: any K and any alignment, 4 values a lane and step, U steps at a time.
 template <class W, bool LO, int RT, int NT>
 __device__ __forceinline__ void dot(f32x4 (&acc)[RT][NT], const W (&w)[RT], const float* const (&hi)[NT], int64_t, int K,
                                     int part, int parts) {
+  constexpr int U = 4;
   const int g = lane_id() >> 4;
-  const int steps = (K + 15) / 16;
+  const int steps = (K + 15) / 16, full = K / 16;
   uintptr_t at = 0;
 #pragma unroll
   for (int r = 0; r < RT; ++r) at |= (uintptr_t)w[r].p;
 #pragma unroll
   for (int t = 0; t < NT; ++t) at |= (uintptr_t)hi[t];
   const bool vec = __all((at & 15) == 0);
-  for (int s = part; s < steps; s += parts) {
-    const int k = s * 16 + g * 4;
-    float a[NT][4], b[RT][4];
-    if (vec && s * 16 + 16 <= K) {
-#pragma unroll
-      for (int r = 0; r < RT; ++r) *(float4*)b[r] = *(const float4*)(w[r].p + k);
-#pragma unroll
-      for (int t = 0; t < NT; ++t) *(float4*)a[t] = *(const float4*)(hi[t] + k);
-    } else {
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-#pragma unroll
-        for (int r = 0; r < RT; ++r) b[r][i] = k + i < K ? w[r].p[k + i] : 0.f;
-#pragma unroll
-        for (int t = 0; t < NT; ++t) a[t][i] = k + i < K ? hi[t][k + i] : 0.f;
-      }
-    }
+  auto mma = [&](const float (&b)[RT][4], const float (&x)[NT][4]) {
 #pragma unroll
     for (int i = 0; i < 4; ++i)
 #pragma unroll
       for (int r = 0; r < RT; ++r)
 #pragma unroll
         for (int t = 0; t < NT; ++t)
-          acc[r][t] = __builtin_amdgcn_mfma_f32_16x16x4f32(b[r][i], a[t][i], acc[r][t], 0, 0, 0);
+          acc[r][t] = __builtin_amdgcn_mfma_f32_16x16x4f32(b[r][i], x[t][i], acc[r][t], 0, 0, 0);
+  };
+  int s = part;
+  if (vec)
+    for (; s + (U - 1) * parts < full; s += U * parts) {
+      float b[U][RT][4], x[U][NT][4];
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const int k = (s + u * parts) * 16 + g * 4;
+#pragma unroll
+        for (int r = 0; r < RT; ++r) *(float4*)b[u][r] = *(const float4*)(w[r].p + k);
+#pragma unroll
+        for (int t = 0; t < NT; ++t) *(float4*)x[u][t] = *(const float4*)(hi[t] + k);
+      }
+#pragma unroll
+      for (int u = 0; u < U; ++u) mma(b[u], x[u]);
+    }
+  for (; s < steps; s += parts) {
+    const int k = s * 16 + g * 4;
+    float b[RT][4], x[NT][4];
+    if (vec && s < full) {
+#pragma unroll
+      for (int r = 0; r < RT; ++r) *(float4*)b[r] = *(const float4*)(w[r].p + k);
+#pragma unroll
+      for (int t = 0; t < NT; ++t) *(float4*)x[t] = *(const float4*)(hi[t] + k);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+#pragma unroll
+        for (int r = 0; r < RT; ++r) b[r][i] = k + i < K ? w[r].p[k + i] : 0.f;
+#pragma unroll
+        for (int t = 0; t < NT; ++t) x[t][i] = k + i < K ? hi[t][k + i] : 0.f;
+      }
+    }
+    mma(b, x);
   }
 }
 
@@ -190,29 +209,44 @@ __device__ __forceinline__ int64_t lo_offset(const FewAct& a) { return (const T*
 
 // ------------------------------------------------------------ phases
 
-// Sums of the waves' accumulators, in wave order, G row tiles at a time (a
-// gate tile and its up tile together): f(group, t, sums) gets those of token
-// tile t, each 4 weight rows 4 g .. of token r16.
-template <int G, int RT, int NT, class F>
+// Sums of the accumulators of the KS waves (all of a workgroup, or 1) that
+// share rows, in wave order, G row tiles at a time (a gate tile and its up tile
+// together): f(group, t, sums) gets those of token tile t, each 4 weight rows
+// 4 g .. of token r16.
+template <int G, int KS, int RT, int NT, class F>
 __device__ __forceinline__ void reduce(f32x4 (&acc)[RT][NT], f32x4* lds, F f) {
-  static_assert(RT % G == 0, "whole groups");
+  static_assert(RT % G == 0 && (KS == 1 || KS == NW), "whole groups");
   const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
-  __syncthreads();
+  if constexpr (KS == 1) {
 #pragma unroll
-  for (int r = 0; r < RT; ++r)
+    for (int grp = 0; grp < RT / G; ++grp)
 #pragma unroll
-    for (int t = 0; t < NT; ++t) lds[((wave * RT + r) * NT + t) * 64 + lane] = acc[r][t];
-  __syncthreads();
-  for (int p = wave; p < RT / G * NT; p += NW) {
-    const int grp = p / NT, t = p % NT;
-    f32x4 s[G];
+      for (int t = 0; t < NT; ++t) {
+        f32x4 s[G];
 #pragma unroll
-    for (int i = 0; i < G; ++i) {
-      s[i] = lds[((grp * G + i) * NT + t) * 64 + lane];
+        for (int i = 0; i < G; ++i) s[i] = acc[grp * G + i][t];
+        f(grp, t, s);
+      }
+    return;
+  }
 #pragma unroll
-      for (int w = 1; w < NW; ++w) s[i] += lds[((w * RT + grp * G + i) * NT + t) * 64 + lane];
+  for (int grp = 0; grp < RT / G; ++grp) {  // a group at a time: NW * G * NT KB of LDS
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < G; ++i)
+#pragma unroll
+      for (int t = 0; t < NT; ++t) lds[((wave * G + i) * NT + t) * 64 + lane] = acc[grp * G + i][t];
+    __syncthreads();
+    if (wave < NT) {
+      f32x4 s[G];
+#pragma unroll
+      for (int i = 0; i < G; ++i) {
+        s[i] = lds[(i * NT + wave) * 64 + lane];
+#pragma unroll
+        for (int w = 1; w < NW; ++w) s[i] += lds[((w * G + i) * NT + wave) * 64 + lane];
+      }
+      f(grp, wave, s);
     }
-    f(grp, t, s);
   }
 }
 
@@ -227,15 +261,10 @@ __device__ __forceinline__ void zero(f32x4 (&acc)[RT][NT]) {
     for (int t = 0; t < NT; ++t) acc[r][t] = f32x4{0.f, 0.f, 0.f, 0.f};
 }
 
-// Items: 16 RT router rows, then 16 RT rows of W_down, then 16 RT hidden units
-// of a shared expert (their gate and up rows).
 __host__ __device__ __forceinline__ int tiles_of(int n, int rows) { return (n + rows - 1) / rows; }
-template <int RT>
-__host__ __device__ __forceinline__ int project_items(const FewDims& d) {
-  return tiles_of(d.E, 16 * RT) + tiles_of(d.L, 16 * RT) + d.S * tiles_of(d.HS, 16 * RT);
-}
 
-template <class T, int RT, int NT>
+// Items: 16 router rows, then 16 rows of W_down.
+template <class T, int NT>
 __device__ __forceinline__ void project(const FewArgs& a, int item, f32x4* lds) {
   const FewDims& d = a.d;
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, r16 = lane & 15, g = lane >> 4;
@@ -243,52 +272,52 @@ __device__ __forceinline__ void project(const FewArgs& a, int item, f32x4* lds) 
   const T* hi[NT];
 #pragma unroll
   for (int t = 0; t < NT; ++t) hi[t] = (const T*)a.x + (int64_t)min(t * 16 + r16, d.T - 1) * d.D;
-  const int nr = tiles_of(d.E, 16 * RT), nd = tiles_of(d.L, 16 * RT);
-  if (item < nr + nd) {
-    const bool router = item < nr;
-    const int n0 = (router ? item : item - nr) * 16 * RT, N = router ? d.E : d.L;
-    W w[RT];
-#pragma unroll
-    for (int r = 0; r < RT; ++r)
-      w[r] = W{(const T*)(router ? a.w_router : a.w_down) + (int64_t)min(n0 + r * 16 + r16, N - 1) * d.D};
-    f32x4 acc[RT][NT];
-    zero(acc);
-    dot<W, false, RT, NT>(acc, w, hi, 0, d.D, wave, NW);
-    reduce<1, RT, NT>(acc, lds, [&](int r, int t, const f32x4 (&s)[1]) {
-      const int m = t * 16 + r16;
-      if (m >= d.T) return;
-#pragma unroll
-      for (int v = 0; v < 4; ++v) {
-        const int n = n0 + r * 16 + g * 4 + v;
-        if (n >= N) break;
-        if (router) {
-          float b = 0.f;
-          if (a.bias) b = a.bias[(int64_t)(a.bias_row_tokens ? m / a.bias_row_tokens : 0) * d.E + n];
-          a.logits[(int64_t)m * d.E + n] = s[0][v] + b;
-        } else {
-          put_act(a.z, (T*)nullptr, (int64_t)m * d.L + n, s[0][v]);
-        }
-      }
-    });
-    return;
-  }
-  const int ns = tiles_of(d.HS, 16 * RT), i = item - nr - nd, j = i / ns, u0 = (i - j * ns) * 16 * RT;
-  W w[2 * RT];
-#pragma unroll
-  for (int r = 0; r < RT; ++r) {
-    const T* base = (const T*)a.ws13 + ((int64_t)j * 2 * d.HS + min(u0 + r * 16 + r16, d.HS - 1)) * d.D;
-    w[2 * r] = W{base};
-    w[2 * r + 1] = W{base + (int64_t)d.HS * d.D};
-  }
-  f32x4 acc[2 * RT][NT];
+  const int nr = tiles_of(d.E, 16);
+  const bool router = item < nr;
+  const int n0 = (router ? item : item - nr) * 16, N = router ? d.E : d.L;
+  const W w[1] = {{(const T*)(router ? a.w_router : a.w_down) + (int64_t)min(n0 + r16, N - 1) * d.D}};
+  f32x4 acc[1][NT];
   zero(acc);
-  dot<W, false, 2 * RT, NT>(acc, w, hi, 0, d.D, wave, NW);
-  reduce<2, 2 * RT, NT>(acc, lds, [&](int r, int t, const f32x4 (&s)[2]) {
+  dot<W, false, 1, NT>(acc, w, hi, 0, d.D, wave, NW);
+  reduce<1, NW, 1, NT>(acc, lds, [&](int, int t, const f32x4 (&s)[1]) {
     const int m = t * 16 + r16;
     if (m >= d.T) return;
 #pragma unroll
     for (int v = 0; v < 4; ++v) {
-      const int u = u0 + r * 16 + g * 4 + v;
+      const int n = n0 + g * 4 + v;
+      if (n >= N) break;
+      if (router) {
+        float b = 0.f;
+        if (a.bias) b = a.bias[(int64_t)(a.bias_row_tokens ? m / a.bias_row_tokens : 0) * d.E + n];
+        a.logits[(int64_t)m * d.E + n] = s[0][v] + b;
+      } else {
+        put_act(a.z, (T*)nullptr, (int64_t)m * d.L + n, s[0][v]);
+      }
+    }
+  });
+}
+
+// Item: 16 hidden units of a shared expert.
+template <class T, int NT>
+__device__ __forceinline__ void shared_expert(const FewArgs& a, int item, f32x4* lds) {
+  const FewDims& d = a.d;
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, r16 = lane & 15, g = lane >> 4;
+  using W = typename Weights<T>::type;
+  const T* hi[NT];
+#pragma unroll
+  for (int t = 0; t < NT; ++t) hi[t] = (const T*)a.x + (int64_t)min(t * 16 + r16, d.T - 1) * d.D;
+  const int ns = tiles_of(d.HS, 16), j = item / ns, u0 = (item - j * ns) * 16;
+  const T* base = (const T*)a.ws13 + ((int64_t)j * 2 * d.HS + min(u0 + r16, d.HS - 1)) * d.D;
+  const W w[2] = {{base}, {base + (int64_t)d.HS * d.D}};
+  f32x4 acc[2][NT];
+  zero(acc);
+  dot<W, false, 2, NT>(acc, w, hi, 0, d.D, wave, NW);
+  reduce<2, NW, 2, NT>(acc, lds, [&](int, int t, const f32x4 (&s)[2]) {
+    const int m = t * 16 + r16;
+    if (m >= d.T) return;
+#pragma unroll
+    for (int v = 0; v < 4; ++v) {
+      const int u = u0 + g * 4 + v;
       if (u < d.HS) put_act(a.hs, (T*)nullptr, ((int64_t)m * d.S + j) * d.HS + u, silu_exact(s[0][v]) * s[1][v]);
     }
   });
@@ -314,32 +343,28 @@ template <> __device__ __forceinline__ WMx Bank<WMx>::row(int64_t r, int K) cons
   return {(const uint8_t*)codes + r * (K / 2), scales + r * mx_scale_bytes(K)};
 }
 
-// Item: 16 RT hidden units of a chosen expert.
-template <class T, class W, int RT, int NT>
-__device__ __forceinline__ void gate_up(const FewArgs& a, int i, int u0, const int* list, int n, f32x4* lds) {
+// 16 hidden units of a chosen expert for its tokens m0 .. m0 + 16 NT - 1, by
+// one wave (KS = 1) or with K shared by the waves of a workgroup (KS = NW).
+template <class T, class W, int KS, int NT>
+__device__ __forceinline__ void gate_up(const FewArgs& a, int i, int u0, const int* list, int m0, int n, f32x4* lds) {
   const FewDims& d = a.d;
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, r16 = lane & 15, g = lane >> 4;
   const T* hi[NT];
 #pragma unroll
-  for (int t = 0; t < NT; ++t) hi[t] = (const T*)a.z.hi + (int64_t)list[min(t * 16 + r16, n - 1)] * d.L;
+  for (int t = 0; t < NT; ++t) hi[t] = (const T*)a.z.hi + (int64_t)list[min(m0 + t * 16 + r16, n - 1)] * d.L;
   const Bank<W> bank{a.w13, a.w13_scales};
-  W w[2 * RT];
-#pragma unroll
-  for (int r = 0; r < RT; ++r) {
-    const int64_t row = (int64_t)a.active[i] * 2 * d.H + min(u0 + r * 16 + r16, d.H - 1);
-    w[2 * r] = bank.row(row, d.L);
-    w[2 * r + 1] = bank.row(row + d.H, d.L);
-  }
-  f32x4 acc[2 * RT][NT];
+  const int64_t row = (int64_t)a.active[i] * 2 * d.H + min(u0 + r16, d.H - 1);
+  const W w[2] = {bank.row(row, d.L), bank.row(row + d.H, d.L)};
+  f32x4 acc[2][NT];
   zero(acc);
-  dot<W, sizeof(T) == 2, 2 * RT, NT>(acc, w, hi, lo_offset<T>(a.z), d.L, wave, NW);
+  dot<W, sizeof(T) == 2, 2, NT>(acc, w, hi, lo_offset<T>(a.z), d.L, KS == 1 ? 0 : wave, KS);
   const int64_t first = a.first[i];
-  reduce<2, 2 * RT, NT>(acc, lds, [&](int r, int t, const f32x4 (&s)[2]) {
-    const int m = t * 16 + r16;
+  reduce<2, KS, 2, NT>(acc, lds, [&](int, int t, const f32x4 (&s)[2]) {
+    const int m = m0 + t * 16 + r16;
     if (m >= n) return;
 #pragma unroll
     for (int v = 0; v < 4; ++v) {
-      const int u = u0 + r * 16 + g * 4 + v;
+      const int u = u0 + g * 4 + v;
       if (u < d.H) put_act(a.h, (T*)nullptr, (first + m) * d.H + u, silu_exact(s[0][v]) * s[1][v]);
     }
   });
@@ -350,13 +375,15 @@ __device__ __forceinline__ void gate_up(const FewArgs& a, int i, int u0, const i
 // turn, weighs each piece's sums with the tokens' routing weights and adds
 // them to its own rows in LDS; the waves' rows are added in wave order, and
 // the last of a tile's shares to finish adds the shares in their order.
-constexpr int DOWN_K = 512;
+constexpr int DOWN_K_ACT = 256, DOWN_K_MX = 512;
+template <class W>
+constexpr int DOWN_K = W::KSTEP == 128 ? DOWN_K_MX : DOWN_K_ACT;
 
 template <class T, class W, int RT, int NT>
 __device__ __forceinline__ void down_piece(const FewArgs& a, int i, int k0, int l0, uint64_t mask, int m0, float* rows) {
   const FewDims& d = a.d;  // the expert's tokens m0 .. m0 + 16 NT - 1
   const int lane = threadIdx.x & 63, r16 = lane & 15, g = lane >> 4, n = __popcll(mask);
-  const int K = min(DOWN_K, d.H - k0);
+  const int K = min(DOWN_K<W>, d.H - k0);
   const int64_t first = a.first[i], e = a.active[i];
   const T* hi[NT];
   int tok[NT];
@@ -406,9 +433,9 @@ __device__ __forceinline__ void down(const FewArgs& a, int part, int tile, float
   const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63, l0 = tile * R;
   float* rows = lds + wave * d.T * R;
   for (int i = lane; i < d.T * R; i += 64) rows[i] = 0.f;
-  const int active = a.count[0], chunks = (d.H + DOWN_K - 1) / DOWN_K, pieces = active * chunks;
+  const int active = a.count[0], chunks = tiles_of(d.H, DOWN_K<W>), pieces = active * chunks;
   for (int p = part * NW + wave; p < pieces; p += a.parts * NW) {
-    const int i = p / chunks, k0 = (p - i * chunks) * DOWN_K;
+    const int i = p / chunks, k0 = (p - i * chunks) * DOWN_K<W>;
     const uint64_t mask = a.mask[i];
     const int n = __popcll(mask);
     if (NTMAX == 1 || n <= 16) down_piece<T, W, RT, 1>(a, i, k0, l0, mask, 0, rows);
@@ -474,7 +501,7 @@ __device__ __forceinline__ void up(const FewArgs& a, int n0, f32x4* lds) {
       hi[t] = (const T*)a.hs.hi + ((int64_t)min(t * 16 + r16, d.T - 1) * d.S + j) * d.HS;
     dot<W, sizeof(T) == 2, RT, NT>(acc, w, hi, lo_offset<T>(a.hs), d.HS, wave, NW);
   }
-  reduce<1, RT, NT>(acc, lds, [&](int r, int t, const f32x4 (&s)[1]) {
+  reduce<1, NW, RT, NT>(acc, lds, [&](int r, int t, const f32x4 (&s)[1]) {
     const int m = t * 16 + r16;
     if (m >= d.T) return;
 #pragma unroll
@@ -489,10 +516,10 @@ __device__ __forceinline__ void up(const FewArgs& a, int n0, f32x4* lds) {
 
 // ------------------------------------------------------------ kernels
 
-template <class T, int RT, int NT>
+template <class T, int NT>
 __global__ void __launch_bounds__(NTHREADS) few_project(FewArgs a) {
-  __shared__ f32x4 lds[NW * 2 * RT * NT * 64];
-  project<T, RT, NT>(a, blockIdx.x, lds);
+  __shared__ f32x4 lds[NW * NT * 64];
+  project<T, NT>(a, blockIdx.x, lds);
 }
 
 // Largest key of the wave, in every lane: rotations inside each row of 16
@@ -519,16 +546,20 @@ __device__ __forceinline__ uint64_t max_key(uint64_t k) {
 // NaN by its bits, so that a token always gets k experts); then the chosen
 // experts in ascending order with their tokens (a bit each: an expert is
 // chosen once a token).  It also clears the counters of the down product.
+struct SelectLds {
+  unsigned long long mask[2048];
+  int wave_n[NW], wave_p[NW];
+};
+
 template <int EPL>
-__global__ void __launch_bounds__(1024) few_select(FewArgs a) {
-  __shared__ unsigned long long mask[2048];
-  __shared__ int wave_n[16], wave_p[16];
+__device__ __forceinline__ void select(const FewArgs& a, SelectLds& lds) {
+  auto& mask = lds.mask;
   const FewDims& d = a.d;
   const int tid = threadIdx.x, wave = tid >> 6, lane = tid & 63;
-  for (int e = tid; e < d.X; e += 1024) mask[e] = 0;
-  for (int i = tid; i < a.tiles; i += 1024) a.arrived[i] = 0;
+  for (int e = tid; e < d.X; e += NTHREADS) mask[e] = 0;
+  for (int i = tid; i < a.tiles; i += NTHREADS) a.arrived[i] = 0;
   __syncthreads();
-  for (int t = wave; t < d.T; t += 16) {
+  for (int t = wave; t < d.T; t += NW) {
     uint64_t key[EPL];
 #pragma unroll
     for (int j = 0; j < EPL; ++j) {
@@ -573,10 +604,16 @@ __global__ void __launch_bounds__(1024) few_select(FewArgs a) {
     }
   }
   __syncthreads();
-  // chosen experts and their pair rows: two experts a thread, scans inside the waves and over them
-  const int e0 = tid * 2;
-  const uint64_t m0 = e0 < d.X ? mask[e0] : 0, m1 = e0 + 1 < d.X ? mask[e0 + 1] : 0;
-  const int n = (m0 != 0) + (m1 != 0), p = __popcll(m0) + __popcll(m1);
+  // chosen experts and their pair rows: four experts a thread, scans inside the waves and over them
+  constexpr int PER = 2048 / NTHREADS;
+  int n = 0, p = 0;
+#pragma unroll
+  for (int j = 0; j < PER; ++j) {
+    const int e = tid * PER + j;
+    const uint64_t m = e < d.X ? mask[e] : 0;
+    n += m != 0;
+    p += __popcll(m);
+  }
   int sn = n, sp = p;
   for (int o = 1; o < 64; o <<= 1) {
     const int an = __shfl_up(sn, o), ap = __shfl_up(sp, o);
@@ -586,42 +623,58 @@ __global__ void __launch_bounds__(1024) few_select(FewArgs a) {
     }
   }
   if (lane == 63) {
-    wave_n[wave] = sn;
-    wave_p[wave] = sp;
+    lds.wave_n[wave] = sn;
+    lds.wave_p[wave] = sp;
   }
   __syncthreads();
   int at = sn - n, row = sp - p;
   for (int w = 0; w < wave; ++w) {
-    at += wave_n[w];
-    row += wave_p[w];
+    at += lds.wave_n[w];
+    row += lds.wave_p[w];
   }
-  if (m0) {
-    a.active[at] = e0;
-    a.mask[at] = m0;
+#pragma unroll
+  for (int j = 0; j < PER; ++j) {
+    const int e = tid * PER + j;
+    const uint64_t m = e < d.X ? mask[e] : 0;
+    if (!m) continue;
+    a.active[at] = e;
+    a.mask[at] = m;
     a.first[at] = row;
     ++at;
-    row += __popcll(m0);
+    row += __popcll(m);
   }
-  if (m1) {
-    a.active[at] = e0 + 1;
-    a.mask[at] = m1;
-    a.first[at] = row;
-    ++at;
-  }
-  if (tid == 1023) a.count[0] = at;
+  if (tid == NTHREADS - 1) a.count[0] = at;
 }
 
-template <class T, class W, int RT, int NTMAX>
-__global__ void __launch_bounds__(NTHREADS) few_gate_up(FewArgs a) {
-  __shared__ f32x4 lds[NW * 2 * RT * NTMAX * 64];
+// The choice needs one workgroup and the shared experts do not wait for it:
+// workgroup 0 chooses while the others stream the shared experts' weights.
+template <class T, int EPL, int NT>
+__global__ void __launch_bounds__(NTHREADS) few_select_shared(FewArgs a) {
+  constexpr int SUMS = NW * 2 * NT * 64 * (int)sizeof(f32x4), SELECT = (int)sizeof(SelectLds);
+  __shared__ __attribute__((aligned(16))) char lds[SUMS > SELECT ? SUMS : SELECT];
+  if (blockIdx.x) {
+    shared_expert<T, NT>(a, blockIdx.x - 1, (f32x4*)lds);
+    return;
+  }
+  select<EPL>(a, *(SelectLds*)lds);
+}
+
+// Workgroups of 4 waves that work apart (KS = 1), or of NW that share K.
+constexpr int GU_WAVES = 4;
+
+template <class T, class W, int KS, int NTMAX>
+__global__ void __launch_bounds__(KS == 1 ? GU_WAVES * 64 : NTHREADS) few_gate_up(FewArgs a) {
+  __shared__ f32x4 lds[KS == 1 ? 1 : NW * 2 * NTMAX * 64];
   __shared__ int list[64];
-  const int tiles = tiles_of(a.d.H, 16 * RT);
-  const int i = blockIdx.x / tiles, u0 = (blockIdx.x - i * tiles) * 16 * RT;
+  constexpr int BLOCK = KS == 1 ? GU_WAVES * 16 : 16;
+  const int tiles = tiles_of(a.d.H, BLOCK);
+  const int i = blockIdx.x / tiles, u0 = (blockIdx.x - i * tiles) * BLOCK + (KS == 1 ? (threadIdx.x >> 6) * 16 : 0);
   if (i >= a.count[0]) return;
   const int n = token_list(a.mask[i], list);
-  if (NTMAX == 1 || n <= 16) gate_up<T, W, RT, 1>(a, i, u0, list, n, lds);
-  else if (NTMAX == 2 || n <= 32) gate_up<T, W, RT, (NTMAX >= 2 ? 2 : 1)>(a, i, u0, list, n, lds);
-  else gate_up<T, W, RT, NTMAX>(a, i, u0, list, n, lds);
+  if (KS == 1 && u0 >= a.d.H) return;
+  if (NTMAX == 1 || n <= 16) gate_up<T, W, KS, 1>(a, i, u0, list, 0, n, lds);
+  else  // more than 32 tokens read the expert's rows twice
+    for (int m0 = 0; m0 < n; m0 += 32) gate_up<T, W, KS, NTMAX>(a, i, u0, list, m0, n, lds);
 }
 
 template <class T, class W, int RT, int NTMAX>
@@ -633,7 +686,7 @@ __global__ void __launch_bounds__(NTHREADS) few_down(FewArgs a) {
 
 template <class T, int RT, int NT>
 __global__ void __launch_bounds__(NTHREADS) few_up(FewArgs a) {
-  __shared__ f32x4 lds[NW * RT * NT * 64];
+  __shared__ f32x4 lds[NW * NT * 64];
   up<T, RT, NT>(a, blockIdx.x * 16 * RT, lds);
 }
 
@@ -666,8 +719,8 @@ FewWs few_layout(const FewDims& d) {
   // tokens' hidden values are read once a tile), and shares as many as give
   // every CU two workgroups and every wave of a share something to do.
   const int64_t most = d.X < d.T * d.k ? d.X : d.T * d.k;
-  const int64_t pieces = most * ((d.H + DOWN_K - 1) / DOWN_K), most_parts = (pieces + NW - 1) / NW;
-  w.down_rt = d.T <= 16 ? 4 : 2;
+  const int64_t pieces = most * tiles_of(d.H, d.mx ? DOWN_K_MX : DOWN_K_ACT), most_parts = (pieces + NW - 1) / NW;
+  w.down_rt = 2;
   while (w.down_rt > 1 && tiles_of(d.L, 16 * w.down_rt) * most_parts < 2 * FEW_CUS) w.down_rt /= 2;
   w.tiles = tiles_of(d.L, 16 * w.down_rt);
   int64_t parts = (2 * FEW_CUS + w.tiles - 1) / w.tiles;
@@ -693,51 +746,32 @@ hipError_t few_dispatch(const FewDims& d, F f) {
   return hipGetLastError();
 }
 
-// Row tiles of the products with all tokens: two where the tokens' own rows
-// are much of the traffic, one where there are few tokens (more workgroups) or
-// more than 32 (the waves' sums would not fit beside a second workgroup's).
-template <class F>
-void few_row_tiles(const FewDims& d, F f) {
-  if (d.T > 8 && d.T <= 32) f(std::integral_constant<int, 2>());
-  else f(std::integral_constant<int, 1>());
-}
-
 hipError_t launch_few_project(const FewArgs& a, hipStream_t st) {
   return few_dispatch(a.d, [&](auto t, auto, auto nt) {
-    few_row_tiles(a.d, [&](auto rt) {
-      constexpr int RT = decltype(rt)::value, NT = decltype(nt)::value;
-      if constexpr (RT * NT <= 4)
-        launch((few_project<decltype(t), RT, NT>), dim3((unsigned)project_items<RT>(a.d)), dim3(NTHREADS), 0, st, a);
-    });
+    launch((few_project<decltype(t), decltype(nt)::value>), dim3((unsigned)(tiles_of(a.d.E, 16) + tiles_of(a.d.L, 16))),
+           dim3(NTHREADS), 0, st, a);
   });
 }
 
 hipError_t launch_few_select(const FewArgs& a, hipStream_t st) {
-  const int epl = (a.d.E + 63) / 64;
-#define SELECT(N) launch(few_select<N>, dim3(1), dim3(1024), 0, st, a)
-  if (epl <= 1) SELECT(1);
-  else if (epl <= 2) SELECT(2);
-  else if (epl <= 4) SELECT(4);
-  else if (epl <= 8) SELECT(8);
-  else if (epl <= 16) SELECT(16);
-  else SELECT(32);
-#undef SELECT
-  return hipGetLastError();
+  return few_dispatch(a.d, [&](auto t, auto, auto nt) {
+    const dim3 grid((unsigned)(1 + a.d.S * tiles_of(a.d.HS, 16)));
+    constexpr int NT = decltype(nt)::value;
+    if (a.d.E <= 512) launch((few_select_shared<decltype(t), 8, NT>), grid, dim3(NTHREADS), 0, st, a);
+    else launch((few_select_shared<decltype(t), 32, NT>), grid, dim3(NTHREADS), 0, st, a);
+  });
 }
 
 hipError_t launch_few_gate_up(const FewArgs& a, hipStream_t st) {
   const unsigned most = (unsigned)(a.d.X < a.d.T * a.d.k ? a.d.X : a.d.T * a.d.k);
   return few_dispatch(a.d, [&](auto t, auto w, auto nt) {
-    constexpr int NT = decltype(nt)::value;
-    auto go = [&](auto rt) {
-      constexpr int RT = decltype(rt)::value;
-      launch((few_gate_up<decltype(t), decltype(w), RT, NT>), dim3(most * tiles_of(a.d.H, 16 * RT)), dim3(NTHREADS), 0, st, a);
-    };
-    // four times the hidden units a workgroup where that still gives every CU four of them
-    if constexpr (NT <= 1) {
-      if (most * tiles_of(a.d.H, 64) >= 4 * FEW_CUS) return go(std::integral_constant<int, 4>());
-    }
-    go(std::integral_constant<int, 1>());
+    constexpr int NT = decltype(nt)::value > 2 ? 2 : decltype(nt)::value;
+    // a wave to itself for 16 units where that gives every CU 16 of them
+    if ((int64_t)most * tiles_of(a.d.H, 16) >= 16 * FEW_CUS)
+      launch((few_gate_up<decltype(t), decltype(w), 1, NT>), dim3(most * tiles_of(a.d.H, GU_WAVES * 16)), dim3(GU_WAVES * 64),
+             0, st, a);
+    else
+      launch((few_gate_up<decltype(t), decltype(w), NW, NT>), dim3(most * tiles_of(a.d.H, 16)), dim3(NTHREADS), 0, st, a);
   });
 }
 
@@ -749,9 +783,6 @@ hipError_t launch_few_down(const FewArgs& a, hipStream_t st) {
       launch((few_down<decltype(t), decltype(w), RT, NT>), dim3((unsigned)(a.parts * a.tiles)), dim3(NTHREADS),
              (uint32_t)(NW * a.d.T * 16 * RT * 4), st, a);
     };
-    if constexpr (NT == 1) {
-      if (a.down_rt == 4) return go(std::integral_constant<int, 4>());
-    }
     if (a.down_rt == 2) go(std::integral_constant<int, 2>());
     else go(std::integral_constant<int, 1>());
   });
@@ -759,11 +790,16 @@ hipError_t launch_few_down(const FewArgs& a, hipStream_t st) {
 
 hipError_t launch_few_up(const FewArgs& a, hipStream_t st) {
   return few_dispatch(a.d, [&](auto t, auto, auto nt) {
-    few_row_tiles(a.d, [&](auto rt) {
-      constexpr int RT = decltype(rt)::value, NT = decltype(nt)::value;
-      if constexpr (RT * NT <= 4)
-        launch((few_up<decltype(t), RT, NT>), dim3((unsigned)tiles_of(a.d.D, 16 * RT)), dim3(NTHREADS), 0, st, a);
-    });
+    auto go = [&](auto rt) {
+      constexpr int RT = decltype(rt)::value;
+      launch((few_up<decltype(t), RT, decltype(nt)::value>), dim3((unsigned)tiles_of(a.d.D, 16 * RT)), dim3(NTHREADS), 0, st, a);
+    };
+    // two row tiles share each read of the tokens' rows where those are much
+    // of the traffic (they come in two parts); with few tokens one, for more
+    // workgroups.  6144 x 5120, 16 tokens: 30 us with two, 37 with one; 64:
+    // 61 and 94; one token: 20 with one.
+    if (a.d.T > 8) go(std::integral_constant<int, 2>());
+    else go(std::integral_constant<int, 1>());
   });
 }
 

@@ -302,7 +302,7 @@ const char* moe_last_error(void);
  * zero_dropped, combine, shared_gate_up, up_shared_down, and the tail-split
  * fixups route_fixup, gate_up_fixup, down_fixup, up_fixup; mx_quantize,
  * mx_dequantize, mx_gemm, mx_gather, mx_gate_up, mx_down;
- * few_project, few_select, few_gate_up, few_down, few_up. */
+ * few_project, few_select_shared, few_gate_up, few_down, few_up. */
 typedef struct moe_kernel_time {
   char name[32];    /* kernel label */
   int32_t launches; /* launches recorded since the last moe_timing_read */
