@@ -677,14 +677,16 @@ _DTYPE = {torch.bfloat16: B.MOE_ACT_BF16, torch.float32: B.MOE_ACT_F32}
 
 
 _HERE = contextlib.nullcontext()
+# the raw handle of a device's current stream, without a Stream object around it (1 us a call)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
 def _on(t):
     """(stream handle, device guard) for work on tensor t: its device's current stream."""
     if not t.is_cuda:
         raise ValueError("the library works on GPU tensors")
-    index = t.device.index
-    stream = torch.cuda.current_stream(index).cuda_stream
+    index = t.get_device()
+    stream = _raw_stream(index) if _raw_stream is not None else torch.cuda.current_stream(index).cuda_stream
     # a guard costs as much as a launch: only where the device is not the current one
     return stream, _HERE if index == torch.cuda.current_device() else torch.cuda.device(index)
 
