@@ -5,12 +5,26 @@
 // bound it: each is read once, 16 bytes a lane straight from memory into the
 // A operand of a 16 x 16 matrix instruction (16 weight rows; the tokens are
 // the B operand, 16 at a time), and the tokens' rows come from the caches.
-// The layer is a chain of all-to-all dependencies:
-//   project  logits = x W_r^T, z = x W_d^T, hs = silu(x Wg^T) (x Wu^T)
-//   select   top-k of each token; the chosen experts and their tokens
+// The layer is a chain of all-to-all dependencies, a launch for each:
+//   project  logits = x W_r^T, z = x W_d^T
+//   select   top-k of each token, the chosen experts and their tokens (one
+//            workgroup); beside it hs = silu(x Wg^T) (x Wu^T) of the shared experts
 //   gate_up  h = silu(z Wg^T) (z Wu^T) of each chosen expert
 //   down     c = sum over the chosen experts of w (h W2^T)
 //   up       out = c U^T + sum hs W2s^T
+// MI355X, model width 6144, latent 2048, 8 of 384 experts of 1536 and two
+// shared ones: one token 100 us (319 MB: 3.2 TB/s), 64 tokens 1.0 ms (5.5 GB:
+// 5.5 TB/s), 16 tokens with MX-FP4 experts 250 us (0.72 GB: 2.9 TB/s); a small
+// layer (512 wide, one token) 21 us.  What bounds the small ones is the five
+// round trips to memory, 2 us and more each with cold caches, and launching.
+// One launch for all after the projections (a queue of items in order of
+// dependency, device-scope counters and waits between them) was built and
+// took 58 us for the small layer and 216 us for one token: a wait across the
+// eight XCDs costs more than the end of a launch.  Also slower or level: the
+// tokens' rows staged in LDS with the weights one group ahead (108 us for one
+// token; the registers halve the waves in flight), 16 waves a workgroup in the
+// products with all tokens, and one read of the tokens' rows for several row
+// tiles in the experts' products.
 
 #include "few.h"
 
@@ -19,7 +33,7 @@ namespace moe {
 namespace {
 
 constexpr int FEW_CUS = 256;  // what the split of the down product is sized for (the workspace's size depends on it)
-constexpr int NW = 8;  // waves of a workgroup
+constexpr int NW = 8;       // waves of a workgroup
 constexpr int NTHREADS = NW * 64;
 
 // ------------------------------------------------------------ operands
@@ -375,6 +389,8 @@ __device__ __forceinline__ void gate_up(const FewArgs& a, int i, int u0, const i
 // turn, weighs each piece's sums with the tokens' routing weights and adds
 // them to its own rows in LDS; the waves' rows are added in wave order, and
 // the last of a tile's shares to finish adds the shares in their order.
+// Hidden units of a piece, measured: one token 16.0 us with 256 and 18.7 with 512 (bf16); 16 tokens 59.9 us with 512
+// and 64.8 with 1024 (MX-FP4).
 constexpr int DOWN_K_ACT = 256, DOWN_K_MX = 512;
 template <class W>
 constexpr int DOWN_K = W::KSTEP == 128 ? DOWN_K_MX : DOWN_K_ACT;
@@ -715,9 +731,10 @@ FewWs few_layout(const FewDims& d) {
   w.h_lo = take((size_t)d.T * d.k * d.H * second);
   w.c = take((size_t)d.T * d.L * es);
   w.c_lo = take((size_t)d.T * d.L * second);
-  // The down product: row tiles as high as the tokens' rows in LDS allow (the
-  // tokens' hidden values are read once a tile), and shares as many as give
-  // every CU two workgroups and every wave of a share something to do.
+  // The down product: two row tiles share the reads of the tokens' hidden
+  // values (16 tokens with MX-FP4 experts: 60 us, one tile or four 77; 64 tokens:
+  // 315 us, one 337), one where there would be too few workgroups; shares as
+  // many as give every CU two workgroups and every wave of a share something to do.
   const int64_t most = d.X < d.T * d.k ? d.X : d.T * d.k;
   const int64_t pieces = most * tiles_of(d.H, d.mx ? DOWN_K_MX : DOWN_K_ACT), most_parts = (pieces + NW - 1) / NW;
   w.down_rt = 2;
@@ -766,7 +783,9 @@ hipError_t launch_few_gate_up(const FewArgs& a, hipStream_t st) {
   const unsigned most = (unsigned)(a.d.X < a.d.T * a.d.k ? a.d.X : a.d.T * a.d.k);
   return few_dispatch(a.d, [&](auto t, auto w, auto nt) {
     constexpr int NT = decltype(nt)::value > 2 ? 2 : decltype(nt)::value;
-    // a wave to itself for 16 units where that gives every CU 16 of them
+    // A wave to itself for 16 units where that gives every CU 16 of them (110
+    // MX-FP4 experts of 1536 x 2048: 116 us, sharing K 130; 284 bf16 experts: 551
+    // and 555), else K is shared: one token's 8 experts are only 768 such tiles.
     if ((int64_t)most * tiles_of(a.d.H, 16) >= 16 * FEW_CUS)
       launch((few_gate_up<decltype(t), decltype(w), 1, NT>), dim3(most * tiles_of(a.d.H, GU_WAVES * 16)), dim3(GU_WAVES * 64),
              0, st, a);

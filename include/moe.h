@@ -35,7 +35,8 @@
  *     accumulation is fp32; logits and routing weights are fp32.
  *   - Return 0 (MOE_OK) or a negative MOE_E* code; moe_last_error() returns a
  *     thread-local message for the last failure.  No exception crosses the
- *     ABI.  Identical inputs give bit-identical outputs (no atomics).
+ *     ABI.  Identical inputs give bit-identical outputs (no
+ *     atomics whose order a result depends on).
  *   - bf16 layers need d_model, latent, expert_hidden and shared_hidden to be
  *     multiples of 64 and n_experts a multiple of 4; fp32 layers need latent
  *     a multiple of 8 and shared_hidden a multiple of 4.

@@ -165,6 +165,11 @@ def _check(got, w, x, k, act, bias=None, first=0):
     (33, 6, 2, 128, 320, 576, 3, 64, "bf16", False),
     (64, 4, 2, 256, 128, 1088, 1, 128, "bf16", False),
     (64, 256, 32, 128, 64, 64, 1, 64, "bf16", False),     # 2048 pairs
+    (3, 2048, 32, 128, 64, 64, 0, 64, "bf16", False),     # the most experts
+    (9, 700, 5, 64, 64, 64, 2, 64, "bf16", True),
+    (2, 513, 4, 24, 16, 12, 1, 8, "f32", False),
+    (1, 2, 2, 64, 4096, 64, 1, 64, "bf16", False),        # one share of the down product; wide latent
+    (12, 96, 6, 64, 64, 2048, 1, 64, "bf16", False),      # a wave to itself for 16 hidden units
     (1, 16, 4, 128, 64, 64, 1, 64, "bf16", True),
     (5, 24, 2, 256, 192, 320, 2, 128, "bf16", True),
     (16, 4, 2, 128, 576, 704, 0, 64, "bf16", True),
