@@ -357,21 +357,29 @@ template <> __device__ __forceinline__ WMx Bank<WMx>::row(int64_t r, int K) cons
   return {(const uint8_t*)codes + r * (K / 2), scales + r * mx_scale_bytes(K)};
 }
 
+constexpr int STAGE_BYTES = 32 * 1024;  // LDS that a workgroup may fill with tokens' rows
+__host__ __device__ __forceinline__ int staged_row(int L) { return 2 * L + 8; }  // elements of a row in LDS
+
 // 16 hidden units of a chosen expert for its tokens m0 .. m0 + 16 NT - 1, by
 // one wave (KS = 1) or with K shared by the waves of a workgroup (KS = NW).
-template <class T, class W, int KS, int NT>
-__device__ __forceinline__ void gate_up(const FewArgs& a, int i, int u0, const int* list, int m0, int n, f32x4* lds) {
+// STAGED: the tokens' rows are in LDS (staged), first part, second part and
+// padding to a row.
+template <class T, class W, int KS, int NT, bool STAGED = false>
+__device__ __forceinline__ void gate_up(const FewArgs& a, int i, int u0, const int* list, int m0, int n, f32x4* lds,
+                                        const T* staged = nullptr) {
   const FewDims& d = a.d;
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, r16 = lane & 15, g = lane >> 4;
   const T* hi[NT];
 #pragma unroll
-  for (int t = 0; t < NT; ++t) hi[t] = (const T*)a.z.hi + (int64_t)list[min(m0 + t * 16 + r16, n - 1)] * d.L;
+  for (int t = 0; t < NT; ++t)
+    hi[t] = STAGED ? staged + min(r16, n - 1) * staged_row(d.L)
+                   : (const T*)a.z.hi + (int64_t)list[min(m0 + t * 16 + r16, n - 1)] * d.L;
   const Bank<W> bank{a.w13, a.w13_scales};
   const int64_t row = (int64_t)a.active[i] * 2 * d.H + min(u0 + r16, d.H - 1);
   const W w[2] = {bank.row(row, d.L), bank.row(row + d.H, d.L)};
   f32x4 acc[2][NT];
   zero(acc);
-  dot<W, sizeof(T) == 2, 2, NT>(acc, w, hi, lo_offset<T>(a.z), d.L, KS == 1 ? 0 : wave, KS);
+  dot<W, sizeof(T) == 2, 2, NT>(acc, w, hi, STAGED ? d.L : lo_offset<T>(a.z), d.L, KS == 1 ? 0 : wave, KS);
   const int64_t first = a.first[i];
   reduce<2, KS, 2, NT>(acc, lds, [&](int, int t, const f32x4 (&s)[2]) {
     const int m = m0 + t * 16 + r16;
@@ -391,9 +399,9 @@ __device__ __forceinline__ void gate_up(const FewArgs& a, int i, int u0, const i
 // the last of a tile's shares to finish adds the shares in their order.
 // Hidden units of a piece, measured: one token 16.0 us with 256 and 18.7 with 512 (bf16); 16 tokens 59.9 us with 512
 // and 64.8 with 1024 (MX-FP4).
-constexpr int DOWN_K_ACT = 256, DOWN_K_MX = 512;
+constexpr int DOWN_K_ACT = 256, DOWN_K_MX = 256, DOWN_K_F32 = 128;
 template <class W>
-constexpr int DOWN_K = W::KSTEP == 128 ? DOWN_K_MX : DOWN_K_ACT;
+constexpr int DOWN_K = W::KSTEP == 128 ? DOWN_K_MX : W::KSTEP == 16 ? DOWN_K_F32 : DOWN_K_ACT;
 
 template <class T, class W, int RT, int NT>
 __device__ __forceinline__ void down_piece(const FewArgs& a, int i, int k0, int l0, uint64_t mask, int m0, float* rows) {
@@ -681,12 +689,29 @@ constexpr int GU_WAVES = 4;
 template <class T, class W, int KS, int NTMAX>
 __global__ void __launch_bounds__(KS == 1 ? GU_WAVES * 64 : NTHREADS) few_gate_up(FewArgs a) {
   __shared__ f32x4 lds[KS == 1 ? 1 : NW * 2 * NTMAX * 64];
+  __shared__ f32x4 rows[KS == 1 && W::KSTEP == 128 ? STAGE_BYTES / 16 : 1];
   __shared__ int list[64];
   constexpr int BLOCK = KS == 1 ? GU_WAVES * 16 : 16;
   const int tiles = tiles_of(a.d.H, BLOCK);
   const int i = blockIdx.x / tiles, u0 = (blockIdx.x - i * tiles) * BLOCK + (KS == 1 ? (threadIdx.x >> 6) * 16 : 0);
   if (i >= a.count[0]) return;
   const int n = token_list(a.mask[i], list);
+  if constexpr (KS == 1 && W::KSTEP == 128) {
+    // MX-FP4: the tokens' rows are eight times the weights' bytes in the L1
+    // (two parts of 16 bits a value, read by every wave); from LDS they leave
+    // the weights' loads alone
+    if (n <= 16 && n * staged_row(a.d.L) * 2 <= STAGE_BYTES) {
+      const int per = a.d.L / 8;
+      for (int x = threadIdx.x; x < n * 2 * per; x += GU_WAVES * 64) {
+        const int r = x / per, c = x - r * per;
+        *(uint4*)((bf16_t*)rows + (r >> 1) * staged_row(a.d.L) + (r & 1) * a.d.L + c * 8) =
+            *(const uint4*)((const bf16_t*)(r & 1 ? a.z.lo : a.z.hi) + (int64_t)list[r >> 1] * a.d.L + c * 8);
+      }
+      __syncthreads();
+      if (u0 < a.d.H) gate_up<T, W, KS, 1, true>(a, i, u0, list, 0, n, lds, (const T*)rows);
+      return;
+    }
+  }
   if (KS == 1 && u0 >= a.d.H) return;
   if (NTMAX == 1 || n <= 16) gate_up<T, W, KS, 1>(a, i, u0, list, 0, n, lds);
   else  // more than 32 tokens read the expert's rows twice
@@ -736,7 +761,7 @@ FewWs few_layout(const FewDims& d) {
   // 315 us, one 337), one where there would be too few workgroups; shares as
   // many as give every CU two workgroups and every wave of a share something to do.
   const int64_t most = d.X < d.T * d.k ? d.X : d.T * d.k;
-  const int64_t pieces = most * tiles_of(d.H, d.mx ? DOWN_K_MX : DOWN_K_ACT), most_parts = (pieces + NW - 1) / NW;
+  const int64_t pieces = most * tiles_of(d.H, d.mx ? DOWN_K_MX : d.bf16 ? DOWN_K_ACT : DOWN_K_F32), most_parts = (pieces + NW - 1) / NW;
   w.down_rt = 2;
   while (w.down_rt > 1 && tiles_of(d.L, 16 * w.down_rt) * most_parts < 2 * FEW_CUS) w.down_rt /= 2;
   w.tiles = tiles_of(d.L, 16 * w.down_rt);
