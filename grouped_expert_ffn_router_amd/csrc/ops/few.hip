@@ -13,18 +13,20 @@
 //   down     c = sum over the chosen experts of w (h W2^T)
 //   up       out = c U^T + sum hs W2s^T
 // MI355X, model width 6144, latent 2048, 8 of 384 experts of 1536 and two
-// shared ones: one token 100 us (319 MB: 3.2 TB/s), 64 tokens 1.0 ms (5.5 GB:
-// 5.5 TB/s), 16 tokens with MX-FP4 experts 250 us (0.72 GB: 2.9 TB/s); a small
-// layer (512 wide, one token) 21 us.  What bounds the small ones is the five
+// shared ones: one token 96 us (319 MB: 3.3 TB/s), 64 tokens 1.0 ms (5.5 GB:
+// 5.5 TB/s), 16 tokens with MX-FP4 experts 218 us (0.72 GB: 3.3 TB/s); a small
+// layer (512 wide, one token) 20 us.  What bounds the small ones is the five
 // round trips to memory, 2 us and more each with cold caches, and launching.
 // One launch for all after the projections (a queue of items in order of
 // dependency, device-scope counters and waits between them) was built and
 // took 58 us for the small layer and 216 us for one token: a wait across the
-// eight XCDs costs more than the end of a launch.  Also slower or level: the
+// eight XCDs costs more than the end of a launch.  Also slower or level: bf16
 // tokens' rows staged in LDS with the weights one group ahead (108 us for one
 // token; the registers halve the waves in flight), 16 waves a workgroup in the
-// products with all tokens, and one read of the tokens' rows for several row
-// tiles in the experts' products.
+// products with all tokens, one read of the tokens' rows for several row tiles
+// in the experts' gate and up products, and in the MX-FP4 experts' down product
+// (58 us) the tokens' rows staged in LDS by each wave (77 us) or the next piece's
+// weights loaded ahead (70 us: 147 registers, a quarter of the waves less).
 
 #include "few.h"
 
@@ -110,10 +112,9 @@ __device__ __forceinline__ void mma(f32x4 (&acc)[NT], const WMx::Piece& w, const
 // Products of RT x 16 weight rows with the tokens over the steps [s0, s1) that
 // fall to wave `part` of `parts`, in groups of U steps.  LO: the tokens' rows
 // have a second part, `lo` elements behind the first.
-template <class W, bool LO, int RT, int NT>
+template <class W, bool LO, int RT, int NT, int U = (sizeof(typename W::Piece) == 16 ? 4 : 2)>
 __device__ __forceinline__ void dot(f32x4 (&acc)[RT][NT], const W (&w)[RT], const bf16_t* const (&hi)[NT], int64_t lo,
                                     int K, int part, int parts) {
-  constexpr int U = sizeof(typename W::Piece) == 16 ? 4 : 2;
   const int g = lane_id() >> 4;
   const int full = K / W::KSTEP, groups = (full + U - 1) / U;
   for (int i = part; i < groups; i += parts) {
@@ -277,11 +278,39 @@ __device__ __forceinline__ void zero(f32x4 (&acc)[RT][NT]) {
 
 __host__ __device__ __forceinline__ int tiles_of(int n, int rows) { return (n + rows - 1) / rows; }
 
+// Products over K shared by the waves of a workgroup.  bf16 rows with one token
+// tile: eight steps in flight as long as every wave has them, then four (one
+// token, 6144 wide: 13, 22 and 19 us for the three phases with all tokens; 14, 24
+// and 20 with four; fp32: level).  Groups of steps go round the waves: `turn` is
+// the wave that takes the first, the next product's turn comes back.
+template <class W, bool LO, int RT, int NT, class T>
+__device__ __forceinline__ int dot_waves(f32x4 (&acc)[RT][NT], const W (&w)[RT], const T* const (&hi)[NT], int64_t lo, int K,
+                                         int turn = 0) {
+  const int part = ((threadIdx.x >> 6) + NW - turn) % NW;
+  if constexpr (W::KSTEP == 32 && NT == 1) {
+    const int deep = K - K % (8 * W::KSTEP * NW);
+    if (deep) {
+      dot<W, LO, RT, NT, 8>(acc, w, hi, lo, deep, part, NW);
+      W w2[RT];
+#pragma unroll
+      for (int r = 0; r < RT; ++r) w2[r] = W{w[r].p + deep};
+      const T* const hi2[NT] = {hi[0] + deep};
+      dot<W, LO, RT, NT>(acc, w2, hi2, lo, K - deep, part, NW);
+    } else {
+      dot<W, LO, RT, NT>(acc, w, hi, lo, K, part, NW);
+    }
+    return (turn + tiles_of(K - deep, 4 * W::KSTEP)) % NW;
+  } else {
+    dot<W, LO, RT, NT>(acc, w, hi, lo, K, part, NW);
+    return (turn + tiles_of(K, (W::KSTEP == 32 ? 4 : 1) * W::KSTEP)) % NW;
+  }
+}
+
 // Items: 16 router rows, then 16 rows of W_down.
 template <class T, int NT>
 __device__ __forceinline__ void project(const FewArgs& a, int item, f32x4* lds) {
   const FewDims& d = a.d;
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, r16 = lane & 15, g = lane >> 4;
+  const int lane = threadIdx.x & 63, r16 = lane & 15, g = lane >> 4;
   using W = typename Weights<T>::type;
   const T* hi[NT];
 #pragma unroll
@@ -292,7 +321,7 @@ __device__ __forceinline__ void project(const FewArgs& a, int item, f32x4* lds) 
   const W w[1] = {{(const T*)(router ? a.w_router : a.w_down) + (int64_t)min(n0 + r16, N - 1) * d.D}};
   f32x4 acc[1][NT];
   zero(acc);
-  dot<W, false, 1, NT>(acc, w, hi, 0, d.D, wave, NW);
+  dot_waves<W, false, 1, NT>(acc, w, hi, 0, d.D);
   reduce<1, NW, 1, NT>(acc, lds, [&](int, int t, const f32x4 (&s)[1]) {
     const int m = t * 16 + r16;
     if (m >= d.T) return;
@@ -315,7 +344,7 @@ __device__ __forceinline__ void project(const FewArgs& a, int item, f32x4* lds) 
 template <class T, int NT>
 __device__ __forceinline__ void shared_expert(const FewArgs& a, int item, f32x4* lds) {
   const FewDims& d = a.d;
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, r16 = lane & 15, g = lane >> 4;
+  const int lane = threadIdx.x & 63, r16 = lane & 15, g = lane >> 4;
   using W = typename Weights<T>::type;
   const T* hi[NT];
 #pragma unroll
@@ -325,7 +354,7 @@ __device__ __forceinline__ void shared_expert(const FewArgs& a, int item, f32x4*
   const W w[2] = {{base}, {base + (int64_t)d.HS * d.D}};
   f32x4 acc[2][NT];
   zero(acc);
-  dot<W, false, 2, NT>(acc, w, hi, 0, d.D, wave, NW);
+  dot_waves<W, false, 2, NT>(acc, w, hi, 0, d.D);
   reduce<2, NW, 2, NT>(acc, lds, [&](int, int t, const f32x4 (&s)[2]) {
     const int m = t * 16 + r16;
     if (m >= d.T) return;
@@ -397,8 +426,8 @@ __device__ __forceinline__ void gate_up(const FewArgs& a, int i, int u0, const i
 // turn, weighs each piece's sums with the tokens' routing weights and adds
 // them to its own rows in LDS; the waves' rows are added in wave order, and
 // the last of a tile's shares to finish adds the shares in their order.
-// Hidden units of a piece, measured: one token 16.0 us with 256 and 18.7 with 512 (bf16); 16 tokens 59.9 us with 512
-// and 64.8 with 1024 (MX-FP4).
+// Hidden units of a piece, measured: bf16, one token, 16.0 us with 256 and 18.7 with 512; MX-FP4, 16 tokens, 57.5 us
+// with 256, 59.9 with 512 and 64.8 with 1024; fp32, 7 tokens, 8.7 us with 128, 10.0 with 64 and 11 with 256.
 constexpr int DOWN_K_ACT = 256, DOWN_K_MX = 256, DOWN_K_F32 = 128;
 template <class W>
 constexpr int DOWN_K = W::KSTEP == 128 ? DOWN_K_MX : W::KSTEP == 16 ? DOWN_K_F32 : DOWN_K_ACT;
@@ -503,7 +532,7 @@ __device__ __forceinline__ void down(const FewArgs& a, int part, int tile, float
 template <class T, int RT, int NT>
 __device__ __forceinline__ void up(const FewArgs& a, int n0, f32x4* lds) {
   const FewDims& d = a.d;
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, r16 = lane & 15, g = lane >> 4;
+  const int lane = threadIdx.x & 63, r16 = lane & 15, g = lane >> 4;
   using W = typename Weights<T>::type;
   int64_t row[RT];
 #pragma unroll
@@ -516,14 +545,14 @@ __device__ __forceinline__ void up(const FewArgs& a, int n0, f32x4* lds) {
   for (int r = 0; r < RT; ++r) w[r] = W{(const T*)a.w_up + row[r] * d.L};
 #pragma unroll
   for (int t = 0; t < NT; ++t) hi[t] = (const T*)a.c.hi + (int64_t)min(t * 16 + r16, d.T - 1) * d.L;
-  dot<W, sizeof(T) == 2, RT, NT>(acc, w, hi, lo_offset<T>(a.c), d.L, wave, NW);
+  int turn = dot_waves<W, sizeof(T) == 2, RT, NT>(acc, w, hi, lo_offset<T>(a.c), d.L);
   for (int j = 0; j < d.S; ++j) {
 #pragma unroll
     for (int r = 0; r < RT; ++r) w[r] = W{(const T*)a.ws2 + ((int64_t)j * d.D + row[r]) * d.HS};
 #pragma unroll
     for (int t = 0; t < NT; ++t)
       hi[t] = (const T*)a.hs.hi + ((int64_t)min(t * 16 + r16, d.T - 1) * d.S + j) * d.HS;
-    dot<W, sizeof(T) == 2, RT, NT>(acc, w, hi, lo_offset<T>(a.hs), d.HS, wave, NW);
+    turn = dot_waves<W, sizeof(T) == 2, RT, NT>(acc, w, hi, lo_offset<T>(a.hs), d.HS, turn);
   }
   reduce<1, NW, RT, NT>(acc, lds, [&](int r, int t, const f32x4 (&s)[1]) {
     const int m = t * 16 + r16;
@@ -699,7 +728,7 @@ __global__ void __launch_bounds__(KS == 1 ? GU_WAVES * 64 : NTHREADS) few_gate_u
   if constexpr (KS == 1 && W::KSTEP == 128) {
     // MX-FP4: the tokens' rows are eight times the weights' bytes in the L1
     // (two parts of 16 bits a value, read by every wave); from LDS they leave
-    // the weights' loads alone
+    // the weights' loads alone (110 experts of 1536 x 2048: 90 us, without 116)
     if (n <= 16 && n * staged_row(a.d.L) * 2 <= STAGE_BYTES) {
       const int per = a.d.L / 8;
       for (int x = threadIdx.x; x < n * 2 * per; x += GU_WAVES * 64) {
@@ -809,7 +838,7 @@ hipError_t launch_few_gate_up(const FewArgs& a, hipStream_t st) {
   return few_dispatch(a.d, [&](auto t, auto w, auto nt) {
     constexpr int NT = decltype(nt)::value > 2 ? 2 : decltype(nt)::value;
     // A wave to itself for 16 units where that gives every CU 16 of them (110
-    // MX-FP4 experts of 1536 x 2048: 116 us, sharing K 130; 284 bf16 experts: 551
+    // MX-FP4 experts of 1536 x 2048: 90 us, sharing K 130; 284 bf16 experts: 551
     // and 555), else K is shared: one token's 8 experts are only 768 such tiles.
     if ((int64_t)most * tiles_of(a.d.H, 16) >= 16 * FEW_CUS)
       launch((few_gate_up<decltype(t), decltype(w), 1, NT>), dim3(most * tiles_of(a.d.H, GU_WAVES * 16)), dim3(GU_WAVES * 64),
@@ -840,10 +869,14 @@ hipError_t launch_few_up(const FewArgs& a, hipStream_t st) {
     };
     // two row tiles share each read of the tokens' rows where those are much
     // of the traffic (they come in two parts); with few tokens one, for more
-    // workgroups.  6144 x 5120, 16 tokens: 30 us with two, 37 with one; 64:
+    // workgroups.  6144 x 5120, 16 tokens: 26 us with two, 37 with one; 64:
     // 61 and 94; one token: 20 with one.
-    if (a.d.T > 8) go(std::integral_constant<int, 2>());
-    else go(std::integral_constant<int, 1>());
+    if constexpr (decltype(nt)::value > 1) {
+      go(std::integral_constant<int, 2>());
+    } else {
+      if (a.d.T > 8) go(std::integral_constant<int, 2>());
+      else go(std::integral_constant<int, 1>());
+    }
   });
 }
 
