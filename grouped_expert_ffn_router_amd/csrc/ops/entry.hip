@@ -66,6 +66,8 @@ struct MxLayout {
 int mx_layout(const Q& q, MxLayout* w) {
   if (q.L % MX_BLOCK || q.H % MX_BLOCK)
     return fail(MOE_EINVAL, "MX-FP4 experts need latent and expert_hidden to be multiples of 32");
+  if (q.WX * ceil_div(q.rcap, 256) * ceil_div(2 * q.H > q.L ? 2 * q.H : q.L, 256) > (1ll << 21))
+    return fail(MOE_EINVAL, "a wave's products exceed 2^21 tiles of 256 x 256, what a launch takes");
   const size_t rows = (size_t)(q.WR > 0 ? q.WR : q.WX * q.rcap);
   size_t off = 0;
   auto take = [&](size_t bytes) {
@@ -105,8 +107,9 @@ int few_dims(const moe_dims* d, FewDims* f) {
   if (bf16 && (d->d_model % 64 || d->latent % 64 || d->expert_hidden % 64 || d->shared_hidden % 64))
     return fail(MOE_EINVAL, "bf16 layers need d_model, latent, expert_hidden, shared_hidden multiples of 64");
   const int X = d->n_experts / d->n_ranks;
-  if ((int64_t)d->tokens * d->top_k * ceil_div(d->expert_hidden, 16) > (1ll << 30))
-    return fail(MOE_EINVAL, "tokens * top_k * expert_hidden exceeds the kernels' index range");
+  if ((int64_t)d->tokens * d->top_k * ceil_div(d->expert_hidden, 16) > (1ll << 25) ||
+      d->shared_experts * ceil_div(d->shared_hidden, 16) > (1ll << 20))
+    return fail(MOE_EINVAL, "tokens * top_k * expert_hidden or shared_experts exceed what a launch takes");
   *f = FewDims{d->tokens, d->d_model, d->latent, d->n_experts, d->top_k, d->expert_hidden, d->shared_experts,
                d->shared_hidden, X, d->my_rank * X, bf16, false};
   return MOE_OK;
@@ -156,7 +159,7 @@ int moe_mx_gemm(int32_t out_dtype, int32_t groups, int64_t max_rows, int64_t n, 
   int rc = mx_cols(k, "k");
   if (rc) return rc;
   if (groups > 4096 || max_rows > (1 << 24) || groups * max_rows > (1ll << 30) || groups * n > (1ll << 30) ||
-      groups * ceil_div(max_rows, 256) * ceil_div(n, 256) > (1ll << 28))
+      groups * ceil_div(max_rows, 256) * ceil_div(n, 256) > (1ll << 21))  // a launch has fewer than 2^32 threads
     return fail(MOE_EINVAL, "groups, max_rows or n exceed the kernels' index range");
   if (groups == 0 || max_rows == 0) return MOE_OK;
   if ((rc = mx_rows_ok(a, k, "a")) || (rc = mx_rows_ok(b, k, "b"))) return rc;
@@ -232,12 +235,14 @@ int moe_few_workspace_size(const moe_dims* dims, size_t* bytes) {
   const int rc = few_dims(dims, &f);
   if (rc) return rc;
   if (!bytes) return fail(MOE_EINVAL, "bytes is NULL");
-  // enough for every smaller batch too (the shares of the down product depend on the tokens)
+  // enough for every smaller batch and for experts of either form (the shares of the down product depend on both)
   size_t most = 0;
-  for (; f.T > 0; --f.T) {
-    const size_t n = few_layout(f).total;
-    if (n > most) most = n;
-  }
+  for (; f.T > 0; --f.T)
+    for (int mx = 0; mx <= (f.bf16 ? 1 : 0); ++mx) {
+      f.mx = mx != 0;
+      const size_t n = few_layout(f).total;
+      if (n > most) most = n;
+    }
   *bytes = most;
   return MOE_OK;
 }

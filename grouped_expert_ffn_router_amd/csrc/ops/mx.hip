@@ -66,14 +66,22 @@ struct QGather {  // row r = j * rcap + m of a wave
 
 constexpr int Q_UNROLL = 2;
 
-// cpr: 16-byte pieces of an input row.  Block b covers pieces b * 512 ..,
-// row after row.
+// Launches f(first block, blocks) over `blocks` blocks of 256 threads, 2^23 at
+// a time (a launch has fewer than 2^32 threads).
+template <class F>
+hipError_t in_launches(int64_t blocks, F f) {
+  for (int64_t b = 0; b < blocks; b += 1 << 23) f(b, dim3((unsigned)(blocks - b < 1 << 23 ? blocks - b : 1 << 23)));
+  return hipGetLastError();
+}
+
+// cpr: 16-byte pieces of an input row.  Block b (counted from block0) covers
+// pieces b * 512 .., row after row.
 template <class T, class Src>
 __global__ void __launch_bounds__(256)
-mx_quantize_kernel(Src src, int cpr, uint8_t* __restrict__ codes, int64_t ldc, uint8_t* __restrict__ scales,
-                   int64_t lds) {
+mx_quantize_kernel(Src src, int64_t block0, int cpr, uint8_t* __restrict__ codes, int64_t ldc,
+                   uint8_t* __restrict__ scales, int64_t lds) {
   constexpr int V = 16 / sizeof(T), G = MX_BLOCK / V;
-  const int64_t first = (int64_t)blockIdx.x * (256 * Q_UNROLL);
+  const int64_t first = (block0 + blockIdx.x) * (256 * Q_UNROLL);
   const int64_t row0 = first / cpr;
   const uint32_t off0 = (uint32_t)(first - row0 * cpr);
   uint4 d[Q_UNROLL];
@@ -133,9 +141,9 @@ mx_quantize_kernel(Src src, int cpr, uint8_t* __restrict__ codes, int64_t ldc, u
 template <class T>
 __global__ void __launch_bounds__(256)
 mx_dequantize_kernel(const uint8_t* __restrict__ codes, int64_t ldc, const uint8_t* __restrict__ scales, int64_t lds,
-                     int64_t rows, int cpr, char* __restrict__ outp, int64_t ldo) {
+                     int64_t rows, int64_t block0, int cpr, char* __restrict__ outp, int64_t ldo) {
   constexpr int V = 16 / sizeof(T), G = MX_BLOCK / V;
-  const int64_t first = (int64_t)blockIdx.x * (256 * Q_UNROLL);
+  const int64_t first = (block0 + blockIdx.x) * (256 * Q_UNROLL);
   const int64_t row0 = first / cpr;
   const uint32_t off0 = (uint32_t)(first - row0 * cpr);
   uint32_t c[Q_UNROLL], s[Q_UNROLL], piece[Q_UNROLL];
@@ -179,8 +187,9 @@ hipError_t run_quantize(const Src& src, int64_t rows, int64_t cols, uint8_t* cod
                         int64_t lds, hipStream_t st) {
   if (rows <= 0) return hipSuccess;
   const int64_t cpr = cols * sizeof(T) / 16, blocks = (rows * cpr + 256 * Q_UNROLL - 1) / (256 * Q_UNROLL);
-  launch((mx_quantize_kernel<T, Src>), dim3((unsigned)blocks), dim3(256), 0, st, src, (int)cpr, codes, ldc, scales, lds);
-  return hipGetLastError();
+  return in_launches(blocks, [&](int64_t b, dim3 grid) {
+    launch((mx_quantize_kernel<T, Src>), grid, dim3(256), 0, st, src, b, (int)cpr, codes, ldc, scales, lds);
+  });
 }
 
 hipError_t launch_mx_quantize(bool bf16, int64_t rows, int64_t cols, const void* x, int64_t ldx, uint8_t* codes,
@@ -202,13 +211,12 @@ hipError_t launch_mx_dequantize(bool bf16, int64_t rows, int64_t cols, const uin
                                 const uint8_t* scales, int64_t lds, void* out, int64_t ldo, hipStream_t st) {
   if (rows <= 0) return hipSuccess;
   const int64_t cpr = cols * (bf16 ? 2 : 4) / 16, blocks = (rows * cpr + 256 * Q_UNROLL - 1) / (256 * Q_UNROLL);
-  if (bf16)
-    launch(mx_dequantize_kernel<bf16_t>, dim3((unsigned)blocks), dim3(256), 0, st, codes, ldc, scales, lds, rows,
-           (int)cpr, (char*)out, ldo);
-  else
-    launch(mx_dequantize_kernel<float>, dim3((unsigned)blocks), dim3(256), 0, st, codes, ldc, scales, lds, rows,
-           (int)cpr, (char*)out, ldo);
-  return hipGetLastError();
+  return in_launches(blocks, [&](int64_t b, dim3 grid) {
+    if (bf16)
+      launch(mx_dequantize_kernel<bf16_t>, grid, dim3(256), 0, st, codes, ldc, scales, lds, rows, b, (int)cpr, (char*)out, ldo);
+    else
+      launch(mx_dequantize_kernel<float>, grid, dim3(256), 0, st, codes, ldc, scales, lds, rows, b, (int)cpr, (char*)out, ldo);
+  });
 }
 
 // ------------------------------------------------------------ product, rows by operand

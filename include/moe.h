@@ -377,7 +377,7 @@ typedef struct moe_mx_rows {
  *            group's count are left as they were
  * k is a multiple of 32; k and n at most 2^24, max_rows at most 2^24, groups
  * at most 4096, groups * max_rows and groups * n at most 2^30, and the output
- * at most 2^28 tiles of 256 x 256.  A product with no rows or no groups does
+ * at most 2^21 tiles of 256 x 256.  A product with no rows or no groups does
  * nothing. */
 int moe_mx_gemm(int32_t out_dtype, int32_t groups, int64_t max_rows, int64_t n, int64_t k,
                 const moe_mx_rows* a, const int32_t* counts, const moe_mx_rows* b, void* out,
@@ -385,7 +385,8 @@ int moe_mx_gemm(int32_t out_dtype, int32_t groups, int64_t max_rows, int64_t n, 
 
 /* Device bytes moe_mx_expert_gemm needs beside the layer's workspace (host
  * only): the MX-FP4 rows of live_waves waves.  Needs latent and
- * expert_hidden to be multiples of 32. */
+ * expert_hidden to be multiples of 32, and a wave's products to have at most
+ * 2^21 tiles of 256 x 256. */
 int moe_mx_workspace_size(const moe_dims* dims, size_t* bytes);
 
 /* moe_expert_gemm with MX-FP4 experts: for each expert j of the wave and each
@@ -417,8 +418,8 @@ int moe_mx_expert_gemm(const moe_dims* dims, int32_t wave, const void* wave_buf,
  * layer's if one of them passes the shared experts and the others
  * shared_experts = 0.  Capacity factors, waves and the wave fields of dims
  * play no part and are not looked at, and any number of experts may be held
- * here; fp32 layers take any widths.  T * k <= 2048 follows; the products of
- * the chosen experts are limited to 2^30 groups of 16 hidden units.
+ * here; fp32 layers take any widths.  T * k <= 2048 follows; T * k experts have
+ * at most 2^25 groups of 16 hidden units, the shared experts 2^20.
  *   x, w_router, w_down, bias, bias_row_tokens, w_up, ws13, ws2: as for
  *            moe_route, moe_shared_experts and moe_combine
  *   w13, w2  [X][2H][L] and [X][L][H] act, or their MX-FP4 codes (bf16 layers

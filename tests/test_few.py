@@ -34,6 +34,8 @@ def _dims(**kw):
     (dict(d_model=1 << 25), B.MOE_EINVAL), (dict(shared_experts=1 << 20), B.MOE_EINVAL),
     (dict(shared_experts=-1), B.MOE_EINVAL), (dict(expert_hidden=1 << 25), B.MOE_EINVAL),
     (dict(tokens=64, top_k=32, n_experts=2048, expert_hidden=1 << 24, act_dtype=1), B.MOE_EINVAL),
+    (dict(tokens=64, top_k=32, n_experts=2048, expert_hidden=1 << 19, act_dtype=1), B.MOE_EINVAL),  # threads of a launch
+    (dict(shared_experts=1 << 21, shared_hidden=4, act_dtype=1), B.MOE_EINVAL),
 ])
 def test_bad_dims_are_refused(kw, code):
     with pytest.raises(B.MoeError) as e:

@@ -93,6 +93,7 @@ def _gemm_args(**kw):
     (dict(groups=4096, max_rows=1 << 20), B.MOE_EINVAL, "range"),
     (dict(groups=4096, n=1 << 20), B.MOE_EINVAL, "range"),
     (dict(groups=1, max_rows=1 << 24, n=1 << 21, out_stride_bytes=1 << 22), B.MOE_EINVAL, "range"),
+    (dict(groups=1, max_rows=1 << 20, n=1 << 18, out_stride_bytes=1 << 19), B.MOE_EINVAL, "range"),  # 2^32 threads
     (dict(a=None), B.MOE_EINVAL, "a is NULL"),
     (dict(b=None), B.MOE_EINVAL, "b is NULL"),
     (dict(a=B.mx_rows(None, 256, 32, 16)), B.MOE_EINVAL, "a is NULL"),
