@@ -13,8 +13,8 @@
 //   down     c = sum over the chosen experts of w (h W2^T)
 //   up       out = c U^T + sum hs W2s^T
 // MI355X, model width 6144, latent 2048, 8 of 384 experts of 1536 and two
-// shared ones: one token 96 us (319 MB: 3.3 TB/s), 64 tokens 1.0 ms (5.5 GB:
-// 5.5 TB/s), 16 tokens with MX-FP4 experts 218 us (0.72 GB: 3.3 TB/s); a small
+// shared ones: one token 95 us (319 MB: 3.4 TB/s), 64 tokens 0.96 ms (5.5 GB:
+// 5.8 TB/s), 16 tokens with MX-FP4 experts 218 us (0.72 GB: 3.3 TB/s); a small
 // layer (512 wide, one token) 20 us.  What bounds the small ones is the five
 // round trips to memory, 2 us and more each with cold caches, and launching.
 // One launch for all after the projections (a queue of items in order of
@@ -111,13 +111,22 @@ __device__ __forceinline__ void mma(f32x4 (&acc)[NT], const WMx::Piece& w, const
 
 // Products of RT x 16 weight rows with the tokens over the steps [s0, s1) that
 // fall to wave `part` of `parts`, in groups of U steps.  LO: the tokens' rows
-// have a second part, `lo` elements behind the first.
-template <class W, bool LO, int RT, int NT, int U = (sizeof(typename W::Piece) == 16 ? 4 : 2)>
+// have a second part, `lo` elements behind the first.  FORM: ROUND, each
+// workgroup begins at another group, so that workgroups that run together do not
+// read the same columns of rows a power of two apart, which lie in the same
+// channels of memory; AHEAD, the tokens' values of a group are loaded before its
+// first product (bf16 rows).
+enum DotForm { PLAIN, ROUND, AHEAD };
+template <class W, bool LO, int RT, int NT, int U = (sizeof(typename W::Piece) == 16 ? 4 : 2), DotForm FORM = PLAIN>
 __device__ __forceinline__ void dot(f32x4 (&acc)[RT][NT], const W (&w)[RT], const bf16_t* const (&hi)[NT], int64_t lo,
                                     int K, int part, int parts) {
   const int g = lane_id() >> 4;
   const int full = K / W::KSTEP, groups = (full + U - 1) / U;
-  for (int i = part; i < groups; i += parts) {
+  const int mine = part < groups ? (groups - part + parts - 1) / parts : 0;
+  const int begin = FORM == ROUND && mine > 0 ? (int)(blockIdx.x % (unsigned)mine) * parts : 0;
+  for (int j = part; j < groups; j += parts) {
+    int i = j;
+    if (FORM == ROUND && (i += begin) >= part + mine * parts) i -= mine * parts;
     const int s0 = i * U;
     if (s0 + U <= full) {
       typename W::Piece p[U][RT];
@@ -125,6 +134,29 @@ __device__ __forceinline__ void dot(f32x4 (&acc)[RT][NT], const W (&w)[RT], cons
       for (int u = 0; u < U; ++u)
 #pragma unroll
         for (int r = 0; r < RT; ++r) p[u][r] = w[r].load((s0 + u) * W::KSTEP, g);
+      if constexpr (FORM == AHEAD) {
+        bf16x8 x[U][NT][1 + LO];
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+#pragma unroll
+          for (int t = 0; t < NT; ++t) {
+            const bf16_t* a = hi[t] + (s0 + u) * W::KSTEP + g * 8;
+            x[u][t][0] = *(const bf16x8*)a;
+            if constexpr (LO) x[u][t][1] = *(const bf16x8*)(a + lo);
+          }
+        __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+#pragma unroll
+          for (int r = 0; r < RT; ++r)
+#pragma unroll
+            for (int t = 0; t < NT; ++t)
+#pragma unroll
+              for (int l = 0; l < 1 + LO; ++l)
+                acc[r][t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, p[u][r].w), x[u][t][l],
+                                                                    acc[r][t], 0, 0, 0);
+        continue;
+      }
 #pragma unroll
       for (int u = 0; u < U; ++u)
 #pragma unroll
@@ -151,7 +183,7 @@ __device__ __forceinline__ void dot(f32x4 (&acc)[RT][NT], const W (&w)[RT], cons
 }
 
 // fp32: any K and any alignment, 4 values a lane and step, U steps at a time.
-template <class W, bool LO, int RT, int NT>
+template <class W, bool LO, int RT, int NT, int = 0, DotForm = PLAIN>
 __device__ __forceinline__ void dot(f32x4 (&acc)[RT][NT], const W (&w)[RT], const float* const (&hi)[NT], int64_t, int K,
                                     int part, int parts) {
   constexpr int U = 4;
@@ -281,7 +313,8 @@ __host__ __device__ __forceinline__ int tiles_of(int n, int rows) { return (n + 
 // Products over K shared by the waves of a workgroup.  bf16 rows with one token
 // tile: eight steps in flight as long as every wave has them, then four (one
 // token, 6144 wide: 13, 22 and 19 us for the three phases with all tokens; 14, 24
-// and 20 with four; fp32: level).  Groups of steps go round the waves: `turn` is
+// and 20 with four; fp32: level).  More token tiles: their values loaded ahead
+// (64 tokens: 34, 43 and 52 us, 38, 44 and 61 without).  Groups of steps go round the waves: `turn` is
 // the wave that takes the first, the next product's turn comes back.
 template <class W, bool LO, int RT, int NT, class T>
 __device__ __forceinline__ int dot_waves(f32x4 (&acc)[RT][NT], const W (&w)[RT], const T* const (&hi)[NT], int64_t lo, int K,
@@ -301,7 +334,7 @@ __device__ __forceinline__ int dot_waves(f32x4 (&acc)[RT][NT], const W (&w)[RT],
     }
     return (turn + tiles_of(K - deep, 4 * W::KSTEP)) % NW;
   } else {
-    dot<W, LO, RT, NT>(acc, w, hi, lo, K, part, NW);
+    dot<W, LO, RT, NT, 4, AHEAD>(acc, w, hi, lo, K, part, NW);
     return (turn + tiles_of(K, (W::KSTEP == 32 ? 4 : 1) * W::KSTEP)) % NW;
   }
 }
@@ -408,7 +441,9 @@ __device__ __forceinline__ void gate_up(const FewArgs& a, int i, int u0, const i
   const W w[2] = {bank.row(row, d.L), bank.row(row + d.H, d.L)};
   f32x4 acc[2][NT];
   zero(acc);
-  dot<W, sizeof(T) == 2, 2, NT>(acc, w, hi, STAGED ? d.L : lo_offset<T>(a.z), d.L, KS == 1 ? 0 : wave, KS);
+  // 284 bf16 experts of 1536 x 2048: 516 us, all from the first group on 553
+  dot<W, sizeof(T) == 2, 2, NT, W::KSTEP == 128 ? 2 : 4, W::KSTEP == 32 ? ROUND : PLAIN>(
+      acc, w, hi, STAGED ? d.L : lo_offset<T>(a.z), d.L, KS == 1 ? 0 : wave, KS);
   const int64_t first = a.first[i];
   reduce<2, KS, 2, NT>(acc, lds, [&](int, int t, const f32x4 (&s)[2]) {
     const int m = m0 + t * 16 + r16;
@@ -569,8 +604,12 @@ __device__ __forceinline__ void up(const FewArgs& a, int n0, f32x4* lds) {
 
 // ------------------------------------------------------------ kernels
 
+// The grids of the products with all tokens are smaller than the chip: with
+// several token tiles two waves a SIMD are all that run, and may have the registers.
+#define DENSE_WAVES __attribute__((amdgpu_waves_per_eu(2, NT > 1 ? 2 : 8)))
+
 template <class T, int NT>
-__global__ void __launch_bounds__(NTHREADS) few_project(FewArgs a) {
+__global__ void __launch_bounds__(NTHREADS) DENSE_WAVES few_project(FewArgs a) {
   __shared__ f32x4 lds[NW * NT * 64];
   project<T, NT>(a, blockIdx.x, lds);
 }
@@ -702,7 +741,7 @@ __device__ __forceinline__ void select(const FewArgs& a, SelectLds& lds) {
 // The choice needs one workgroup and the shared experts do not wait for it:
 // workgroup 0 chooses while the others stream the shared experts' weights.
 template <class T, int EPL, int NT>
-__global__ void __launch_bounds__(NTHREADS) few_select_shared(FewArgs a) {
+__global__ void __launch_bounds__(NTHREADS) DENSE_WAVES few_select_shared(FewArgs a) {
   constexpr int SUMS = NW * 2 * NT * 64 * (int)sizeof(f32x4), SELECT = (int)sizeof(SelectLds);
   __shared__ __attribute__((aligned(16))) char lds[SUMS > SELECT ? SUMS : SELECT];
   if (blockIdx.x) {
@@ -755,7 +794,7 @@ __global__ void __launch_bounds__(NTHREADS) few_down(FewArgs a) {
 }
 
 template <class T, int RT, int NT>
-__global__ void __launch_bounds__(NTHREADS) few_up(FewArgs a) {
+__global__ void __launch_bounds__(NTHREADS) DENSE_WAVES few_up(FewArgs a) {
   __shared__ f32x4 lds[NW * NT * 64];
   up<T, RT, NT>(a, blockIdx.x * 16 * RT, lds);
 }
@@ -838,8 +877,8 @@ hipError_t launch_few_gate_up(const FewArgs& a, hipStream_t st) {
   return few_dispatch(a.d, [&](auto t, auto w, auto nt) {
     constexpr int NT = decltype(nt)::value > 2 ? 2 : decltype(nt)::value;
     // A wave to itself for 16 units where that gives every CU 16 of them (110
-    // MX-FP4 experts of 1536 x 2048: 90 us, sharing K 130; 284 bf16 experts: 551
-    // and 555), else K is shared: one token's 8 experts are only 768 such tiles.
+    // MX-FP4 experts of 1536 x 2048: 90 us, sharing K 128; 284 bf16 experts: 516
+    // and 554), else K is shared: one token's 8 experts are only 768 such tiles.
     if ((int64_t)most * tiles_of(a.d.H, 16) >= 16 * FEW_CUS)
       launch((few_gate_up<decltype(t), decltype(w), 1, NT>), dim3(most * tiles_of(a.d.H, GU_WAVES * 16)), dim3(GU_WAVES * 64),
              0, st, a);
@@ -870,7 +909,7 @@ hipError_t launch_few_up(const FewArgs& a, hipStream_t st) {
     // two row tiles share each read of the tokens' rows where those are much
     // of the traffic (they come in two parts); with few tokens one, for more
     // workgroups.  6144 x 5120, 16 tokens: 26 us with two, 37 with one; 64:
-    // 61 and 94; one token: 20 with one.
+    // 53 and 94; one token: 20 with one.
     if constexpr (decltype(nt)::value > 1) {
       go(std::integral_constant<int, 2>());
     } else {

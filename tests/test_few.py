@@ -175,6 +175,8 @@ def _check(got, w, x, k, act, bias=None, first=0):
     (1, 16, 4, 128, 64, 64, 1, 64, "bf16", True),
     (3, 8, 2, 2368, 2176, 64, 3, 2112, "bf16", False),    # whole rounds of deep steps, then groups and single steps
     (13, 8, 2, 4160, 2048, 64, 2, 192, "bf16", True),
+    (12, 96, 6, 64, 320, 1024, 0, 64, "bf16", False),     # waves apart, each workgroup from another group of K on
+    (20, 64, 6, 704, 448, 1088, 2, 448, "bf16", False),
     (5, 24, 2, 256, 192, 320, 2, 128, "bf16", True),
     (16, 4, 2, 128, 576, 704, 0, 64, "bf16", True),
     (40, 4, 2, 192, 128, 1152, 1, 64, "bf16", True),
