@@ -14,7 +14,7 @@
 //   up       out = c U^T + sum hs W2s^T
 // MI355X, model width 6144, latent 2048, 8 of 384 experts of 1536 and two
 // shared ones: one token 95 us (319 MB: 3.4 TB/s), 64 tokens 0.96 ms (5.5 GB:
-// 5.8 TB/s), 16 tokens with MX-FP4 experts 218 us (0.72 GB: 3.3 TB/s); a small
+// 5.8 TB/s), 16 tokens with MX-FP4 experts 215 us (0.72 GB: 3.3 TB/s); a small
 // layer (512 wide, one token) 20 us.  What bounds the small ones is the five
 // round trips to memory, 2 us and more each with cold caches, and launching.
 // One launch for all after the projections (a queue of items in order of
@@ -314,8 +314,9 @@ __host__ __device__ __forceinline__ int tiles_of(int n, int rows) { return (n + 
 // tile: eight steps in flight as long as every wave has them, then four (one
 // token, 6144 wide: 13, 22 and 19 us for the three phases with all tokens; 14, 24
 // and 20 with four; fp32: level).  More token tiles: their values loaded ahead
-// (64 tokens: 34, 43 and 52 us, 38, 44 and 61 without).  Groups of steps go round the waves: `turn` is
-// the wave that takes the first, the next product's turn comes back.
+// (64 tokens: 34, 43 and 52 us, 38, 44 and 61 without).  Groups of steps go
+// round the waves: `turn` is the wave that takes the first, the next product's
+// turn comes back.
 template <class W, bool LO, int RT, int NT, class T>
 __device__ __forceinline__ int dot_waves(f32x4 (&acc)[RT][NT], const W (&w)[RT], const T* const (&hi)[NT], int64_t lo, int K,
                                          int turn = 0) {
@@ -604,8 +605,9 @@ __device__ __forceinline__ void up(const FewArgs& a, int n0, f32x4* lds) {
 
 // ------------------------------------------------------------ kernels
 
-// The grids of the products with all tokens are smaller than the chip: with
-// several token tiles two waves a SIMD are all that run, and may have the registers.
+// The products with all tokens have a workgroup a CU or fewer at the widths above
+// (152 to 192): with several token tiles their two waves a SIMD may have all
+// registers (64 tokens: the last of them 53 us, 61 with fewer).
 #define DENSE_WAVES __attribute__((amdgpu_waves_per_eu(2, NT > 1 ? 2 : 8)))
 
 template <class T, int NT>
