@@ -94,17 +94,20 @@ __device__ __forceinline__ bf16x8 mx_to_bf16(uint32_t codes, uint32_t scale) {
   return bf16x8{a[0], a[1], b[0], b[1], c[0], c[1], d[0], d[1]};
 }
 
+// `in`: false in lanes whose block is past the rows' end; they read nothing and
+// multiply zeros (a token's value there instead would be 0 * inf = NaN).
 template <bool LO, int NT>
 __device__ __forceinline__ void mma(f32x4 (&acc)[NT], const WMx::Piece& w, const bf16_t* const (&hi)[NT], int64_t lo, int k,
-                                    int g) {
+                                    int g, bool in = true) {
+  auto load = [&](const bf16_t* a) { return in ? *(const bf16x8*)a : bf16x8{}; };
 #pragma unroll
   for (int q = 0; q < 4; ++q) {
     const bf16x8 wv = mx_to_bf16((uint32_t)w.w[q], w.scale);
 #pragma unroll
     for (int t = 0; t < NT; ++t) {
       const bf16_t* a = hi[t] + k + g * 32 + q * 8;
-      acc[t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(wv, *(const bf16x8*)a, acc[t], 0, 0, 0);
-      if (LO) acc[t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(wv, *(const bf16x8*)(a + lo), acc[t], 0, 0, 0);
+      acc[t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(wv, load(a), acc[t], 0, 0, 0);
+      if (LO) acc[t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(wv, load(a + lo), acc[t], 0, 0, 0);
     }
   }
 }
@@ -168,7 +171,7 @@ __device__ __forceinline__ void dot(f32x4 (&acc)[RT][NT], const W (&w)[RT], cons
     }
   }
   if constexpr (W::KSTEP == 128) {
-    // the last blocks of 32 that do not fill a step: lanes past them multiply zeros
+    // the last blocks of 32 that do not fill a step: lanes past them have nothing
     const int k = full * W::KSTEP;
     if (k < K && part == groups % parts) {
       const bool in = k + g * 32 < K;
@@ -176,7 +179,7 @@ __device__ __forceinline__ void dot(f32x4 (&acc)[RT][NT], const W (&w)[RT], cons
       for (int r = 0; r < RT; ++r) {
         typename W::Piece p = {i32x4{0, 0, 0, 0}, 0};
         if (in) p = w[r].load(k, g);
-        mma<LO, NT>(acc[r], p, hi, lo, in ? k : k - g * 32, g);
+        mma<LO, NT>(acc[r], p, hi, lo, k, g, in);
       }
     }
   }

@@ -354,3 +354,22 @@ def test_writes_stay_inside_the_outputs_and_the_workspace():
         torch.cuda.synchronize()
         assert (ws[n:] == 0x3C).all() and (out[T * D:] == 5).all() and (idx[T * k:] == -5).all() and (tw[T * k:] == -5).all()
         _check((out[:T * D].view(T, D), idx[:T * k].view(T, k), tw[:T * k].view(T, k)), w, x, k, act)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("L,H", [(64, 128), (128, 64), (192, 64), (320, 192), (128, 128)])
+def test_infinities_in_the_last_blocks_of_a_row(L, H):
+    """MX-FP4 rows whose width is 64 beyond a multiple of 128: lanes past the row's end must not meet its values, since
+    their 0 * inf would be NaN.  All experts' weights are 1, so an infinite latent value makes every sum +inf."""
+    from grouped_expert_ffn_router_amd import runner
+    one = lambda *s: torch.ones(s, dtype=torch.bfloat16, device="cuda")  # noqa: E731
+    D = 64
+    for at in (0, L - 64, L - 1):
+        w_down = one(L, D) / 64
+        w_down[at] = 3e38                              # 64 * 3e38 passes fp32
+        lay = runner.FewTokenLayer(torch.zeros_like(one(2, D)), w_down, runner.mx_quantize(one(2, 2 * H, L)),
+                                   runner.mx_quantize(one(2, L, H)), one(D, L), top_k=1)
+        x = one(3, D)
+        x[1] = 0                                       # a token of zeros beside the infinite ones
+        out = lay(x)[0]
+        assert (out[0] == float("inf")).all() and (out[2] == float("inf")).all() and (out[1] == 0).all()
