@@ -19,6 +19,7 @@ are provided:
 """
 
 import contextlib
+import threading
 
 import numpy as np
 import torch
@@ -834,9 +835,11 @@ class FewTokenLayer:
     serves token t.  With n_ranks > 1 this rank holds X = E / n_ranks experts and
     `out` is its share of the sum over the ranks.
 
-    The layer keeps its weights and one workspace: its calls run in order on one
-    stream (graphs captured from it too); a second layer object over the same
-    weights serves a second stream.
+    Calls may come from any stream and any thread, and may be captured.  The layer
+    keeps its weights and one workspace, for eager calls on the stream that was
+    current when it was made; a call on another stream, or one that is being
+    captured, takes a workspace of its own from torch's allocator (a graph's lies
+    in its memory pool), so that calls that run at once share nothing.
     """
 
     def __init__(self, w_router, w_down, w13, w2, w_up, ws13=None, ws2=None, bias=None, bias_row_tokens=0, top_k=1,
@@ -882,7 +885,10 @@ class FewTokenLayer:
         self.dims = B.Dims(tokens=B.MOE_FEW_TOKENS_MAX, d_model=D, latent=L, n_experts=E, top_k=top_k, n_ranks=n_ranks,
                            waves=1, expert_hidden=H, shared_experts=S, shared_hidden=HS, my_rank=rank,
                            act_dtype=_DTYPE[dt], send_num=1, send_den=1, recv_num=1, recv_den=1)
+        self._by_tokens = {}   # the dims of each batch size met; self.dims are those of the largest
         self.ws = torch.empty((B.few_workspace_size(self.dims),), dtype=torch.uint8, device=dev)
+        self._ws_stream = _on(self.ws)[0] if dev.type == "cuda" else None
+        self._ws_lock = threading.Lock()   # a call launches several kernels: those of two threads must not mix
         self._weights = (self.w_router.data_ptr(), self.w_down.data_ptr(), B._ptr(bias), self.bias_row_tokens) + (
             (w13.codes.data_ptr(), w13.scales.data_ptr(), w2.codes.data_ptr(), w2.scales.data_ptr()) if self._mx
             else (w13.data_ptr(), None, w2.data_ptr(), None)) + (w_up.data_ptr(), B._ptr(self.ws13), B._ptr(self.ws2))
@@ -905,6 +911,16 @@ class FewTokenLayer:
                 out = torch.empty_like(x)
             idx = torch.empty((T, k), dtype=torch.int32, device=x.device)
             w = torch.empty((T, k), dtype=torch.float32, device=x.device)
-            self.dims.tokens = T
-            B.few_tokens(self.dims, x.data_ptr(), *self._weights, idx, w, out, self.ws, st)
+            dims = self._by_tokens.get(T)
+            if dims is None:
+                dims = B.Dims.from_buffer_copy(self.dims)
+                dims.tokens = T
+                self._by_tokens[T] = dims
+            args = (dims, x.data_ptr(), *self._weights, idx, w, out)
+            # the default stream (0) cannot be captured
+            if st == self._ws_stream and not (st and torch.cuda.is_current_stream_capturing()):
+                with self._ws_lock:
+                    B.few_tokens(*args, self.ws, st)
+            else:
+                B.few_tokens(*args, torch.empty_like(self.ws), st)
         return out, idx, w

@@ -373,3 +373,119 @@ def test_infinities_in_the_last_blocks_of_a_row(L, H):
         x[1] = 0                                       # a token of zeros beside the infinite ones
         out = lay(x)[0]
         assert (out[0] == float("inf")).all() and (out[2] == float("inf")).all() and (out[1] == 0).all()
+
+
+# ---------------------------------------------------------------- calls at once
+
+def _cpu_layer(monkeypatch, call, stream, **kw):
+    """A layer on CPU tensors whose library call is `call` and whose current stream is stream()."""
+    import contextlib
+    from grouped_expert_ffn_router_amd import runner
+    z = lambda *s: torch.zeros(s)  # noqa: E731
+    monkeypatch.setattr(runner, "_on", lambda t: (stream(), contextlib.nullcontext()))
+    monkeypatch.setattr(B, "few_tokens", call)
+    monkeypatch.setattr(torch.cuda, "is_current_stream_capturing", lambda: False)
+    good = dict(w_router=z(6, 40), w_down=z(16, 40), w13=z(6, 20, 16), w2=z(6, 16, 10), w_up=z(40, 16), top_k=2)
+    return runner.FewTokenLayer(**{**good, **kw})
+
+
+def test_calls_on_two_streams_share_no_workspace(monkeypatch):
+    seen = []
+    now = [7]
+    lay = _cpu_layer(monkeypatch, lambda *a: seen.append(a[16:18]), lambda: now[0])
+    for now[0] in (7, 8):
+        lay(torch.zeros(3, 40))
+    (a, sa), (b, sb) = seen
+    n = B.few_workspace_size(lay.dims)
+    assert (sa, sb) == (7, 8) and a.numel() >= n and b.numel() >= n
+    assert a.data_ptr() + a.numel() <= b.data_ptr() or b.data_ptr() + b.numel() <= a.data_ptr()
+
+
+def test_calls_of_two_threads_keep_their_own_batch_size(monkeypatch):
+    """The library call releases the interpreter: while one thread is in it, another thread's call begins."""
+    import threading
+    inside, other_done = threading.Event(), threading.Event()
+    read = []
+
+    def call(dims, x, *rest):
+        if dims.tokens == 3:
+            inside.set()
+            assert other_done.wait(20)
+            read.append(dims.tokens)
+        else:
+            other_done.set()
+
+    lay = _cpu_layer(monkeypatch, call, lambda: 7)
+    t = threading.Thread(target=lambda: lay(torch.zeros(3, 40)))
+    t.start()
+    assert inside.wait(20)
+    lay(torch.zeros(5, 40))
+    t.join(20)
+    assert read == [3]
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("act,mx", [("bf16", False), ("bf16", True), ("f32", False)])
+def test_one_layer_on_two_streams_in_two_graphs_and_from_threads(act, mx):
+    """One layer object: calls on two streams at once, two graphs captured from it replayed at once beside an eager call,
+    and two threads on one stream give each call's own bits."""
+    import threading
+    from grouped_expert_ffn_router_amd import runner
+    w, g, dt = _weights(22, 24, 512, 256, 192, 2, 128, act, mx)
+    xs = [torch.randn((T, 512), generator=g, device="cuda").to(dt) for T in (1, 33)]
+    lay = runner.FewTokenLayer(**w, top_k=4)
+    want = [tuple(t.clone() for t in lay(x)) for x in xs]
+    torch.cuda.synchronize()
+    same = lambda a, b: all(torch.equal(u, v) for u, v in zip(a, b))  # noqa: E731
+    streams = [torch.cuda.Stream() for _ in xs]
+    got = [[], []]
+    for _ in range(20):
+        for i, s in enumerate(streams):
+            with torch.cuda.stream(s):
+                got[i].append(lay(xs[i]))
+    torch.cuda.synchronize()
+    assert all(same(want[i], one) for i in range(2) for one in got[i])
+    graphs, held = [], []
+    for i, s in enumerate(streams):
+        graphs.append(torch.cuda.CUDAGraph())
+        with torch.cuda.graph(graphs[i], stream=s):
+            held.append(lay(xs[i]))
+    for _ in range(4):
+        for h in held:
+            for t in h:
+                t.zero_()
+        torch.cuda.synchronize()
+        for i, s in enumerate(streams):
+            with torch.cuda.stream(s):
+                graphs[i].replay()
+        mid = lay(xs[1])
+        torch.cuda.synchronize()
+        assert all(same(want[i], held[i]) for i in range(2)) and same(want[1], mid)
+    # a layer made on a side stream and captured on that stream
+    with torch.cuda.stream(streams[0]):
+        side = runner.FewTokenLayer(**w, top_k=4)
+        first = side(xs[0])
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=streams[0]):
+        inside = side(xs[0])
+    for _ in range(3):
+        graph.replay()
+        with torch.cuda.stream(streams[0]):
+            mid = side(xs[1])
+        torch.cuda.synchronize()
+        assert same(inside, want[0]) and same(first, want[0]) and same(mid, want[1])
+    outs = [[], []]
+
+    def work(i):
+        for _ in range(100):
+            outs[i].append(lay(xs[i]))
+
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(2)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    assert [len(o) for o in outs] == [100, 100]
+    assert all(same(want[i], one) for i in range(2) for one in outs[i])
