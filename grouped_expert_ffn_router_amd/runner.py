@@ -726,30 +726,44 @@ class MxRows:
     codes [..., rows, cols / 2] and scales [..., rows, cols / 32 rounded up to 16], uint8."""
 
     def __init__(self, codes, scales, cols):
-        cb, sb = _mx_strides(cols)
+        self.codes, self.scales, self.cols = codes, scales, cols
+        self._layout()
+
+    @classmethod
+    def _made(cls, codes, scales, cols, code_stride, scale_stride, at):
+        """From contiguous tensors made here, which are at the addresses `at`."""
+        q = cls.__new__(cls)
+        q.codes, q.scales, q.cols = codes, scales, cols
+        q.code_stride, q.scale_stride, q._at, q._arg = code_stride, scale_stride, at, None
+        return q
+
+    def _layout(self):
+        """Checks the tensors and takes their strides."""
+        codes, scales = self.codes, self.scales
+        cb, sb = _mx_strides(self.cols)
         if codes.dtype != torch.uint8 or scales.dtype != torch.uint8:
             raise TypeError("codes and scales are uint8")
         if codes.shape[:-1] != scales.shape[:-1] or codes.shape[-1] != cb or scales.shape[-1] < sb:
-            raise ValueError(f"codes {tuple(codes.shape)} and scales {tuple(scales.shape)} are not rows of {cols} values")
+            raise ValueError(f"codes {tuple(codes.shape)} and scales {tuple(scales.shape)} are not rows of {self.cols} "
+                             "values")
         if codes.device != scales.device:
             raise ValueError("codes and scales are on different devices")
-        self.codes, self.scales, self.cols = codes, scales, cols
         self.code_stride, self.scale_stride = _row_stride(codes, "codes"), _row_stride(scales, "scales")
-        self._arg = None
+        self._at, self._arg = (codes.data_ptr(), scales.data_ptr()), None
 
-    @classmethod
-    def _made(cls, codes, scales, cols, code_stride, scale_stride):
-        """From contiguous tensors made here."""
-        q = cls.__new__(cls)
-        q.codes, q.scales, q.cols = codes, scales, cols
-        q.code_stride, q.scale_stride, q._arg = code_stride, scale_stride, None
-        return q
+    def _where(self):
+        """The tensors' addresses now; memory put in their place since the last call is checked first."""
+        at = (self.codes.data_ptr(), self.scales.data_ptr())
+        if at != self._at:
+            self._layout()
+        return at
 
     @property
     def arg(self):
-        """moe_mx_rows of these tensors."""
+        """moe_mx_rows of the tensors as they are now."""
+        at = self._where()
         if self._arg is None:
-            self._arg = B.mx_rows(self.codes, self.scales, self.code_stride, self.scale_stride)
+            self._arg = B.MxRowsArg(at[0], at[1], self.code_stride, self.scale_stride)
         return self._arg
 
     @property
@@ -780,8 +794,9 @@ def mx_quantize(x):
     with dev:
         codes = torch.empty(lead + (cb,), dtype=torch.uint8, device=x.device)
         scales = torch.empty(lead + (sb,), dtype=torch.uint8, device=x.device)
-        B.mx_quantize(code, x.numel() // cols, cols, x, ld * x.element_size(), codes, cb, scales, sb, st)
-    return MxRows._made(codes, scales, cols, cb, sb)
+        at = (codes.data_ptr(), scales.data_ptr())
+        B.mx_quantize(code, x.numel() // cols, cols, x, ld * x.element_size(), at[0], cb, at[1], sb, st)
+    return MxRows._made(codes, scales, cols, cb, sb, at)
 
 
 def mx_dequantize(q, dtype=torch.bfloat16):
@@ -792,7 +807,8 @@ def mx_dequantize(q, dtype=torch.bfloat16):
     st, dev = _on(q.codes)
     with dev:
         out = torch.empty(q.codes.shape[:-1] + (q.cols,), dtype=dtype, device=q.codes.device)
-        B.mx_dequantize(code, out.numel() // q.cols, q.cols, q.codes, q.code_stride, q.scales, q.scale_stride, out,
+        at = q._where()
+        B.mx_dequantize(code, out.numel() // q.cols, q.cols, at[0], q.code_stride, at[1], q.scale_stride, out,
                         q.cols * out.element_size(), st)
     return out
 
@@ -835,6 +851,10 @@ class FewTokenLayer:
     serves token t.  With n_ranks > 1 this rank holds X = E / n_ranks experts and
     `out` is its share of the sum over the ranks.
 
+    The weights are read where they are at each call: values changed in place and
+    memory put in a tensor's place (w.data = ..., or an attribute of the layer set)
+    count from the next call on, but for graphs captured before; sizes and types stay.
+
     Calls may come from any stream and any thread, and may be captured.  The layer
     keeps its weights and one workspace, for eager calls on the stream that was
     current when it was made; a call on another stream, or one that is being
@@ -844,7 +864,23 @@ class FewTokenLayer:
 
     def __init__(self, w_router, w_down, w13, w2, w_up, ws13=None, ws2=None, bias=None, bias_row_tokens=0, top_k=1,
                  n_ranks=1, rank=0):
-        dt, dev = w_router.dtype, w_router.device
+        self.w_router, self.w_down, self.w13, self.w2, self.w_up = w_router, w_down, w13, w2, w_up
+        self.ws13, self.ws2 = (ws13, ws2) if ws13 is not None and ws13.shape[0] else (None, None)
+        self.bias, self.bias_row_tokens, self.n_ranks = bias, int(bias_row_tokens), n_ranks
+        self._made_of = E, D, L, H, S, HS, dt, dev, _ = self._sizes()
+        self.dims = B.Dims(tokens=B.MOE_FEW_TOKENS_MAX, d_model=D, latent=L, n_experts=E, top_k=top_k, n_ranks=n_ranks,
+                           waves=1, expert_hidden=H, shared_experts=S, shared_hidden=HS, my_rank=rank,
+                           act_dtype=_DTYPE[dt], send_num=1, send_den=1, recv_num=1, recv_den=1)
+        self._by_tokens = {}   # the dims of each batch size met; self.dims are those of the largest
+        self.ws = torch.empty((B.few_workspace_size(self.dims),), dtype=torch.uint8, device=dev)
+        self._ws_stream = _on(self.ws)[0] if dev.type == "cuda" else None
+        self._ws_lock = threading.Lock()   # a call launches several kernels: those of two threads must not mix
+        self._at = self._addresses()
+
+    def _sizes(self):
+        """Checks the weights and gives what a call takes for granted of them."""
+        w_router, w_down, w13, w2, ws13, bias = self.w_router, self.w_down, self.w13, self.w2, self.ws13, self.bias
+        dt, dev, n_ranks = w_router.dtype, w_router.device, self.n_ranks
         if dt not in _DTYPE:
             raise TypeError(f"weights are bf16 or fp32, not {dt}")
         if w_router.dim() != 2 or w_down.dim() != 2:
@@ -856,21 +892,25 @@ class FewTokenLayer:
         if len(w13.shape) != 3 or n_ranks < 1 or E % n_ranks:
             raise ValueError("w13 is [E / n_ranks, 2 H, L]")
         X, H = E // n_ranks, w13.shape[1] // 2
-        self._mx = isinstance(w13, MxRows)
-        if self._mx != isinstance(w2, MxRows):
+        mx = isinstance(w13, MxRows)
+        if mx != isinstance(w2, MxRows):
             raise TypeError("w13 and w2 are both MxRows, or neither")
-        want = {"w_router": (w_router, (E, D)), "w_down": (w_down, (L, D)), "w_up": (w_up, (D, L)),
+        want = {"w_router": (w_router, (E, D)), "w_down": (w_down, (L, D)), "w_up": (self.w_up, (D, L)),
                 "w13": (w13, (X, 2 * H, L)), "w2": (w2, (X, L, H))}
         if S:
-            want |= {"ws13": (ws13, (S, 2 * HS, D)), "ws2": (ws2, (S, D, HS))}
+            want |= {"ws13": (ws13, (S, 2 * HS, D)), "ws2": (self.ws2, (S, D, HS))}
+        bias_tokens = B.MOE_FEW_TOKENS_MAX   # that the bias serves
         if bias is not None:
-            if bias.dtype != torch.float32 or bias.dim() not in (1, 2) or (bias.dim() == 2) != (bias_row_tokens > 0):
+            if bias.dtype != torch.float32 or bias.dim() not in (1, 2) or (bias.dim() == 2) != (self.bias_row_tokens > 0):
                 raise ValueError("bias is fp32 [E], or [nb, E] with bias_row_tokens > 0")
             want["bias"] = (bias, tuple(bias.shape[:-1]) + (E,))
-            self._bias_tokens = bias.shape[0] * bias_row_tokens if bias.dim() == 2 else B.MOE_FEW_TOKENS_MAX
+            if bias.dim() == 2:
+                bias_tokens = bias.shape[0] * self.bias_row_tokens
         for name, (t, shape) in want.items():
             if tuple(t.shape) != shape:
                 raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {shape}")
+            if isinstance(t, MxRows):
+                t._layout()
             parts = [t.codes, t.scales] if isinstance(t, MxRows) else [t]
             for p in parts:
                 if p.device != dev or not p.is_contiguous():
@@ -879,19 +919,16 @@ class FewTokenLayer:
                 raise TypeError(f"{name} is {t.dtype}, not {dt}")
             if isinstance(t, MxRows) and t.scales.shape[-1] != B.mx_strides(t.cols)[1]:
                 raise ValueError(f"{name}: scale rows at their smallest stride are needed")
-        self.w_router, self.w_down, self.w13, self.w2, self.w_up = w_router, w_down, w13, w2, w_up
-        self.ws13, self.ws2 = (ws13, ws2) if S else (None, None)
-        self.bias, self.bias_row_tokens = bias, int(bias_row_tokens)
-        self.dims = B.Dims(tokens=B.MOE_FEW_TOKENS_MAX, d_model=D, latent=L, n_experts=E, top_k=top_k, n_ranks=n_ranks,
-                           waves=1, expert_hidden=H, shared_experts=S, shared_hidden=HS, my_rank=rank,
-                           act_dtype=_DTYPE[dt], send_num=1, send_den=1, recv_num=1, recv_den=1)
-        self._by_tokens = {}   # the dims of each batch size met; self.dims are those of the largest
-        self.ws = torch.empty((B.few_workspace_size(self.dims),), dtype=torch.uint8, device=dev)
-        self._ws_stream = _on(self.ws)[0] if dev.type == "cuda" else None
-        self._ws_lock = threading.Lock()   # a call launches several kernels: those of two threads must not mix
-        self._weights = (self.w_router.data_ptr(), self.w_down.data_ptr(), B._ptr(bias), self.bias_row_tokens) + (
-            (w13.codes.data_ptr(), w13.scales.data_ptr(), w2.codes.data_ptr(), w2.scales.data_ptr()) if self._mx
-            else (w13.data_ptr(), None, w2.data_ptr(), None)) + (w_up.data_ptr(), B._ptr(self.ws13), B._ptr(self.ws2))
+        return E, D, L, H, S, HS, dt, dev, (mx, bias_tokens)
+
+    def _addresses(self):
+        """The weights as moe_few_tokens takes them."""
+        w13, w2, bias, ws13 = self.w13, self.w2, self.bias, self.ws13
+        experts = ((w13.codes.data_ptr(), w13.scales.data_ptr(), w2.codes.data_ptr(), w2.scales.data_ptr())
+                   if isinstance(w13, MxRows) else (w13.data_ptr(), None, w2.data_ptr(), None))
+        shared = (None, None) if ws13 is None else (ws13.data_ptr(), self.ws2.data_ptr())
+        return (self.w_router.data_ptr(), self.w_down.data_ptr(), None if bias is None else bias.data_ptr(),
+                self.bias_row_tokens, *experts, self.w_up.data_ptr(), *shared)
 
     def __call__(self, x, out=None):
         T, k = x.shape[0], self.dims.top_k
@@ -900,11 +937,16 @@ class FewTokenLayer:
                              f"{self.w_router.dtype} values are needed")
         if x.device != self.w_router.device:
             raise ValueError("x is on another device than the layer")
-        if T > B.MOE_FEW_TOKENS_MAX or self.bias is not None and T > self._bias_tokens:
+        if T > self._made_of[-1][1]:
             raise ValueError(f"{T} tokens are more than the layer (or its bias) takes")
         if out is not None and (out.shape != x.shape or out.dtype != x.dtype or not out.is_contiguous()
                                 or out.device != x.device):
             raise ValueError("out must be like x")
+        at = self._addresses()
+        if at != self._at:   # memory put in a weight's place since the last call
+            if self._sizes() != self._made_of:
+                raise ValueError("the weights' sizes or types are not those the layer was made with")
+            self._at = at
         st, dev = _on(x)
         with dev:
             if out is None:
@@ -916,7 +958,7 @@ class FewTokenLayer:
                 dims = B.Dims.from_buffer_copy(self.dims)
                 dims.tokens = T
                 self._by_tokens[T] = dims
-            args = (dims, x.data_ptr(), *self._weights, idx, w, out)
+            args = (dims, x.data_ptr(), *at, idx, w, out)
             # the default stream (0) cannot be captured
             if st == self._ws_stream and not (st and torch.cuda.is_current_stream_capturing()):
                 with self._ws_lock:

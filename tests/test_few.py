@@ -424,6 +424,62 @@ def test_calls_of_two_threads_keep_their_own_batch_size(monkeypatch):
     assert read == [3]
 
 
+@pytest.mark.parametrize("mx", [False, True])
+def test_weights_are_read_where_they_are(monkeypatch, mx):
+    """Memory put in a weight's place is what the next call reads, and is checked first: addresses kept from the
+    construction would point into freed memory."""
+    from grouped_expert_ffn_router_amd import runner
+    seen = []
+    z = lambda *s: torch.zeros(s, dtype=torch.bfloat16)  # noqa: E731
+    rows = lambda *s: runner.MxRows(torch.zeros(s[:-1] + (s[-1] // 2,), dtype=torch.uint8),  # noqa: E731
+                                    torch.zeros(s[:-1] + (16,), dtype=torch.uint8), s[-1]) if mx else z(*s)
+    kw = dict(w_router=z(6, 64), w_down=z(128, 64), w13=rows(6, 128, 128), w2=rows(6, 128, 64), w_up=z(64, 128),
+              ws13=z(2, 128, 64), ws2=z(2, 64, 64), bias=torch.zeros(6))
+    lay = _cpu_layer(monkeypatch, lambda *a: seen.append(a), lambda: 7, **kw)
+    at = dict(w_router=2, w_down=3, bias=4, w13=6, w13_scales=7, w2=8, w2_scales=9, w_up=10, ws13=11, ws2=12)
+    names = [n for n in at if mx or not n.endswith("_scales")]
+
+    def tensor(n):
+        t = kw[n.replace("_scales", "")]
+        return (t.scales if n.endswith("_scales") else t.codes) if isinstance(t, runner.MxRows) else t
+
+    for n in names:
+        tensor(n).data = torch.zeros_like(tensor(n))
+        lay(z(3, 64))
+        for m in names:
+            assert seen[-1][at[m]] == tensor(m).data_ptr(), (n, m)
+    lay.w_up = kw["w_up"] = z(64, 128)
+    lay(z(3, 64))
+    assert seen[-1][at["w_up"]] == lay.w_up.data_ptr()
+    n = len(seen)
+    for name in names:
+        old = tensor(name).data
+        tensor(name).data = torch.zeros(tuple(old.shape[:-1]) + (old.shape[-1] + 1,), dtype=old.dtype)
+        with pytest.raises(ValueError):
+            lay(z(3, 64))
+        tensor(name).data = old
+    lay.w_router = torch.zeros(6, 64)
+    with pytest.raises((ValueError, TypeError)):
+        lay(torch.zeros(3, 64))
+    assert len(seen) == n
+
+
+def test_rows_follow_their_tensors():
+    """MxRows hands on the tensors' addresses and strides as they are, not as they were at the first call."""
+    from grouped_expert_ffn_router_amd import runner
+    u8 = lambda *s: torch.zeros(s, dtype=torch.uint8)  # noqa: E731
+    q = runner.MxRows(u8(3, 32), u8(3, 16), 64)
+    assert (q.arg.codes, q.arg.scales) == (q.codes.data_ptr(), q.scales.data_ptr())
+    q.codes.data = u8(5, 48)[:3, :32]
+    q.scales.data = u8(3, 32)
+    assert (q.arg.codes, q.arg.scales) == (q.codes.data_ptr(), q.scales.data_ptr())
+    assert (q.arg.code_stride_bytes, q.arg.scale_stride_bytes) == (48, 32)
+    for codes, scales in ((u8(3, 33), u8(3, 16)), (u8(4, 32), u8(3, 16)), (u8(3, 32), u8(3, 8))):
+        q.codes, q.scales = codes, scales
+        with pytest.raises(ValueError):
+            q.arg
+
+
 @pytest.mark.gpu
 @pytest.mark.parametrize("act,mx", [("bf16", False), ("bf16", True), ("f32", False)])
 def test_one_layer_on_two_streams_in_two_graphs_and_from_threads(act, mx):
