@@ -865,6 +865,8 @@ class FewTokenLayer:
     def __init__(self, w_router, w_down, w13, w2, w_up, ws13=None, ws2=None, bias=None, bias_row_tokens=0, top_k=1,
                  n_ranks=1, rank=0):
         self.w_router, self.w_down, self.w13, self.w2, self.w_up = w_router, w_down, w13, w2, w_up
+        if (ws13 is None) != (ws2 is None) or ws13 is not None and ws13.shape[0] != ws2.shape[0]:
+            raise ValueError("ws13 and ws2 go together, with as many shared experts each")
         self.ws13, self.ws2 = (ws13, ws2) if ws13 is not None and ws13.shape[0] else (None, None)
         self.bias, self.bias_row_tokens, self.n_ranks = bias, int(bias_row_tokens), n_ranks
         self._made_of = E, D, L, H, S, HS, dt, dev, _ = self._sizes()

@@ -545,3 +545,18 @@ def test_one_layer_on_two_streams_in_two_graphs_and_from_threads(act, mx):
     torch.cuda.synchronize()
     assert [len(o) for o in outs] == [100, 100]
     assert all(same(want[i], one) for i in range(2) for one in outs[i])
+
+
+# ---------------------------------------------------------------- weights that do not go together
+
+def test_shared_experts_need_both_weights():
+    """One of ws13 and ws2 alone, or of another number of experts, is refused and not taken as no shared experts."""
+    from grouped_expert_ffn_router_amd import runner
+    z = lambda *s: torch.zeros(s)  # noqa: E731
+    good = dict(w_router=z(6, 40), w_down=z(16, 40), w13=z(6, 20, 16), w2=z(6, 16, 10), w_up=z(40, 16), top_k=2)
+    assert runner.FewTokenLayer(**good, ws13=z(2, 8, 40), ws2=z(2, 40, 4)).dims.shared_experts == 2
+    assert runner.FewTokenLayer(**good, ws13=z(0, 8, 40), ws2=z(0, 40, 4)).dims.shared_experts == 0
+    for ws13, ws2 in ((None, z(2, 40, 4)), (z(2, 8, 40), None), (z(0, 8, 40), z(2, 40, 4)), (z(2, 8, 40), z(0, 40, 4)),
+                      (z(2, 8, 40), z(1, 40, 4))):
+        with pytest.raises(ValueError):
+            runner.FewTokenLayer(**good, ws13=ws13, ws2=ws2)
