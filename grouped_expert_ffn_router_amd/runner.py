@@ -897,6 +897,8 @@ class FewTokenLayer:
         mx = isinstance(w13, MxRows)
         if mx != isinstance(w2, MxRows):
             raise TypeError("w13 and w2 are both MxRows, or neither")
+        if mx and dt != torch.bfloat16:
+            raise TypeError("MxRows as experts need bf16 weights beside them")
         want = {"w_router": (w_router, (E, D)), "w_down": (w_down, (L, D)), "w_up": (self.w_up, (D, L)),
                 "w13": (w13, (X, 2 * H, L)), "w2": (w2, (X, L, H))}
         if S:

@@ -560,3 +560,18 @@ def test_shared_experts_need_both_weights():
                       (z(2, 8, 40), z(1, 40, 4))):
         with pytest.raises(ValueError):
             runner.FewTokenLayer(**good, ws13=ws13, ws2=ws2)
+
+
+def test_mx_experts_need_a_bf16_layer():
+    """Refused when the layer is made, not at its first call."""
+    from grouped_expert_ffn_router_amd import runner
+    rows = lambda *s: runner.MxRows(torch.zeros(s[:-1] + (s[-1] // 2,), dtype=torch.uint8),  # noqa: E731
+                                    torch.zeros(s[:-1] + (16,), dtype=torch.uint8), s[-1])
+    for dt in (torch.bfloat16, torch.float32):
+        z = lambda *s: torch.zeros(s, dtype=dt)  # noqa: E731, B023
+        kw = dict(w_router=z(6, 64), w_down=z(64, 64), w13=rows(6, 128, 64), w2=rows(6, 64, 64), w_up=z(64, 64))
+        if dt == torch.bfloat16:
+            assert runner.FewTokenLayer(**kw).dims.expert_hidden == 64
+        else:
+            with pytest.raises(TypeError):
+                runner.FewTokenLayer(**kw)
