@@ -246,7 +246,8 @@ __device__ __forceinline__ void dot(f32x4 (&acc)[RT][NT], const W (&w)[RT], cons
 // ------------------------------------------------------------ activations
 
 __device__ __forceinline__ void put_act(const FewAct& a, bf16_t*, int64_t i, float v) {
-  const bf16_t hi = f32_to_bf16(v);
+  bf16_t hi = f32_to_bf16(v);
+  if ((hi & 0x7fff) == 0x7f80 && __builtin_isfinite(v)) --hi;  // rounded past bf16's largest: that, and the rest below
   const float rest = v - bf16_to_f32(hi);
   ((bf16_t*)a.hi)[i] = hi;
   ((bf16_t*)a.lo)[i] = __builtin_isfinite(rest) ? f32_to_bf16(rest) : (bf16_t)0;

@@ -575,3 +575,27 @@ def test_mx_experts_need_a_bf16_layer():
         else:
             with pytest.raises(TypeError):
                 runner.FewTokenLayer(**kw)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("mx", [False, True])
+@pytest.mark.parametrize("sign", [1, -1])
+def test_values_between_the_largest_of_bf16_and_of_fp32(sign, mx):
+    """A latent value of 1.9970 * 2^127 rounds to an infinity in bf16, but not as two bf16 parts.  D = 64 weights of it:
+    the largest bf16 value and 1.25 * 2^119.  The experts' weights of 2^-124 bring it back: gate = up = sign * 15.98."""
+    from grouped_expert_ffn_router_amd import runner
+    z = lambda *s: torch.zeros(s, dtype=torch.bfloat16, device="cuda")  # noqa: E731
+    D = L = H = 64
+    w_down = z(L, D)
+    w_down[0, 0] = sign * torch.finfo(torch.bfloat16).max
+    w_down[0, 1] = sign * 1.25 * 2.0 ** 119
+    w13 = z(1, 2 * H, L)
+    w13[:, :, 0] = 2.0 ** -124
+    w2 = z(1, L, H) + 2.0 ** -10
+    if mx:
+        w13, w2 = runner.mx_quantize(w13), runner.mx_quantize(w2)
+    w = dict(w_router=z(1, D), w_down=w_down, w13=w13, w2=w2, w_up=z(D, L) + 1, ws13=z(0, 2, D), ws2=z(0, D, 1))
+    x = z(3, D) + 1
+    got = runner.FewTokenLayer(**w, top_k=1)(x)
+    assert torch.isfinite(got[0].float()).all()
+    _check(got, w, x, 1, "bf16")
