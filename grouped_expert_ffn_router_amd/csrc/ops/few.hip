@@ -82,8 +82,9 @@ __device__ __forceinline__ void mma(f32x4 (&acc)[NT], const WBf16::Piece& w, con
 }
 
 // Eight codes (one dword) with their block's scale as bf16 values: exact (a
-// code has two significant bits).  The conversion takes the scale's exponent
-// field as the scale byte itself.
+// code has two significant bits) up to bf16's range, which only scale bytes 253
+// and 254 pass.  The conversion takes the scale's exponent field as the scale
+// byte itself: 0 stands for 2^-127 and 255 for NaN.
 __device__ __forceinline__ bf16x8 mx_to_bf16(uint32_t codes, uint32_t scale) {
   const float s = __uint_as_float(scale << 23);
   typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));

@@ -413,7 +413,11 @@ int moe_mx_expert_gemm(const moe_dims* dims, int32_t wave, const void* wave_buf,
  *   c = sum_i topk_w[i] * (h_i . W2^T) over the chosen experts held here,
  *   out = act(c . U^T + sum_j h_s[j] . W2_j^T), h_s as moe_shared_experts,
  * with nothing rounded below fp32 before `out` (products with bf16 weights
- * take the fp32 activations as two bf16 parts, 2^-17 off at most).  With
+ * take the fp32 activations as two bf16 parts, 2^-17 off at most above 2^-117,
+ * and want finite weights: an infinite one may give NaN in the place of an
+ * infinity).  The other tokens of a call have a part in a token's `out` only in
+ * the order of its fp32 sums: the same call gives the same bits, the same token
+ * in another batch may differ by a rounding.  With
  * n_ranks > 1 and the tokens on every rank, the ranks' outputs add up to the
  * layer's if one of them passes the shared experts and the others
  * shared_experts = 0.  Capacity factors, waves and the wave fields of dims
@@ -422,9 +426,12 @@ int moe_mx_expert_gemm(const moe_dims* dims, int32_t wave, const void* wave_buf,
  * at most 2^25 groups of 16 hidden units, the shared experts 2^20.
  *   x, w_router, w_down, bias, bias_row_tokens, w_up, ws13, ws2: as for
  *            moe_route, moe_shared_experts and moe_combine
- *   w13, w2  [X][2H][L] and [X][L][H] act, or their MX-FP4 codes (bf16 layers
- *            with L and H multiples of 32) with w13_scales and w2_scales set,
- *            rows at the smallest strides (moe_mx_strides)
+ *   w13, w2  [X][2H][L] and [X][L][H] act, or their MX-FP4 codes (bf16
+ *            layers, whose L and H are multiples of 64) with w13_scales and
+ *            w2_scales set, rows at the smallest strides (moe_mx_strides).  The
+ *            products take the codes' values in bf16, so those of 2^128 and more
+ *            (4 and 6 at scale byte 253, 2 and more at 254; moe_mx_quantize
+ *            writes 252 at most) are infinite here
  *   topk_idx [T][k] int32, topk_w [T][k] fp32, out [T][D] act: outputs
  *   ws       moe_few_workspace_size() bytes, used by one call at a time */
 #define MOE_FEW_TOKENS_MAX 64

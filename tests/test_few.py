@@ -599,3 +599,55 @@ def test_values_between_the_largest_of_bf16_and_of_fp32(sign, mx):
     got = runner.FewTokenLayer(**w, top_k=1)(x)
     assert torch.isfinite(got[0].float()).all()
     _check(got, w, x, 1, "bf16")
+
+
+# ---------------------------------------------------------------- scale bytes of the experts' blocks
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("T", [1, 7, 40])
+@pytest.mark.parametrize("L,H,E", [(192, 320, 6), (128, 1024, 64)])     # the second: a wave to itself for 16 units (T > 7)
+def test_zero_and_nan_scales_of_the_experts(T, L, H, E):
+    """Scale byte 255 in one block of w13 and of w2 gives NaN to the tokens that choose those experts and to no other;
+    blocks of scale byte 0 (2^-127, some with codes 0) count as what they stand for."""
+    from grouped_expert_ffn_router_amd import runner
+    w, g, dt = _weights(31 + T, E, 256, L, H, 1, 64, "bf16", mx=True)
+    for q in (w["w13"], w["w2"]):
+        q.scales[3, 5, 1] = 0                                                # random codes times 2^-127
+        q.scales[4, :, 0] = 0
+        q.codes[4, :, :16] = 0
+    x = torch.randn((T, 256), generator=g, device="cuda").to(dt)
+    bias = torch.zeros((T, E), device="cuda")
+    for t in range(T):                                                       # token t: experts t % 6 and (t + 2) % 6
+        bias[t, [t % 6, (t + 2) % 6]] = 50
+    kw = dict(bias=bias, bias_row_tokens=1, top_k=2)
+    _check(runner.FewTokenLayer(**w, **kw)(x), w, x, 2, "bf16", bias)
+    w["w13"].scales[1, 2 * H - 1, L // 32 - 1] = 255                         # the last block of the last up row
+    w["w2"].scales[2, 17, 0] = 255
+    out, idx, tw = runner.FewTokenLayer(**w, **kw)(x)
+    hit = ((idx == 1) | (idx == 2)).any(1)
+    assert torch.isnan(out[hit].float()).all() and torch.isfinite(out[~hit].float()).all()
+    if bool((~hit).any()):
+        _check((out[~hit], idx[~hit], tw[~hit]), w, x[~hit], 2, "bf16", bias[~hit])
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("byte", [0, 1, 2, 127, 251, 252, 253, 254])
+def test_every_kind_of_scale_times_a_latent_value_that_balances_it(byte):
+    """One expert whose gate and up blocks all have one scale byte, and latent values of about its inverse; codes up to the
+    largest whose value bf16 holds (6, but 3 with byte 253 and 1.5 with 254: of a magnitude above that a product is not
+    finite)."""
+    from grouped_expert_ffn_router_amd import runner
+    g = torch.Generator().manual_seed(byte)
+    D = L = H = 64
+    top = {253: 6, 254: 4}.get(byte, 8)                                      # magnitudes' codes below this
+    mag = lambda *s: torch.randint(0, top, s, generator=g) + 8 * torch.randint(0, 2, s, generator=g)  # noqa: E731
+    codes = (mag(1, 2 * H, L // 2) | mag(1, 2 * H, L // 2) << 4).to(torch.uint8)
+    scales = torch.full((1, 2 * H, 16), byte, dtype=torch.uint8)
+    w2 = runner.mx_quantize((torch.randn((1, L, H), generator=g) / 8).cuda())
+    z = lambda *s: torch.zeros(s, dtype=torch.bfloat16, device="cuda")  # noqa: E731
+    unit = 2.0 ** -max(-120, min(120, byte - 127))
+    w = dict(w_router=z(1, D), w_down=(torch.eye(L) * unit).bfloat16().cuda(),
+             w13=runner.MxRows(codes.cuda(), scales.cuda(), L), w2=w2, w_up=torch.eye(D).bfloat16().cuda(),
+             ws13=z(0, 2, D), ws2=z(0, D, 1))
+    x = torch.randint(1, 4, (5, D), generator=g).bfloat16().cuda()
+    _check(runner.FewTokenLayer(**w, top_k=1)(x), w, x, 1, "bf16")
