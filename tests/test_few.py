@@ -651,3 +651,53 @@ def test_every_kind_of_scale_times_a_latent_value_that_balances_it(byte):
              ws13=z(0, 2, D), ws2=z(0, D, 1))
     x = torch.randint(1, 4, (5, D), generator=g).bfloat16().cuda()
     _check(runner.FewTokenLayer(**w, top_k=1)(x), w, x, 1, "bf16")
+
+
+# ---------------------------------------------------------------- the forms that large layers take
+
+def _forms(T, E, k, L, H, act, mx):
+    """What the launches go by (ops/few.hip): waves that share K in the experts' gate and up products, row tiles of the
+    down product, and the most tokens of an expert whose rows are staged in LDS (MX-FP4, a wave to itself)."""
+    up = lambda a, b: -(-a // b)  # noqa: E731
+    most = min(E, T * k)
+    waves = 1 if most * up(H, 16) >= 16 * 256 else 8
+    parts = up(most * up(H, 128 if act == "f32" else 256), 8)
+    row_tiles = 2 if up(L, 32) * parts >= 2 * 256 else 1
+    return waves, row_tiles, min(16, 32 * 1024 // ((2 * L + 8) * 2)) if mx and waves == 1 else 0
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("T,E,k,L,H,act,mx,forms", [
+    (12, 96, 6, 320, 1024, "bf16", True, (1, 1, 16)),
+    (16, 128, 8, 1088, 512, "bf16", True, (1, 2, 7)),     # in one launch, experts of few tokens from LDS and others not
+    (20, 64, 8, 192, 1088, "bf16", True, (1, 1, 16)),
+    (40, 64, 8, 512, 1024, "bf16", True, (1, 2, 15)),
+    (64, 64, 8, 512, 1024, "bf16", True, (1, 2, 15)),
+    (64, 16, 4, 2304, 576, "bf16", True, (8, 1, 0)),
+    (33, 32, 4, 1024, 1024, "bf16", True, (8, 2, 0)),
+    (64, 64, 8, 512, 1024, "bf16", False, (1, 2, 0)),     # 64 KB of LDS a workgroup in the down product
+    (64, 32, 4, 1024, 1024, "bf16", False, (8, 2, 0)),
+    (9, 128, 8, 576, 1024, "bf16", False, (1, 2, 0)),
+    (12, 64, 6, 53, 1030, "f32", False, (1, 1, 0)),
+    (12, 64, 6, 245, 1030, "f32", False, (1, 2, 0)),
+    (40, 64, 3, 61, 1027, "f32", False, (1, 1, 0)),
+    (20, 64, 6, 245, 1030, "f32", False, (1, 2, 0)),
+    (64, 64, 2, 421, 530, "f32", False, (8, 2, 0)),
+])
+def test_forms_of_large_layers(T, E, k, L, H, act, mx, forms):
+    """Every token has expert 1; the other picks are spread, so that experts of one token and of all T are in one launch."""
+    from grouped_expert_ffn_router_amd import runner
+    assert _forms(T, E, k, L, H, act, mx) == forms
+    w, g, dt = _weights(T + L, E, 128, L, H, 1, 64, act, mx)
+    x = torch.randn((T, 128), generator=g, device="cuda").to(dt)
+    bias = torch.zeros(E, device="cuda")
+    bias[1] = 50
+    lay = runner.FewTokenLayer(**w, bias=bias, top_k=k)
+    lay.ws.fill_(0xFF)
+    got = lay(x)
+    assert (got[1][:, 0] == 1).all()
+    tokens = torch.bincount(got[1].flatten().long(), minlength=E)
+    assert int(tokens.max()) == T and (T >= 40 or bool((tokens == 1).any()))
+    _check(got, w, x, k, act, bias)
+    again = lay(x)
+    assert all(torch.equal(a, b) for a, b in zip(got, again))
