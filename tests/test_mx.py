@@ -380,3 +380,48 @@ def test_quantize_product_and_back_together():
     # and the saturation of (6, 8) to 6 is a quarter of 8
     err = (xv - x.float()).abs().view(1000, -1, 32)
     assert (err <= 0.25 * x.float().abs().view(1000, -1, 32).amax(-1, keepdim=True)).all()
+
+
+# ---------------------------------------------------------------- long rows, extreme scales, many groups
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("act", ["bf16", "f32"])
+@pytest.mark.parametrize("M", [1, 17, 33, 64])
+@pytest.mark.parametrize("K", [4128, 6144, 8224, 16416])
+def test_gemm_of_few_long_rows(K, M, act):
+    """More than eight pieces of 512 values: sixteen waves share K; past 8192 a wave takes several pieces."""
+    _gemm_case(1, M, 40, K, act, "mild", None, seed=K + M)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("K", [544, 6144, 8224])
+@pytest.mark.parametrize("M", [3, 40, 300])
+@pytest.mark.parametrize("kind", ["nan_last", "balanced"])
+@pytest.mark.parametrize("act", ["bf16", "f32"])
+def test_gemm_scales_of_long_rows(monkeypatch, act, kind, M, K):
+    """nan_last: scale byte 255 in the last block of a few rows.  balanced: block scales from 2^-127 to 2^127 in the one
+    operand and the inverse in the other, so that each product is of the order of one."""
+    side = []
+
+    def operand(rng, rows, cols, _):
+        codes, scales = _operand_mild(rng, rows, cols, "mild")
+        nb = cols // 32
+        if kind == "nan_last":
+            scales[::5, nb - 1] = 255
+        else:
+            b = np.random.default_rng(9).integers(0, 255, nb)
+            scales[:, :nb] = 254 - b if side else b
+            side.append(1)
+        return codes, scales
+
+    _operand_mild = _operand
+    monkeypatch.setattr(sys.modules[__name__], "_operand", operand)
+    _gemm_case(1, M, 70, K, act, kind, None, seed=M)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("act", ["bf16", "f32"])
+@pytest.mark.parametrize("G,M,N,K", [(300, 5, 33, 96), (300, 70, 20, 64), (4096, 1, 3, 32), (1100, 66, 5, 32)])
+def test_gemm_of_many_groups(G, M, N, K, act):
+    counts = np.random.default_rng(G).integers(-1, M + 2, G).tolist()
+    _gemm_case(G, M, N, K, act, "mild", counts, seed=G)
