@@ -231,3 +231,99 @@ def test_one_rank_layer_two_streams_and_graph():
         lay.run()
         torch.cuda.synchronize()
         assert torch.equal(lay.out, want)
+
+
+# ---------------------------------------------------------------- what comes out of the layer
+
+def _f64(t):
+    return t.double().cpu().numpy()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("name,gather", [("mini_bf16", "fused"), ("mini_bf16_skew", "buffer"), ("mini_bf16_seg", "fused"),
+                                         ("mini_bf16_longk", "fused"), (1, "buffer")])
+def test_output_is_the_weighted_sum_of_the_returned_rows(name, gather):
+    """out = act(c . U^T + sum_j h_j . W2_j^T) with c = act(sum_i w_i ret_i) and h_j = act(silu(x Wg^T) (x Wu^T)), from the
+    rows that the experts returned.  Each rounding to act is off by half a step of its value, each fp32 sum of n products by
+    n * 2^-24 of the sum of their magnitudes; both are carried through the products that follow."""
+    from grouped_expert_ffn_router_amd import runner
+    sh, inp, lay, *_ = _layer(runner.AllRanksLayer, name, gather)
+    half = 2.0 ** -8 if sh.act == "bf16" else 2.0 ** -24
+    eps = 2.0 ** -24
+    T, D, L, k, S, HS = sh.tokens, sh.d_model, sh.latent, sh.top_k, sh.shared_experts, sh.shared_hidden
+    U, ws13, ws2, ret = (_f64(t) for t in (lay.w_up, lay.ws13, lay.ws2, lay.ret))
+    for s in range(sh.n_ranks):
+        w, x, slot = _f64(lay.w[s]), _f64(lay.x[s]), lay.slot_of[s].cpu().numpy()
+        rows = np.where((slot >= 0)[..., None], ret[:, s].reshape(-1, L)[slot.clip(min=0)], 0)   # [T][k][L]
+        c = (w[..., None] * rows).sum(1)
+        dc = k * eps * (w[..., None] * np.abs(rows)).sum(1) + half * np.abs(c)
+        want, tol = c @ U.T, dc @ np.abs(U).T + L * eps * (np.abs(c) @ np.abs(U).T)
+        for j in range(S):
+            wg, wu = ws13[j][:HS], ws13[j][HS:]
+            g, u = x @ wg.T, x @ wu.T
+            dg, du = D * eps * (np.abs(x) @ np.abs(wg).T), D * eps * (np.abs(x) @ np.abs(wu).T)
+            silu = g / (1 + np.exp(-g))
+            h = silu * u
+            # as for the experts' hidden values above; then the rounding to act
+            dh = np.abs(u) * (1.1 * dg + np.abs(silu) * (np.abs(g) + 4) * 2.0 ** -23) + np.abs(silu) * du + dg * du
+            dh += (half + 2.0 ** -22) * np.abs(h)
+            want += h @ ws2[j].T
+            tol += dh @ np.abs(ws2[j]).T + HS * eps * (np.abs(h) @ np.abs(ws2[j]).T)
+        tol = tol + half * (np.abs(want) + tol)
+        got = _f64(lay.out[s])
+        assert (np.abs(got - want) <= tol * (1 + 1e-9)).all(), (s, float((np.abs(got - want) - tol).max()))
+        # the tolerance tells a wrong layer from a right one
+        assert np.sqrt(np.mean(tol ** 2)) < 0.3 * np.sqrt(np.mean(want ** 2))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("name", ["mini_bf16", "mini_bf16_longk", 1])
+def test_how_far_four_bits_move_the_returned_rows(name):
+    """A value of a normally distributed block is off by an eighth of its RMS, give or take (codes a quarter to a half apart
+    in relative size).  Gate and up: two quantised operands, sqrt(2) / 8 = 0.18; silu(gate) up: both, sqrt(1.2^2 + 1) 0.18 =
+    0.28; the hidden row and W2 quantised: sqrt(0.28^2 + 2 / 8^2) = 0.33 of a returned row's RMS.  Half and 1.5 times that
+    bound it."""
+    from grouped_expert_ffn_router_amd import runner
+    sh, inp, lay, *_ = _layer(runner.AllRanksLayer, name, "fused")
+    ref = runner.AllRanksLayer(sh, inp)
+    ref.run()
+    torch.cuda.synchronize()
+    assert torch.equal(ref.slot_of, lay.slot_of)
+    a, b = lay.ret.double(), ref.ret.double()
+    off = float((a - b).square().mean().sqrt() / b.square().mean().sqrt())
+    assert 0.165 <= off <= 0.5, off
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("gather,ragged_banks,live_waves", [("fused", True, 2), ("buffer", True, 1), ("fused", False, 0)])
+def test_ragged_one_rank_layer(gather, ragged_banks, live_waves):
+    """One rank with the dropless ragged exchange: the output bits of the fixed-pool layer whose capacities fit the same
+    counts, on one stream and on two."""
+    from dataclasses import replace
+    from grouped_expert_ffn_router_amd import runner
+    sh = replace(configs.get("mini_bf16"), emulate_all_ranks=False)
+    inp = gen.generate(sh, seed=4, send_cap=B.capacity(B.make_dims(sh))[0])
+    drawn = {s: inp["sources"](s) for s in range(sh.n_ranks)}
+    probe = runner.RaggedOneRankLayer(replace(sh, layer="dispatch"), dict(inp, sources=drawn.__getitem__),
+                                      expert_rows=sh.n_ranks * sh.tokens)
+    probe.run()
+    rep = probe.drop_report()
+    pool_rows = max(max(rep["send_demand"]), max(probe.source_demand.values()))
+    expert_rows = max(rep["expert_arrivals"])
+    fit = configs.exact_fit(sh, pool_rows, expert_rows)
+    inp = gen.generate(fit, seed=4, send_cap=pool_rows)
+    inp["sources"] = drawn.__getitem__
+    fixed = runner.OneRankLayer(fit, inp, gather="fused", experts="mx")
+    fixed.run()
+    lay = runner.RaggedOneRankLayer(sh, inp, expert_rows, gather=gather, ragged_banks=ragged_banks, live_waves=live_waves,
+                                    experts="mx")
+    lay.run()
+    torch.cuda.synchronize()
+    assert isinstance(lay.w13, runner.MxRows) and (lay.wave_rows > 0) == ragged_banks
+    assert lay.drop_report()["recv_dropped"] == 0 and fixed.drop_report()["recv_dropped"] == 0
+    assert torch.isfinite(lay.out.float()).all() and float(lay.out.float().abs().sum()) > 0
+    assert torch.equal(lay.out, fixed.out)
+    lay.out.zero_()
+    lay.run(side=torch.cuda.Stream())
+    torch.cuda.synchronize()
+    assert torch.equal(lay.out, fixed.out)
