@@ -264,16 +264,21 @@ class OneRankLayer:
     def memory(self):
         """Device bytes of one step's buffers.  The SwiGLU hidden rows of a wave
         ([X/W][recv_cap][H] activations) are the part of the receive bank that
-        the waves keep small; the workspace holds live_waves such blocks."""
+        the waves keep small; the workspace holds live_waves such blocks (with
+        MX-FP4 experts the MX workspace does, as MX-FP4 rows)."""
         sh = self.shape
         rows = getattr(self, "wave_rows", 0) or (sh.local_experts // sh.waves) * self.rcap
         hidden_wave = rows * sh.expert_hidden * self.esize if self.full else 0
+        ws_mx = self.ws_mx if self.full else None
+        if ws_mx is not None:
+            hidden_wave = rows * sum(_mx_strides(sh.expert_hidden))
         exch = self.send_pools.numel() + self.recv_pools.numel()
         ret = (self.ret_send.numel() + self.ret_recv.numel()) * self.esize if self.full else 0
         return {"live_waves": self.live_waves, "hidden_rows_per_wave_bytes": hidden_wave,
                 "hidden_rows_live_bytes": hidden_wave * self.live_waves, "workspace_bytes": self.ws.numel(),
                 "wave_buffer_bytes": 0 if self.wave_buf is None else self.wave_buf.numel() * self.esize,
-                "exchange_pool_bytes": exch, "return_row_bytes": ret}
+                "exchange_pool_bytes": exch, "return_row_bytes": ret,
+                **({} if ws_mx is None else {"mx_workspace_bytes": ws_mx.numel()})}
 
 
 class RaggedOneRankLayer(OneRankLayer):
@@ -426,10 +431,11 @@ class RaggedOneRankLayer(OneRankLayer):
                   self.ws2, self.out, self.ws, stream)
 
     def footprint(self):
-        """Bytes of the exchange buffers and the workspace."""
+        """Bytes of the exchange buffers and the workspaces."""
         n = self.send_rows.numel() + self.recv_pools.numel() + self.ws.numel()
         if self.full:
             n += (self.ret_send.numel() + self.ret_back.numel()) * self.esize
+            n += 0 if self.ws_mx is None else self.ws_mx.numel()
         return n
 
 

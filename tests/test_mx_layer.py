@@ -327,3 +327,24 @@ def test_ragged_one_rank_layer(gather, ragged_banks, live_waves):
     lay.run(side=torch.cuda.Stream())
     torch.cuda.synchronize()
     assert torch.equal(lay.out, fixed.out)
+
+
+@pytest.mark.gpu
+def test_memory_counts_the_mx_workspace():
+    """memory() and footprint() of a layer with MX-FP4 experts: hidden rows of H / 2 + 16 bytes (H = 128) in the workspace of
+    the MX-FP4 products, which is counted."""
+    from dataclasses import replace
+    from grouped_expert_ffn_router_amd import runner
+    sh = replace(configs.get("mini_bf16"), emulate_all_ranks=False)
+    scap, rcap, _ = B.capacity(B.make_dims(sh))
+    inp = gen.generate(sh, seed=3, send_cap=scap)
+    act, mx = (runner.OneRankLayer(sh, inp, experts=e, live_waves=2) for e in ("act", "mx"))
+    a, b = act.memory(), mx.memory()
+    assert a["hidden_rows_per_wave_bytes"] == 2 * rcap * 128 * 2 and "mx_workspace_bytes" not in a
+    assert b["hidden_rows_per_wave_bytes"] == 2 * rcap * (64 + 16)
+    assert b["hidden_rows_live_bytes"] == 2 * b["hidden_rows_per_wave_bytes"]
+    assert b["mx_workspace_bytes"] == B.mx_workspace_size(mx.dims) > b["hidden_rows_live_bytes"]
+    drawn = {s: inp["sources"](s) for s in range(sh.n_ranks)}
+    inp = dict(gen.generate(sh, seed=3, send_cap=sh.tokens * sh.top_k), sources=drawn.__getitem__)
+    act, mx = (runner.RaggedOneRankLayer(sh, inp, 2 * rcap, experts=e) for e in ("act", "mx"))
+    assert mx.footprint() == act.footprint() + B.mx_workspace_size(mx.recv_dims)
