@@ -24,6 +24,7 @@ Options: --steps K --warmup W --config {2,3,4,5,6} --gather {fused,buffer} --str
 --dropless (capacities fitted to the exchanged counts against the fixed factors),
 --vendor-gemm (torch's bf16 matmul on the layer's GEMM shapes, a reference point for the GEMM core)
 --graph (the step captured once as a HIP graph, its replays timed)
+--experts mx (the routed experts as MX-FP4 rows; the other weights as they are)
 --no-cpu-baseline --cpu-tokens N --seed S.  --gpus N > 1 exits: the benchmark
 measures one GPU.
 """
@@ -43,10 +44,14 @@ if ROOT not in sys.path:
 
 METRIC = "routed token-assignments/s per GPU (dispatch+expert+combine); HBM GB/s, MFMA %"
 PEAK_MFMA_BF16_TFLOPS = 2500.0   # MI355X dense bf16 MFMA
+PEAK_MFMA_FP4_TFLOPS = 10000.0   # MI355X dense MX-FP4 MFMA
 PEAK_HBM_GBS = 8000.0            # MI355X HBM3E
 SOURCES = ["grouped_expert_ffn_router_amd/csrc/api.hip", "grouped_expert_ffn_router_amd/csrc/kernels.hip",
            "grouped_expert_ffn_router_amd/csrc/gemm.h", "grouped_expert_ffn_router_amd/csrc/moe_common.h",
            "grouped_expert_ffn_router_amd/csrc/moe_internal.h"]
+# what the MX-FP4 operators and the few-token layer are built from (they include headers of the above)
+OPERATOR_SOURCES = ["grouped_expert_ffn_router_amd/csrc/ops/" + f
+                    for f in ("entry.hip", "few.h", "few.hip", "mx.h", "mx.hip")] + SOURCES[2:]
 
 
 def parse():
@@ -66,6 +71,9 @@ def parse():
                          "1: one wave live at a time, waves in order; 0: all waves")
     ap.add_argument("--graph", action="store_true",
                     help="capture one step (both streams) as a HIP graph after the warm-up and time its replays")
+    ap.add_argument("--experts", choices=["act", "mx"], default="act",
+                    help="act: the routed experts in the layer's type; mx: as MX-FP4 rows, which the tokens' rows and "
+                         "hidden rows then are too (no CPU baseline: the oracle's experts are in the layer's type)")
     ap.add_argument("--cpu-runs", type=int, default=0,
                     help="timed runs of the CPU oracle (the median is reported); 0: 3, or 1 for 65,536 tokens")
     ap.add_argument("--no-cpu-baseline", action="store_true")
@@ -83,15 +91,22 @@ def parse():
                     help="instead of the benchmark line: torch's bf16 matmul (the vendor GEMM library) on the "
                          "layer's GEMM shapes with N(0,1) operands, one JSON line per shape (a reference point "
                          "for the GEMM core, to be profiled with the same counters)")
-    return ap.parse_args()
+    args = ap.parse_args()
+    if args.experts == "mx" and (args.sweep_capacity or args.dropless or args.vendor_gemm):
+        ap.error("--experts mx goes with the benchmark line only")
+    return args
 
 
-def source_digest():
+def source_digest(sources=None):
     h = hashlib.sha256()
-    for p in SOURCES:
+    for p in sources or SOURCES:
         with open(os.path.join(ROOT, p), "rb") as f:
             h.update(f.read())
     return h.hexdigest()[:16]
+
+
+def flop_peak(kernel):
+    return PEAK_MFMA_FP4_TFLOPS if kernel.startswith("mx_") else PEAK_MFMA_BF16_TFLOPS
 
 
 def committed_traffic(kernel, workload):
@@ -127,6 +142,10 @@ def algorithmic_work(sh, kept_rows_per_wave, send_kept, send_cap):
         "route_gemm": ("flop", 2.0 * T * (E + L) * D),
         "expert_gate_up": ("flop", 2.0 * rows * 2 * H * L),
         "expert_down": ("flop", 2.0 * rows * L * H),
+        # MX-FP4 experts: the same products; the gather reads a row and writes it in 17 / 32 of a byte a value
+        "mx_gate_up": ("flop", 2.0 * rows * 2 * H * L),
+        "mx_down": ("flop", 2.0 * rows * L * H),
+        "mx_gather": ("byte", rows * (L * es + L * 17 / 32 + 4)),
         "shared_gate_up": ("flop", 2.0 * T * 2 * S * HS * D),
         "up_shared_down": ("flop", 2.0 * T * D * (L + S * HS)),
         # read z once, write each kept row (payload + id), ids of empty slots,
@@ -419,11 +438,13 @@ def main():
     from grouped_expert_ffn_router_amd import binding, runner
 
     sh = configs.get(args.config)
+    if args.experts == "mx" and sh.layer != "full":
+        raise SystemExit("--experts mx needs a workload with experts (configs 3, 5, 6)")
     dev = "cuda:0"
     torch.cuda.set_device(0)
     scap, rcap, _ = binding.capacity(binding.make_dims(sh))
     inp = gen.generate(sh, seed=args.seed, send_cap=scap)
-    lay = runner.OneRankLayer(sh, inp, device=dev, gather=args.gather, live_waves=args.live_waves)
+    lay = runner.OneRankLayer(sh, inp, device=dev, gather=args.gather, live_waves=args.live_waves, experts=args.experts)
     del inp
     stream = torch.cuda.current_stream()
     full = sh.layer == "full"
@@ -496,7 +517,7 @@ def main():
             kind, amount = work[name]
             if kind == "flop":
                 ach = amount / (avg * 1e-3) / 1e12
-                ent.update(unit="TFLOP/s", achieved=ach, frac=ach / PEAK_MFMA_BF16_TFLOPS)
+                ent.update(unit="TFLOP/s", achieved=ach, frac=ach / flop_peak(name))
             else:
                 ach = amount / (avg * 1e-3) / 1e9
                 ent.update(unit="GB/s", achieved=ach, frac=ach / PEAK_HBM_GBS)
@@ -511,27 +532,30 @@ def main():
                     "max": float(np.max(step_ms))},
         "kept_assignments_per_s": rep["send_kept"] / (ms * 1e-3),
         "higher_is_better": True,
-        "scaling": "weak", "vs_baseline": None, "dtype": "bf16" if sh.act == "bf16" else "f32",
+        "scaling": "weak", "vs_baseline": None, "dtype": ("bf16" if sh.act == "bf16" else "f32")
+        + (", routed experts' products in MX-FP4" if args.experts == "mx" else ""),
         "data": "synthetic (seeded; shapes of the pages' 4K-context expert layer)",
         "config": {"workload": sh.name, "tokens_per_rank": T, "d_model": sh.d_model, "latent": sh.latent,
                    "experts": sh.n_experts, "top_k": k, "ep_ranks": sh.n_ranks, "local_experts": sh.local_experts,
                    "waves": sh.waves, "expert_hidden": sh.expert_hidden, "shared_experts": sh.shared_experts,
                    "shared_hidden": sh.shared_hidden, "send_cap": scap, "recv_cap": rcap, "gather": args.gather,
                    "live_waves": lay.live_waves, "streams": args.streams if full else 1, "hip_graph": args.graph,
+                   **({"routed_experts": "MX-FP4"} if args.experts == "mx" else {}),
                    "parallelism": "one EP rank of 64 (the other ranks' pools and returns are inputs)"},
     }
     if kind is not None:
         traffic = committed_traffic(dom, sh.name)
-        ceiling = rates["vendor_bf16_gemm_8192_TFLOPs"] if kind == "flop" else rates["device_copy_GBs"]
+        ceiling = (rates["vendor_bf16_gemm_8192_TFLOPs"] * flop_peak(dom) / PEAK_MFMA_BF16_TFLOPS if kind == "flop"
+                   else rates["device_copy_GBs"])
         out["roofline"] = {"bound": "mfma" if kind == "flop" else "hbm", "achieved": d["achieved"],
-                           "peak": PEAK_MFMA_BF16_TFLOPS if kind == "flop" else PEAK_HBM_GBS, "unit": d["unit"],
+                           "peak": flop_peak(dom) if kind == "flop" else PEAK_HBM_GBS, "unit": d["unit"],
                            "frac": d["frac"], "traffic": traffic, "kernel": dom, "avg_ms": d["avg_ms"],
                            "work_per_launch": work[dom][1], "work_unit": kind,
                            "measured_ceiling": ceiling, "frac_of_measured_ceiling": d["achieved"] / ceiling}
     for name, ent in kernels.items():
         if ent.get("unit") == "GB/s":
             ent["frac_of_device_copy"] = ent["achieved"] / rates["device_copy_GBs"]
-        elif ent.get("unit") == "TFLOP/s":
+        elif ent.get("unit") == "TFLOP/s" and not name.startswith("mx_"):
             ent["frac_of_vendor_gemm"] = ent["achieved"] / rates["vendor_bf16_gemm_8192_TFLOPs"]
     out["kernels"] = kernels
     out["reference_rates"] = rates
@@ -539,7 +563,9 @@ def main():
     out["drops"] = {"send_dropped": rep["send_dropped"], "recv_dropped": rep["recv_dropped"],
                     "send_kept": rep["send_kept"], "recv_kept": rep["recv_kept"]}
     out["source_digest"] = source_digest()
-    if not args.no_cpu_baseline:
+    if args.experts == "mx":
+        out["operator_source_digest"] = source_digest(OPERATOR_SOURCES)
+    if not args.no_cpu_baseline and args.experts == "act":
         ctok = min(args.cpu_tokens, sh.tokens) if args.cpu_tokens else sh.tokens
         runs = args.cpu_runs if args.cpu_runs else (1 if ctok >= 65536 else 3)
         out["cpu_baseline"] = cpu_baseline(args.config, args.seed, ctok, runs)
