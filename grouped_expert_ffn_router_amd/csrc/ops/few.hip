@@ -34,7 +34,7 @@ namespace moe {
 
 namespace {
 
-constexpr int FEW_CUS = 256;  // what the split of the down product is sized for (the workspace's size depends on it)
+constexpr int FEW_CUS = 256;  // what the products' splits are sized for (the workspace's size depends on it)
 constexpr int NW = 8;       // waves of a workgroup
 constexpr int NTHREADS = NW * 64;
 
@@ -913,16 +913,12 @@ hipError_t launch_few_up(const FewArgs& a, hipStream_t st) {
       constexpr int RT = decltype(rt)::value;
       launch((few_up<decltype(t), RT, decltype(nt)::value>), dim3((unsigned)tiles_of(a.d.D, 16 * RT)), dim3(NTHREADS), 0, st, a);
     };
-    // two row tiles share each read of the tokens' rows where those are much
-    // of the traffic (they come in two parts); with few tokens one, for more
-    // workgroups.  6144 x 5120, 16 tokens: 26 us with two, 37 with one; 64:
-    // 53 and 94; one token: 20 with one.
-    if constexpr (decltype(nt)::value > 1) {
-      go(std::integral_constant<int, 2>());
-    } else {
-      if (a.d.T > 8) go(std::integral_constant<int, 2>());
-      else go(std::integral_constant<int, 1>());
-    }
+    // One row tile a workgroup while every CU has at most one of those, else two, which share each read of the tokens'
+    // rows (two parts of 16 bits a value), but for one or two tokens, whose rows are little.  One and two tiles, bf16:
+    // 4096 wide, 8 tokens 10.6 and 14.0 us, 64 tokens 28.9 and 32.4; 6144 wide, one token 20.1 and 20.3, 4 tokens 23.5 and
+    // 20.9, 16: 36.6 and 26.1, 64: 87.6 and 52.3; fp32, 4096 wide, 64 tokens 35.2 and 49.2, 6144 wide 108 and 81.
+    if (tiles_of(a.d.D, 16) > FEW_CUS && a.d.T > 2) go(std::integral_constant<int, 2>());
+    else go(std::integral_constant<int, 1>());
   });
 }
 

@@ -701,3 +701,19 @@ def test_forms_of_large_layers(T, E, k, L, H, act, mx, forms):
     _check(got, w, x, k, act, bias)
     again = lay(x)
     assert all(torch.equal(a, b) for a, b in zip(got, again))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("T", [2, 3, 16, 17, 40, 64])
+@pytest.mark.parametrize("D,act", [(4096, "bf16"), (4160, "bf16"), (4096, "f32"), (4099, "f32")])
+def test_row_tiles_of_the_last_product(D, act, T):
+    """Output widths whose tiles of 16 rows are 256 and more: a tile a workgroup, or two with more than two tokens.  The
+    width 4099 ends inside the first tile of a pair."""
+    from grouped_expert_ffn_router_amd import runner
+    w, g, dt = _weights(T, 6, D, 64, 64, 2, 64, act)
+    x = torch.randn((T, D), generator=g, device="cuda").to(dt)
+    lay = runner.FewTokenLayer(**w, top_k=2)
+    guard = torch.full((T * D + 64,), 5.0, dtype=dt, device="cuda")
+    got = lay(x, out=guard[:T * D].view(T, D))
+    _check(got, w, x, 2, act)
+    assert (guard[T * D:] == 5).all()
