@@ -13,9 +13,9 @@
 //   down     c = sum over the chosen experts of w (h W2^T)
 //   up       out = c U^T + sum hs W2s^T
 // MI355X, model width 6144, latent 2048, 8 of 384 experts of 1536 and two
-// shared ones: one token 95 us (319 MB: 3.4 TB/s), 64 tokens 0.96 ms (5.5 GB:
-// 5.8 TB/s), 16 tokens with MX-FP4 experts 215 us (0.72 GB: 3.3 TB/s); a small
-// layer (512 wide, one token) 20 us.  What bounds the small ones is the five
+// shared ones: one token 95 us (319 MB: 3.4 TB/s), 64 tokens 0.91 - 0.94 ms (5.5
+// GB: 5.9 TB/s), 16 tokens with MX-FP4 experts 214 us (0.72 GB: 3.4 TB/s); a small
+// layer (512 wide, one token) 23 us.  What bounds the small ones is the five
 // round trips to memory, 2 us and more each with cold caches, and launching.
 // One launch for all after the projections (a queue of items in order of
 // dependency, device-scope counters and waits between them) was built and

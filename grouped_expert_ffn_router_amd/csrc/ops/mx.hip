@@ -240,7 +240,9 @@ struct MxARows {  // rows of group g: bank rows g * group_rows .., or end to end
 // Tile of workgroup `bid`: the tiles of the rows that exist, group by group and
 // 4 tile rows at a time inside a group, in 8 contiguous ranges, one for each
 // XCD (workgroups go round-robin to the XCDs), so that an XCD's L2 sees
-// neighbouring tiles.  False: none is left.
+// neighbouring tiles.  False: none is left.  Every workgroup goes through the
+// groups' rows twice, one after the other: groups of 128 rows x 128 x 512 take
+// 5.8 us for 8 of them and 14 for 64, but 74 for 384 and 5.3 ms for 4096.
 template <int BM>
 __device__ __forceinline__ bool mx_tile_of(const MxARows& a, int groups, int tiles_n, int bid, int& g, int& tm, int& tn) {
   int total = 0;
@@ -314,8 +316,11 @@ __device__ __forceinline__ i32x8 mx_operand(i32x4 v) { return __builtin_shufflev
 // a 512-piece are one 16-byte load, whose dword j holds the scales of MFMA j.
 // The last piece may end early: codes past the row are read from its last
 // block, and their scales are 0 on both sides (2^-254: nothing in fp32).
-// 64 x 4096 x 6144 takes 11 us, one row x 6144 x 2048 4.4: the bytes are 2.9 and
-// 1.4 us, the rest is one launch and one trip to memory and back.
+// One row x 6144 x 2048 takes 4.4 us, one row x 4096 x 6144 4.8: the bytes are
+// 1.4 and 2.8 us, the rest is one launch and one trip to memory and back.  More
+// rows: 16 x 4096 x 6144 5.9 us, 32 7.6, 48 9.6, 64 10.8 (the bytes 2.9 us).
+// Each workgroup reads all rows of A for its 16 columns, 1.6 us for each 16 rows
+// of A (64 rows: 209 KB a workgroup, 53 MB in all out of the L2s).
 template <int MT, int NW, class T>
 __global__ void __launch_bounds__(NW * 64)
 mx_gemm_rows(MxARows a, MxBRows b, EMxOut<T> e, int N, int K) {
@@ -408,10 +413,10 @@ mx_gemm_rows(MxARows a, MxBRows b, EMxOut<T> e, int N, int K) {
 // two such workgroups share a CU.
 //
 // MI355X: 8192 x 6144 x 6144 in 160 us, 3.86 PFLOP/s (2.8 times the rate of a
-// large bf16 library product on the card), the matrix units busy 44 % of the
-// cycles at 2.0 GHz; the same MFMAs with nothing else in the loop take 0.72 of
-// the time, at a clock the power limit sets.  Half of the rest is the loads, half
-// the LDS reads.  Slower here: 4 waves of 128 x 128 (two thirds of the LDS reads,
+// large bf16 library product on the card), the matrix units busy half of the
+// cycles.  The same MFMAs with nothing else in the loop take 0.72 of the time, at
+// a clock the power limit sets; half of the other 0.28 is the loads, half the LDS
+// reads.  Slower here: 4 waves of 128 x 128 (two thirds of the LDS reads,
 // but one wave a SIMD has nothing to hide its address arithmetic behind), and a
 // ring of four 64-byte-deep buffers with counted waits (187 us against 166).
 template <int B_>
@@ -751,8 +756,11 @@ hipError_t run_mx_tiles(const MxARows& a, const B& b, const E& e, int N, int K, 
 // Rounds of the card's CUs that the tiles take: one workgroup of 256 x 256 a
 // CU, or two of 128 x 128, which together take MX_SMALL_ROUND of a large
 // tile's time for half of its work.  Measured, large and small tiles:
-// 1024 x 4096 x 4096 27 and 17 us, 2048 x 4096 x 4096 30 and 26,
-// 4096 x 4096 x 4096 40 and 49, 8192 x 6144 x 6144 170 and 217.
+// 1024 x 4096 x 4096 26 and 17 us, 2048 x 4096 x 4096 29 and 24,
+// 4096 x 4096 x 4096 40 and 47, 8192 x 6144 x 6144 167 and 210; with rows of 512
+// values 10.0 and 7.5, 11.7 and 10.5, 14.5 and 15.2 us (8192 x 6144: 34 and 36).
+// 3000 x 3100 x 512, 2048 and 6144: 15.6 and 17.3, 23.9 and 27.1, 45 and 57.
+// The rows are max_rows, as the launch does not know the counts.
 constexpr double MX_SMALL_ROUND = 0.65;
 
 template <bool GATEUP, class B, class E>
