@@ -757,6 +757,9 @@ class MxRows:
         self.code_stride, self.scale_stride = _row_stride(codes, "codes"), _row_stride(scales, "scales")
         self._at, self._arg = (codes.data_ptr(), scales.data_ptr()), None
 
+    def __getstate__(self):
+        return {**self.__dict__, "_arg": None}   # ctypes pointers do not go into copies
+
     def _where(self):
         """The tensors' addresses now; memory put in their place since the last call is checked first."""
         at = (self.codes.data_ptr(), self.scales.data_ptr())
@@ -879,11 +882,25 @@ class FewTokenLayer:
         self.dims = B.Dims(tokens=B.MOE_FEW_TOKENS_MAX, d_model=D, latent=L, n_experts=E, top_k=top_k, n_ranks=n_ranks,
                            waves=1, expert_hidden=H, shared_experts=S, shared_hidden=HS, my_rank=rank,
                            act_dtype=_DTYPE[dt], send_num=1, send_den=1, recv_num=1, recv_den=1)
+        self._prepare()
+
+    def _prepare(self):
+        """What a layer object has to itself, beside its weights and sizes."""
+        dev = self.w_router.device
         self._by_tokens = {}   # the dims of each batch size met; self.dims are those of the largest
         self.ws = torch.empty((B.few_workspace_size(self.dims),), dtype=torch.uint8, device=dev)
         self._ws_stream = _on(self.ws)[0] if dev.type == "cuda" else None
         self._ws_lock = threading.Lock()   # a call launches several kernels: those of two threads must not mix
         self._at = self._addresses()
+
+    def __getstate__(self):
+        own = ("_by_tokens", "ws", "_ws_stream", "_ws_lock", "_at")
+        return {k: v for k, v in self.__dict__.items() if k not in own}
+
+    def __setstate__(self, state):
+        self.__dict__.update(state)
+        self._made_of = self._sizes()
+        self._prepare()
 
     def _sizes(self):
         """Checks the weights and gives what a call takes for granted of them."""

@@ -717,3 +717,32 @@ def test_row_tiles_of_the_last_product(D, act, T):
     got = lay(x, out=guard[:T * D].view(T, D))
     _check(got, w, x, 2, act)
     assert (guard[T * D:] == 5).all()
+
+
+# ---------------------------------------------------------------- copies
+
+@pytest.mark.parametrize("mx", [False, True])
+def test_a_copied_layer_serves_its_own_weights(monkeypatch, mx):
+    """copy.deepcopy and pickle give a layer of its own: its weights' addresses, its workspace, its lock."""
+    import copy
+    import pickle
+    from grouped_expert_ffn_router_amd import runner
+    seen = []
+    z = lambda *s: torch.zeros(s, dtype=torch.bfloat16)  # noqa: E731
+    rows = lambda *s: runner.MxRows(torch.zeros(s[:-1] + (s[-1] // 2,), dtype=torch.uint8),  # noqa: E731
+                                    torch.zeros(s[:-1] + (16,), dtype=torch.uint8), s[-1]) if mx else z(*s)
+    lay = _cpu_layer(monkeypatch, lambda *a: seen.append(a), lambda: 7, w_router=z(6, 64), w_down=z(128, 64),
+                     w13=rows(6, 128, 128), w2=rows(6, 128, 64), w_up=z(64, 128))
+    lay(z(3, 64))
+    if mx:
+        assert lay.w13.arg.codes == lay.w13.codes.data_ptr()
+    for twin in (copy.deepcopy(lay), pickle.loads(pickle.dumps(lay))):
+        twin(z(3, 64))
+        tensor = lambda t: t.codes if mx else t  # noqa: E731
+        for i, name in ((2, "w_router"), (3, "w_down"), (6, "w13"), (8, "w2"), (10, "w_up")):
+            mine, other = (tensor(getattr(x, name)) if name in ("w13", "w2") else getattr(x, name) for x in (twin, lay))
+            assert seen[-1][i] == mine.data_ptr() != other.data_ptr()
+        assert twin.ws.data_ptr() != lay.ws.data_ptr() and twin.ws.numel() == lay.ws.numel()
+        assert twin.dims.latent == 128 and twin.dims is not lay.dims and twin._ws_lock is not lay._ws_lock
+        if mx:
+            assert twin.w13.arg.codes == twin.w13.codes.data_ptr()
