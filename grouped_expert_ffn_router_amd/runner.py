@@ -92,7 +92,8 @@ def _expert_gemm(dims, wave, wave_buf, pools, src_stride, row_src, wave_count, w
 class OneRankLayer:
     """One EP rank's layer.  ``inp`` is a workload.gen.generate() dict.
     experts="mx" quantises the routed experts to MX-FP4 rows and runs their
-    products on them (moe_mx_expert_gemm)."""
+    products on them (moe_mx_expert_gemm), which rounds the tokens' rows and
+    the hidden rows to 4 bits too."""
 
     def __init__(self, shape, inp, device="cuda", gather="fused", keep_source_logits=False, live_waves=0,
                  experts="act"):
@@ -851,7 +852,11 @@ def mx_gemm(a, b, counts=None, out=None, dtype=torch.bfloat16):
 class FewTokenLayer:
     """A whole layer for up to 64 tokens at a time on one GPU (moe_few_tokens), as a
     decode step runs it: __call__(x [T, D]) -> (out [T, D], topk_idx [T, k] int32,
-    topk_w [T, k] fp32).
+    topk_w [T, k] fp32).  Forward only.  Weights, x and out start 16-byte aligned.
+
+    Activations keep two bf16 parts (2^-17) with bf16 and MX-FP4 weights; the wave
+    path's MX-FP4 products (experts="mx" above) round them to 4 bits, so the two differ
+    by that on the same weights.
 
     w_router [E, D], w_down [L, D], w_up [D, L], ws13 [S, 2 HS, D], ws2 [S, D, HS]
     are bf16 or fp32, as x; the routed experts w13 [X, 2H, L] and w2 [X, L, H] too,

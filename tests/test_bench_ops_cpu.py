@@ -45,3 +45,12 @@ def test_mx_experts_go_with_the_benchmark_line_only(args):
     r = subprocess.run([sys.executable, os.path.join(ROOT, "bench.py"), "--experts", "mx", *args], stdout=subprocess.PIPE,
                        stderr=subprocess.PIPE, text=True, timeout=300, cwd=ROOT)
     assert r.returncode != 0 and "--experts mx" in r.stderr
+
+
+def test_committed_operator_profiles_are_of_the_current_sources():
+    """Kernel times and counters of the operators, and of the layer with MX-FP4 experts, carry the digest of the sources
+    they were taken from."""
+    names = [f for f in os.listdir(os.path.join(ROOT, "profiles")) if f.startswith("operators_")]
+    assert {"operators_kernels_trace.md", "operators_pmc.md", "operators_mx_layer_cfg3_full_layer_4k.md"} <= set(names)
+    for f in names:
+        assert bench.source_digest(bench.OPERATOR_SOURCES) in open(os.path.join(ROOT, "profiles", f)).read(), f
