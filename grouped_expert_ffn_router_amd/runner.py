@@ -733,20 +733,36 @@ class MxRows:
     codes [..., rows, cols / 2] and scales [..., rows, cols / 32 rounded up to 16], uint8."""
 
     def __init__(self, codes, scales, cols):
-        self.codes, self.scales, self.cols = codes, scales, cols
+        self._codes, self._scales, self.cols = codes, scales, cols
         self._layout()
 
     @classmethod
     def _made(cls, codes, scales, cols, code_stride, scale_stride, at):
         """From contiguous tensors made here, which are at the addresses `at`."""
         q = cls.__new__(cls)
-        q.codes, q.scales, q.cols = codes, scales, cols
+        q._codes, q._scales, q.cols = codes, scales, cols
         q.code_stride, q.scale_stride, q._at, q._arg = code_stride, scale_stride, at, None
         return q
 
+    @property
+    def codes(self):
+        return self._codes
+
+    @codes.setter
+    def codes(self, t):
+        self._codes, self._at = t, None   # checked at the next use
+
+    @property
+    def scales(self):
+        return self._scales
+
+    @scales.setter
+    def scales(self, t):
+        self._scales, self._at = t, None
+
     def _layout(self):
         """Checks the tensors and takes their strides."""
-        codes, scales = self.codes, self.scales
+        codes, scales = self._codes, self._scales
         cb, sb = _mx_strides(self.cols)
         if codes.dtype != torch.uint8 or scales.dtype != torch.uint8:
             raise TypeError("codes and scales are uint8")
@@ -763,7 +779,7 @@ class MxRows:
 
     def _where(self):
         """The tensors' addresses now; memory put in their place since the last call is checked first."""
-        at = (self.codes.data_ptr(), self.scales.data_ptr())
+        at = (self._codes.data_ptr(), self._scales.data_ptr())
         if at != self._at:
             self._layout()
         return at
@@ -771,10 +787,10 @@ class MxRows:
     @property
     def arg(self):
         """moe_mx_rows of the tensors as they are now."""
-        at = self._where()
-        if self._arg is None:
-            self._arg = B.MxRowsArg(at[0], at[1], self.code_stride, self.scale_stride)
-        return self._arg
+        at, arg = self._where(), self._arg
+        if arg is None:
+            arg = self._arg = B.MxRowsArg(at[0], at[1], self.code_stride, self.scale_stride)
+        return arg
 
     @property
     def shape(self):
@@ -897,6 +913,11 @@ class FewTokenLayer:
         self._ws_stream = _on(self.ws)[0] if dev.type == "cuda" else None
         self._ws_lock = threading.Lock()   # a call launches several kernels: those of two threads must not mix
         self._at = self._addresses()
+
+    def __setattr__(self, name, value):
+        object.__setattr__(self, name, value)
+        if name in ("w_router", "w_down", "w13", "w2", "w_up", "ws13", "ws2", "bias", "bias_row_tokens", "n_ranks"):
+            self.__dict__["_at"] = None   # checked at the next call, which the address alone might not ask for
 
     def __getstate__(self):
         own = ("_by_tokens", "ws", "_ws_stream", "_ws_lock", "_at")

@@ -746,3 +746,46 @@ def test_a_copied_layer_serves_its_own_weights(monkeypatch, mx):
         assert twin.dims.latent == 128 and twin.dims is not lay.dims and twin._ws_lock is not lay._ws_lock
         if mx:
             assert twin.w13.arg.codes == twin.w13.codes.data_ptr()
+
+
+# ---------------------------------------------------------------- other tensors at the same address
+
+def test_attributes_set_to_other_views_are_checked(monkeypatch):
+    """A view that begins where the old tensor did has the old address; its shape and strides count all the same."""
+    from grouped_expert_ffn_router_amd import runner
+    seen = []
+    z = lambda *s: torch.zeros(s, dtype=torch.bfloat16)  # noqa: E731
+    lay = _cpu_layer(monkeypatch, lambda *a: seen.append(a), lambda: 7, w_router=z(6, 64), w_down=z(128, 64),
+                     w13=z(6, 128, 128), w2=z(6, 128, 64), w_up=z(64, 128))
+    lay(z(3, 64))
+    for name in ("w_router", "w_down", "w13", "w2", "w_up"):
+        old = getattr(lay, name)
+        for new in (old[:3], old[..., :32], old.transpose(-1, -2)):
+            setattr(lay, name, new)
+            with pytest.raises(ValueError):
+                lay(z(3, 64))
+        setattr(lay, name, old)
+        lay(z(3, 64))
+    assert len(seen) == 6
+    u8 = lambda *s: torch.zeros(s, dtype=torch.uint8)  # noqa: E731
+    q = runner.MxRows(u8(4, 6, 32), u8(4, 6, 16), 64)
+    assert q.arg.code_stride_bytes == 32
+    q.codes, q.scales = q.codes[:, :5], q.scales[:, :5]
+    with pytest.raises(ValueError):      # rows 0..4, 6..10, ..: not evenly spaced
+        q.arg
+    q.codes, q.scales = u8(4, 6, 32)[:, ::2], u8(4, 6, 16)[:, ::2]
+    assert (q.arg.code_stride_bytes, q.arg.scale_stride_bytes) == (64, 32)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("act,mx", [("bf16", False), ("bf16", True), ("f32", False)])
+def test_output_in_the_place_of_the_input(act, mx):
+    """out may be x: the last product, which writes it, reads no token."""
+    from grouped_expert_ffn_router_amd import runner
+    w, g, dt = _weights(41, 12, 256, 128, 192, 2, 64, act, mx)
+    lay = runner.FewTokenLayer(**w, top_k=3)
+    for T in (1, 20):
+        x = torch.randn((T, 256), generator=g, device="cuda").to(dt)
+        want = [t.clone() for t in lay(x)]
+        got = lay(x, out=x)
+        assert got[0] is x and all(torch.equal(a, b) for a, b in zip(got, want))
