@@ -19,6 +19,8 @@ MOE_OK, MOE_EINVAL, MOE_EALIGN, MOE_EDTYPE, MOE_ECAP, MOE_EHIP = 0, -1, -2, -3, 
 MOE_ACT_BF16, MOE_ACT_F32 = 0, 1
 MOE_MAX_RANKS, MOE_MAX_LOCAL = 1024, 64
 MOE_FEW_TOKENS_MAX = 64
+MOE_SCORE_SOFTMAX, MOE_SCORE_SIGMOID = 0, 1
+MOE_NORM_COLS_MAX = 16384
 
 ENTRY_POINTS = ["moe_capacity", "moe_workspace_size", "moe_route", "moe_pack_pools", "moe_pack_pools_noalloc",
                 "moe_pack_ragged",
@@ -26,7 +28,10 @@ ENTRY_POINTS = ["moe_capacity", "moe_workspace_size", "moe_route", "moe_pack_poo
                 "moe_expert_gemm", "moe_shared_experts", "moe_combine", "moe_drop_stats", "moe_last_error", "moe_timing_enable",
                 "moe_timing_read",
                 "moe_mx_strides", "moe_mx_quantize", "moe_mx_dequantize", "moe_mx_gemm",
-                "moe_mx_workspace_size", "moe_mx_expert_gemm", "moe_few_workspace_size", "moe_few_tokens"]
+                "moe_mx_workspace_size", "moe_mx_expert_gemm", "moe_few_workspace_size", "moe_few_tokens",
+                "moe_mxb_strides", "moe_mxb_quantize", "moe_mxb_dequantize", "moe_rms_norm",
+                "moe_rms_norm_workspace_size", "moe_rms_norm_backward", "moe_select", "moe_select_backward",
+                "moe_swiglu_checkpoint", "moe_swiglu_backward"]
 
 
 class MoeError(RuntimeError):
@@ -70,11 +75,18 @@ class MxRowsArg(ctypes.Structure):
                 ("scale_stride_bytes", ctypes.c_int64)]
 
 
+class RouterRuleArg(ctypes.Structure):
+    """moe_router_rule: how experts are chosen and weighted."""
+    _fields_ = [(n, ctypes.c_int32) for n in ("score", "groups", "top_groups", "group_best", "renormalise")] + [
+        ("scale", ctypes.c_float)]
+
+
 _lib = None
 _loaded = {}
 _P = ctypes.c_void_p
 _I32 = ctypes.c_int32
 _I64 = ctypes.c_int64
+_F32 = ctypes.c_float
 
 
 def lib():
@@ -137,6 +149,17 @@ def _load(path):
     L.moe_mx_expert_gemm.argtypes = [DP, _I32, _P, _P, _I64, _P, _P, RP, RP, _P, _I64, _P, _P, _P]
     L.moe_few_workspace_size.argtypes = [DP, ctypes.POINTER(ctypes.c_size_t)]
     L.moe_few_tokens.argtypes = [DP, _P, _P, _P, _P, _I32] + [_P] * 12
+    UP = ctypes.POINTER(RouterRuleArg)
+    L.moe_mxb_strides.argtypes = [_I64, ctypes.POINTER(_I64), ctypes.POINTER(_I64)]
+    L.moe_mxb_quantize.argtypes = [_I32, _I64, _I64, _P, _I64, RP, _P]
+    L.moe_mxb_dequantize.argtypes = [_I32, _I64, _I64, RP, _P, _I64, _P]
+    L.moe_rms_norm.argtypes = [_I32, _I64, _I64, _P, _I64, _P, _I64, _P, _I32, _F32, _P, _I64, _P, _I64, RP, _P]
+    L.moe_rms_norm_workspace_size.argtypes = [_I64, _I64, ctypes.POINTER(ctypes.c_size_t)]
+    L.moe_rms_norm_backward.argtypes = [_I32, _I64, _I64, _P, _I64, _P, _I64, _P, _I32, _F32, _P, _I64, _P, _I64, _P, _P, _P]
+    L.moe_select.argtypes = [UP, _I64, _I32, _I32, _P, _I64, _P, _P, _P, _P]
+    L.moe_select_backward.argtypes = [UP, _I64, _I32, _I32, _P, _P, _P, _P, _I64, _P, _I64, _P]
+    L.moe_swiglu_checkpoint.argtypes = [_I32, _I32, _I64, _I64, _P, _I64, _P, _P, _I64, RP, _P]
+    L.moe_swiglu_backward.argtypes = [_I32, _I32, _I64, _I64, _P, _I64, RP, _P, _P, _I64, _P, _I64, _P]
     for n in ENTRY_POINTS:
         if n != "moe_last_error":
             getattr(L, n).restype = ctypes.c_int
@@ -309,6 +332,76 @@ def few_tokens(dims, x, w_router, w_down, bias, bias_row_tokens, w13, w13_scales
                                 int(bias_row_tokens), _ptr(w13), _ptr(w13_scales), _ptr(w2), _ptr(w2_scales),
                                 _ptr(w_up), _ptr(ws13), _ptr(ws2), _ptr(topk_idx), _ptr(topk_w), _ptr(out), _ptr(ws),
                                 _stream(stream)))
+
+
+def mx8_strides(cols):
+    """(code, scale) bytes of a row of `cols` MX-FP8 values."""
+    c, s = _I64(), _I64()
+    _check(lib().moe_mxb_strides(int(cols), ctypes.byref(c), ctypes.byref(s)))
+    return c.value, s.value
+
+
+def mx8_quantize(act_dtype, rows, cols, x, x_stride_bytes, out, stream=None):
+    """out: MxRowsArg (mx_rows) or None."""
+    _check(lib().moe_mxb_quantize(int(act_dtype), int(rows), int(cols), _ptr(x), int(x_stride_bytes), _ref(out),
+                                  _stream(stream)))
+
+
+def mx8_dequantize(act_dtype, rows, cols, q, out, out_stride_bytes, stream=None):
+    """q: MxRowsArg (mx_rows) or None."""
+    _check(lib().moe_mxb_dequantize(int(act_dtype), int(rows), int(cols), _ref(q), _ptr(out), int(out_stride_bytes),
+                                    _stream(stream)))
+
+
+def rms_norm(act_dtype, rows, cols, x, x_stride_bytes, residual, residual_stride_bytes, weight, weight_dtype, eps, sum_out,
+             sum_stride_bytes, y, y_stride_bytes, y8, stream=None):
+    """y8: MxRowsArg (mx_rows) or None."""
+    _check(lib().moe_rms_norm(int(act_dtype), int(rows), int(cols), _ptr(x), int(x_stride_bytes), _ptr(residual),
+                              int(residual_stride_bytes), _ptr(weight), int(weight_dtype), float(eps), _ptr(sum_out),
+                              int(sum_stride_bytes), _ptr(y), int(y_stride_bytes), _ref(y8), _stream(stream)))
+
+
+def rms_norm_workspace_size(rows, cols):
+    b = ctypes.c_size_t()
+    _check(lib().moe_rms_norm_workspace_size(int(rows), int(cols), ctypes.byref(b)))
+    return b.value
+
+
+def rms_norm_backward(act_dtype, rows, cols, dy, dy_stride_bytes, sum_in, sum_stride_bytes, weight, weight_dtype, eps, dsum,
+                      dsum_stride_bytes, dx, dx_stride_bytes, dweight, ws, stream=None):
+    _check(lib().moe_rms_norm_backward(int(act_dtype), int(rows), int(cols), _ptr(dy), int(dy_stride_bytes), _ptr(sum_in),
+                                       int(sum_stride_bytes), _ptr(weight), int(weight_dtype), float(eps), _ptr(dsum),
+                                       int(dsum_stride_bytes), _ptr(dx), int(dx_stride_bytes), _ptr(dweight), _ptr(ws),
+                                       _stream(stream)))
+
+
+def select(rule, tokens, n_experts, top_k, logits, logits_stride, balance, topk_idx, topk_w, stream=None):
+    """rule: RouterRuleArg or None."""
+    _check(lib().moe_select(_ref(rule), int(tokens), int(n_experts), int(top_k), _ptr(logits), int(logits_stride),
+                            _ptr(balance), _ptr(topk_idx), _ptr(topk_w), _stream(stream)))
+
+
+def select_backward(rule, tokens, n_experts, top_k, dtopk_w, topk_w, topk_idx, logits, logits_stride, dlogits,
+                    dlogits_stride, stream=None):
+    _check(lib().moe_select_backward(_ref(rule), int(tokens), int(n_experts), int(top_k), _ptr(dtopk_w), _ptr(topk_w),
+                                     _ptr(topk_idx), _ptr(logits), int(logits_stride), _ptr(dlogits), int(dlogits_stride),
+                                     _stream(stream)))
+
+
+def swiglu_checkpoint(act_dtype, groups, max_rows, hidden, gate_up, gate_up_stride_bytes, counts, h, h_stride_bytes, saved,
+                      stream=None):
+    """saved: MxRowsArg (mx_rows) or None."""
+    _check(lib().moe_swiglu_checkpoint(int(act_dtype), int(groups), int(max_rows), int(hidden), _ptr(gate_up),
+                                       int(gate_up_stride_bytes), _ptr(counts), _ptr(h), int(h_stride_bytes), _ref(saved),
+                                       _stream(stream)))
+
+
+def swiglu_backward(act_dtype, groups, max_rows, hidden, dh, dh_stride_bytes, saved, counts, dgate_up,
+                    dgate_up_stride_bytes, h, h_stride_bytes, stream=None):
+    """saved: MxRowsArg (mx_rows) or None."""
+    _check(lib().moe_swiglu_backward(int(act_dtype), int(groups), int(max_rows), int(hidden), _ptr(dh), int(dh_stride_bytes),
+                                     _ref(saved), _ptr(counts), _ptr(dgate_up), int(dgate_up_stride_bytes), _ptr(h),
+                                     int(h_stride_bytes), _stream(stream)))
 
 
 def last_error():

@@ -14,8 +14,9 @@ LIB = os.path.join(PKG, "libmoe.so")
 # the same sources with -DMOE_DEBUG: kernels record invariant violations in
 # the workspace and moe_drop_stats reports them (MOE_ECAP); nothing traps
 LIB_DEBUG = os.path.join(PKG, "libmoe_debug.so")
-# ops/entry.hip holds the whole C ABI: it includes api.hip
-SOURCES = ["kernels.hip", "ops/entry.hip", "ops/mx.hip", "ops/few.hip"]
+# block/entry.hip holds the whole C ABI: it includes ops/entry.hip, which includes api.hip
+SOURCES = ["kernels.hip", "block/entry.hip", "ops/mx.hip", "ops/few.hip", "block/rows8.hip", "block/norm.hip",
+           "block/select.hip"]
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 FLAGS = [

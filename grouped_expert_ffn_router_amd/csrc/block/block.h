@@ -1,0 +1,232 @@
+// The operators around the experts' products (include/moe.h: MX-FP8 rows, norm,
+// choice of experts, SwiGLU with an 8-bit checkpoint): device helpers and the
+// host launchers of the kernels in this directory.
+#pragma once
+
+#include "../ops/mx.h"
+
+namespace moe {
+
+// ------------------------------------------------------------ MX-FP8 blocks
+
+// Exponent of a block's scale from the bits of its largest magnitude m: the
+// smallest e with m 2^-e <= 448, so one more than floor(log2 m) - 8 where the
+// fraction of m is above 1.75.  Field 255 (an infinity or a NaN) is the caller's case.
+__device__ __forceinline__ int mx8_exponent(uint32_t amax_bits) {
+  return max((int)((amax_bits + 0x1fffffu) >> 23) - 135, -127);
+}
+
+// Four values, already multiplied by 2^-e (at most 448 in magnitude), to four
+// E4M3 codes, the first in the low byte.  v_cvt_pk_fp8_f32 rounds to nearest,
+// ties to the even code.
+__device__ __forceinline__ uint32_t mx8_codes4(float a, float b, float c, float d) {
+  int r = 0;
+  r = __builtin_amdgcn_cvt_pk_fp8_f32(a, b, r, false);
+  r = __builtin_amdgcn_cvt_pk_fp8_f32(c, d, r, true);
+  return (uint32_t)r;
+}
+
+// Four E4M3 codes times the scale `unit`.
+__device__ __forceinline__ void mx8_values4(uint32_t codes, float unit, float* v) {
+  const f32x2 lo = __builtin_amdgcn_cvt_pk_f32_fp8((int)codes, false), hi = __builtin_amdgcn_cvt_pk_f32_fp8((int)codes, true);
+  v[0] = lo[0] * unit; v[1] = lo[1] * unit; v[2] = hi[0] * unit; v[3] = hi[1] * unit;
+}
+
+template <int CTRL>
+__device__ __forceinline__ uint32_t dpp_move(uint32_t x) {
+  return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)x, CTRL, 0xf, 0xf, false);
+}
+
+// Maximum over groups of G = 4 or 8 neighbouring lanes: quad permutations
+// [1,0,3,2] and [2,3,0,1], then a mirror of 8 lanes, which swaps the two quads.
+template <int G>
+__device__ __forceinline__ uint32_t lane_group_max(uint32_t v) {
+  v = max(v, dpp_move<0xB1>(v));
+  v = max(v, dpp_move<0x4E>(v));
+  if (G == 8) v = max(v, dpp_move<0x141>(v));
+  return v;
+}
+
+// V values of a lane (a block is 32 / V neighbouring lanes, all active) to
+// codes (V bytes, in c) and the block's scale byte, which is returned.
+template <int V>
+__device__ __forceinline__ int mx8_block(const float (&x)[V], uint32_t (&c)[V / 4]) {
+  uint32_t m = 0;
+#pragma unroll
+  for (int i = 0; i < V; ++i) m = max(m, __float_as_uint(x[i]) & 0x7fffffffu);
+  m = lane_group_max<MX_BLOCK / V>(m);
+  const bool nan = (m >> 23) == 255;
+  const int e = nan ? 0 : mx8_exponent(m);
+  const float inv = mx_inverse_scale(e);
+#pragma unroll
+  for (int i = 0; i < V / 4; ++i)
+    c[i] = nan ? 0u : mx8_codes4(x[4 * i] * inv, x[4 * i + 1] * inv, x[4 * i + 2] * inv, x[4 * i + 3] * inv);
+  return nan ? 255 : e + 127;
+}
+
+// The scale byte of block b of a row, by the block's first lane; the row's
+// last block clears the padding up to a multiple of 16.
+__device__ __forceinline__ void mx8_store_scale(uint8_t* row, int b, int blocks, int byte) {
+  row[b] = (uint8_t)byte;
+  if (b == blocks - 1)
+    for (int p = blocks; p & 15; ++p) row[p] = 0;
+}
+
+template <int N>
+__device__ __forceinline__ void store_codes(uint8_t* p, const uint32_t (&c)[N]) {
+  if constexpr (N == 1) *(uint32_t*)p = c[0];
+  else *(uint2*)p = make_uint2(c[0], c[1]);
+}
+
+// ------------------------------------------------------------ values of a row
+//
+// V consecutive values: 16 bytes (8 bf16, 4 fp32), or one at a time where rows
+// are not 16-byte aligned.
+
+template <class T, int V>
+struct Piece {
+  uint32_t w[4];
+};
+template <class T>
+struct Piece<T, 1> {
+  T v;
+};
+
+template <class T, int V>
+__device__ __forceinline__ Piece<T, V> piece_load(const void* p) {
+  Piece<T, V> r;
+  if constexpr (V == 1) {
+    r.v = *(const T*)p;
+  } else {
+    const uint4 d = *(const uint4*)p;
+    r.w[0] = d.x; r.w[1] = d.y; r.w[2] = d.z; r.w[3] = d.w;
+  }
+  return r;
+}
+
+template <class T, int V>
+__device__ __forceinline__ Piece<T, V> piece_zero() {
+  Piece<T, V> r;
+  if constexpr (V == 1) r.v = (T)0;
+  else
+    for (int i = 0; i < 4; ++i) r.w[i] = 0;
+  return r;
+}
+
+template <class T, int V>
+__device__ __forceinline__ void piece_values(const Piece<T, V>& r, float (&v)[V]) {
+  if constexpr (V == 1) {
+    v[0] = Act<T>::load(r.v);
+  } else if constexpr (sizeof(T) == 2) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      v[2 * i] = __uint_as_float(r.w[i] << 16);
+      v[2 * i + 1] = __uint_as_float(r.w[i] & 0xffff0000u);
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] = __uint_as_float(r.w[i]);
+  }
+}
+
+template <class T, int V>
+__device__ __forceinline__ void piece_store(void* p, const float (&v)[V]) {
+  if constexpr (V == 1) {
+    *(T*)p = Act<T>::store(v[0]);
+  } else if constexpr (sizeof(T) == 2) {
+    *(uint4*)p = make_uint4(f32x2_to_bf16x2(v[0], v[1]), f32x2_to_bf16x2(v[2], v[3]), f32x2_to_bf16x2(v[4], v[5]),
+                            f32x2_to_bf16x2(v[6], v[7]));
+  } else {
+    *(float4*)p = make_float4(v[0], v[1], v[2], v[3]);
+  }
+}
+
+// V values of a vector that is fp32 or bf16 (a uniform choice); 16-byte aligned where V > 1.
+template <int V>
+__device__ __forceinline__ void weight_values(const void* w, bool f32, int64_t i, float (&v)[V]) {
+  if constexpr (V == 1) {
+    v[0] = f32 ? ((const float*)w)[i] : bf16_to_f32(((const bf16_t*)w)[i]);
+  } else if (f32) {
+#pragma unroll
+    for (int q = 0; q < V; q += 4) {
+      const float4 d = *(const float4*)((const float*)w + i + q);
+      v[q] = d.x; v[q + 1] = d.y; v[q + 2] = d.z; v[q + 3] = d.w;
+    }
+  } else {
+#pragma unroll
+    for (int q = 0; q < V; q += 4) {
+      const uint2 d = *(const uint2*)((const bf16_t*)w + i + q);
+      v[q] = __uint_as_float(d.x << 16); v[q + 1] = __uint_as_float(d.x & 0xffff0000u);
+      v[q + 2] = __uint_as_float(d.y << 16); v[q + 3] = __uint_as_float(d.y & 0xffff0000u);
+    }
+  }
+}
+
+// ------------------------------------------------------------ launchers
+
+struct Rows8 {  // MX-FP8 rows to write or read; codes NULL: none
+  uint8_t* codes;
+  uint8_t* scales;
+  int64_t ldc, lds;
+};
+
+hipError_t launch_mx8_quantize(bool bf16, int64_t rows, int64_t cols, const void* x, int64_t ldx, const Rows8& q,
+                               hipStream_t st);
+hipError_t launch_mx8_dequantize(bool bf16, int64_t rows, int64_t cols, const Rows8& q, void* out, int64_t ldo,
+                                 hipStream_t st);
+
+struct NormArgs {
+  int64_t rows, cols;
+  const void *x, *residual, *weight;  // residual may be NULL
+  int64_t ldx, ldr, lds, ldy;         // bytes
+  void *stream, *y;                   // outputs, either may be NULL
+  Rows8 q;
+  float eps;
+  bool bf16, weight_f32;
+};
+hipError_t launch_rms_norm(const NormArgs& a, hipStream_t st);
+
+struct NormBackArgs {
+  int64_t rows, cols;
+  const void *dy, *s, *dstream, *weight;  // dstream may be NULL
+  int64_t lddy, lds, ldds, lddx;          // bytes
+  void* dx;
+  float* dweight;
+  float* part;  // [parts][cols]
+  int64_t parts;
+  float eps;
+  bool bf16, weight_f32;
+};
+// Partial sums of the weight's gradient that a call keeps.
+int64_t norm_parts(int64_t rows, int64_t cols);
+hipError_t launch_rms_norm_backward(const NormBackArgs& a, hipStream_t st);
+hipError_t launch_norm_dweight(const NormBackArgs& a, hipStream_t st);
+
+struct SelectRule {
+  int score, groups, top_groups, group_best, renorm;
+  float scale;
+};
+hipError_t launch_select_rule(const SelectRule& r, const float* logits, int64_t ld, const float* balance, int64_t T, int E,
+                              int k, int32_t* idx, float* w, hipStream_t st);
+hipError_t launch_select_backward(const SelectRule& r, const float* dw, const float* w, const int32_t* idx,
+                                  const float* logits, int64_t ld, int64_t T, int E, int k, float* dlogits, int64_t ldd,
+                                  hipStream_t st);
+
+struct SwigluArgs {
+  int groups;
+  int64_t max_rows, hidden;
+  const int32_t* counts;  // [groups], or NULL
+  const void* gate_up;    // forward
+  const void* dh;         // backward
+  int64_t ldg, ldh, ldd;  // bytes: gate_up / dgate_up rows, h rows, dh rows
+  void* h;                // forward: output; backward: output or NULL
+  void* dgate_up;
+  Rows8 q;
+  bool bf16;
+};
+hipError_t launch_swiglu_checkpoint(const SwigluArgs& a, hipStream_t st);
+hipError_t launch_swiglu_backward(const SwigluArgs& a, hipStream_t st);
+
+hipError_t launch_mx8_gemm(const MxGemmArgs& g, int cus, hipStream_t st);
+
+}  // namespace moe

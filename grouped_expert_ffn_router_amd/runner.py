@@ -728,9 +728,10 @@ def _row_stride(t, what):
     return t.shape[-1] if stride is None else stride
 
 
-class MxRows:
-    """Rows of `cols` MX-FP4 values on the GPU (include/moe.h describes the format):
-    codes [..., rows, cols / 2] and scales [..., rows, cols / 32 rounded up to 16], uint8."""
+class ScaledRows:
+    """Rows of codes with a scale for every 32 values, on the GPU: what MxRows and block.Mx8Rows share."""
+
+    _strides = staticmethod(_mx_strides)   # of a row of that many values: (code, scale) bytes
 
     def __init__(self, codes, scales, cols):
         self._codes, self._scales, self.cols = codes, scales, cols
@@ -763,7 +764,7 @@ class MxRows:
     def _layout(self):
         """Checks the tensors and takes their strides."""
         codes, scales = self._codes, self._scales
-        cb, sb = _mx_strides(self.cols)
+        cb, sb = self._strides(self.cols)
         if codes.dtype != torch.uint8 or scales.dtype != torch.uint8:
             raise TypeError("codes and scales are uint8")
         if codes.shape[:-1] != scales.shape[:-1] or codes.shape[-1] != cb or scales.shape[-1] < sb:
@@ -805,7 +806,12 @@ class MxRows:
 
     def __getitem__(self, i):
         """A part along the leading dimension(s), as of the tensors."""
-        return MxRows(self.codes[i], self.scales[i], self.cols)
+        return type(self)(self.codes[i], self.scales[i], self.cols)
+
+
+class MxRows(ScaledRows):
+    """Rows of `cols` MX-FP4 values on the GPU (include/moe.h describes the format):
+    codes [..., rows, cols / 2] and scales [..., rows, cols / 32 rounded up to 16], uint8."""
 
 
 def mx_quantize(x):
@@ -830,6 +836,8 @@ def mx_dequantize(q, dtype=torch.bfloat16):
     code = _DTYPE.get(dtype)
     if code is None:
         raise TypeError(f"mx_dequantize gives bf16 or fp32, not {dtype}")
+    if not isinstance(q, MxRows):
+        raise TypeError(f"mx_dequantize takes MxRows, not {type(q).__name__}")
     st, dev = _on(q.codes)
     with dev:
         out = torch.empty(q.codes.shape[:-1] + (q.cols,), dtype=dtype, device=q.codes.device)
@@ -843,6 +851,8 @@ def mx_gemm(a, b, counts=None, out=None, dtype=torch.bfloat16):
     """out[g] = a[g] . b[g]^T of MxRows a [G, M, K] and b [G, N, K] (or [M, K] and
     [N, K]) as bf16 or fp32.  counts: int32 [G] rows of each group (the rows of
     `out` behind them are left as they were)."""
+    if not (isinstance(a, MxRows) and isinstance(b, MxRows)):
+        raise TypeError(f"mx_gemm takes MxRows, not {type(a).__name__} and {type(b).__name__}")
     ca, cb = a.codes, b.codes
     sa, sb = ca.shape, cb.shape
     if len(sa) != len(sb) or len(sa) not in (2, 3) or a.cols != b.cols or sa[:-2] != sb[:-2]:

@@ -303,7 +303,9 @@ const char* moe_last_error(void);
  * zero_dropped, combine, shared_gate_up, up_shared_down, and the tail-split
  * fixups route_fixup, gate_up_fixup, down_fixup, up_fixup; mx_quantize,
  * mx_dequantize, mx_gemm, mx_gather, mx_gate_up, mx_down;
- * few_project, few_select_shared, few_gate_up, few_down, few_up. */
+ * few_project, few_select_shared, few_gate_up, few_down, few_up;
+ * mx8_quantize, mx8_dequantize, mx8_gemm, rms_norm, rms_norm_backward,
+ * norm_dweight, select, select_backward, swiglu_checkpoint, swiglu_backward. */
 typedef struct moe_kernel_time {
   char name[32];    /* kernel label */
   int32_t launches; /* launches recorded since the last moe_timing_read */
@@ -440,6 +442,134 @@ int moe_few_tokens(const moe_dims* dims, const void* x, const void* w_router, co
                    const float* bias, int32_t bias_row_tokens, const void* w13, const void* w13_scales,
                    const void* w2, const void* w2_scales, const void* w_up, const void* ws13,
                    const void* ws2, int32_t* topk_idx, float* topk_w, void* out, void* ws, void* stream);
+
+/* ------------------------------------------------------------ MX-FP8 rows
+ * Rows of 8-bit floating point values with one power-of-two scale for every
+ * 32 consecutive values (E4M3 elements, E8M0 scales): as MX-FP4 rows, but
+ *   codes   cols bytes, one E4M3 value each (sign, 4 exponent bits with bias 7,
+ *           3 fraction bits; 0x7f and 0xff are NaN, 448 is the largest value)
+ * so that a code stride is at least cols.  Scales as in MX-FP4 rows.  The
+ * entry points' names have mxb for them: a byte a value. */
+
+/* Smallest strides of a row of `cols` values (host only), as moe_mx_strides. */
+int moe_mxb_strides(int64_t cols, int64_t* code_stride_bytes, int64_t* scale_stride_bytes);
+
+/* Rows to MX-FP8.  For a block with m = max |x| the scale is 2^e with the
+ * smallest e in [-127, 127] for which m * 2^-e <= 448 (the format leaves the
+ * choice open; taking floor(log2 m) - 8 would cut values off at 7/8 of the
+ * largest), and a value becomes x * 2^-e rounded to the nearest code, ties to
+ * the even one: off by at most 2^-4 of itself, or 2^-10 * 2^e where that is
+ * more.  A block that holds a NaN or an infinity gets scale byte 255 and codes
+ * 0.  Scale padding bytes (up to a multiple of 16) are set to 0.
+ *   x    [rows][cols] act at x_stride_bytes a row (a multiple of 16)
+ *   out  rows to write; rows * cols <= 2^40 */
+int moe_mxb_quantize(int32_t act_dtype, int64_t rows, int64_t cols, const void* x, int64_t x_stride_bytes,
+                     const moe_mx_rows* out, void* stream);
+
+/* MX-FP8 rows back to activations (exact, but for overflow and underflow of
+ * the extreme scales). */
+int moe_mxb_dequantize(int32_t act_dtype, int64_t rows, int64_t cols, const moe_mx_rows* q, void* out,
+                       int64_t out_stride_bytes, void* stream);
+
+/* ------------------------------------------------------------ norm
+ * Root-mean-square norm of rows, with the residual stream's addition before it
+ * (a block's norm in front of the layer):
+ *   s = x + residual,  r = (mean(s^2) + eps)^-1/2,  y = s * r * weight
+ * in fp32, from the sum before its rounding; each output is rounded once.
+ *   x, residual   [rows][cols] act; residual may be NULL (s = x)
+ *   weight        [cols] of weight_dtype (MOE_ACT_BF16 / MOE_ACT_F32)
+ *   sum           [rows][cols] act output: s, or NULL; may be x or residual
+ *                 (the same address and stride)
+ *   y             [rows][cols] act output, or NULL; may be x or residual too
+ *   y8            MX-FP8 rows of y (from its fp32 values), or NULL; cols is a
+ *                 multiple of 32 then, and every row and the weight start
+ *                 16-byte aligned
+ * y or y8 is given.  cols <= MOE_NORM_COLS_MAX.  Addresses and strides are
+ * multiples of the value's size; with 16-byte aligned rows and cols a multiple
+ * of 8 (bf16) or 4 (fp32) values are moved 16 bytes at a time.  Squares are
+ * summed in fp32, so a row whose squares exceed 2^127 gives 0. */
+#define MOE_NORM_COLS_MAX 16384
+int moe_rms_norm(int32_t act_dtype, int64_t rows, int64_t cols, const void* x, int64_t x_stride_bytes,
+                 const void* residual, int64_t residual_stride_bytes, const void* weight, int32_t weight_dtype, float eps,
+                 void* sum, int64_t sum_stride_bytes, void* y, int64_t y_stride_bytes, const moe_mx_rows* y8, void* stream);
+
+/* Its backward pass.  With n = s * r and g = dy * weight,
+ *   dx = r * (g - n * mean(g * n)) + dsum   (the gradient of x and of residual)
+ *   dweight = sum over rows of dy * n       (fp32, in a fixed order)
+ * where s is `sum` as moe_rms_norm wrote it, or x where there was no residual.
+ *   dsum     gradient that reached s beside the norm, or NULL
+ *   dx       [rows][cols] act output; may be dy, dsum or sum
+ *   dweight  [cols] fp32 output
+ *   ws       moe_rms_norm_workspace_size() bytes, used by one call at a time */
+int moe_rms_norm_workspace_size(int64_t rows, int64_t cols, size_t* bytes);
+int moe_rms_norm_backward(int32_t act_dtype, int64_t rows, int64_t cols, const void* dy, int64_t dy_stride_bytes,
+                          const void* sum, int64_t sum_stride_bytes, const void* weight, int32_t weight_dtype, float eps,
+                          const void* dsum, int64_t dsum_stride_bytes, void* dx, int64_t dx_stride_bytes, float* dweight,
+                          void* ws, void* stream);
+
+/* ------------------------------------------------------------ choice of experts
+ * The choice that moe_route makes (softmax over the k best logits), under a
+ * rule of the caller's and from logits alone.
+ *   score        MOE_SCORE_SOFTMAX: the softmax over all logits;
+ *                MOE_SCORE_SIGMOID: each logit's sigmoid
+ *   rank         score + balance[e] (the bias counts for the choice alone)
+ *   groups       the experts in `groups` blocks of E / groups (at most 64); the
+ *                top_groups blocks with the largest sum of their group_best (1
+ *                or 2) largest ranks stay, equal ones by lower index
+ *   choice       the top_k largest ranks of the groups that stay, in descending
+ *                order, equal ones by lower expert index
+ *   weight       score of a chosen expert, divided by the sum over the chosen
+ *                ones if `renormalise`, times `scale`
+ * Ranks are compared as 64-bit arithmetic has them (without a bias, the logits
+ * are).  An expert whose logit or rank is -infinity is out: it is chosen only
+ * after all others, by lower index, with weight 0.  Where the chosen scores add
+ * up to 0 in fp32 (all are out, or below 2^-149) the weights are 0.  A token
+ * with a NaN among its logits or ranks, or under softmax a logit of +infinity,
+ * gets experts 0 .. top_k - 1 and NaN weights.
+ *   logits    [T][E] fp32 at logits_stride values a row; E <= 2048
+ *   balance   [E] fp32, or NULL
+ *   topk_idx, topk_w  [T][k] int32 and fp32 outputs; k <= min(32, E) */
+enum { MOE_SCORE_SOFTMAX = 0, MOE_SCORE_SIGMOID = 1 };
+typedef struct moe_router_rule {
+  int32_t score, groups, top_groups, group_best, renormalise;
+  float scale; /* positive */
+} moe_router_rule;
+int moe_select(const moe_router_rule* rule, int64_t tokens, int32_t n_experts, int32_t top_k, const float* logits,
+               int64_t logits_stride, const float* balance, int32_t* topk_idx, float* topk_w, void* stream);
+
+/* Gradient of the weights to the logits (the choice itself has none, and so
+ * the balance bias has none).  dtopk_w is the gradient of topk_w; topk_w,
+ * topk_idx and logits are those of the moe_select call.  Every value of dlogits
+ * is written.  An index out of range and a weight of 0 take no part; an expert
+ * named twice gets both terms. */
+int moe_select_backward(const moe_router_rule* rule, int64_t tokens, int32_t n_experts, int32_t top_k, const float* dtopk_w,
+                        const float* topk_w, const int32_t* topk_idx, const float* logits, int64_t logits_stride,
+                        float* dlogits, int64_t dlogits_stride, void* stream);
+
+/* ------------------------------------------------------------ SwiGLU, 8-bit checkpoint
+ * h = silu(gate) * up of the experts' rows, and the gate and up values kept for
+ * the backward pass as MX-FP8 rows: 33/16 bytes a hidden unit and row in the
+ * place of 4 (bf16).
+ *   gate_up  row m of group g (m < counts[g]) at (g * max_rows + m) *
+ *            gate_up_stride_bytes: `hidden` gate values, then `hidden` up values
+ *   counts   [groups] int32 rows of each group (a negative count is 0), or
+ *            NULL: max_rows each; rows past the count are left as they were
+ *   h        [groups][max_rows][hidden] act output
+ *   saved    MX-FP8 rows of 2 * hidden values, written
+ * hidden is a multiple of 32; rows start 16-byte aligned; groups <= 4096 and
+ * groups * max_rows * 2 * hidden <= 2^40. */
+int moe_swiglu_checkpoint(int32_t act_dtype, int32_t groups, int64_t max_rows, int64_t hidden, const void* gate_up,
+                          int64_t gate_up_stride_bytes, const int32_t* counts, void* h, int64_t h_stride_bytes,
+                          const moe_mx_rows* saved, void* stream);
+
+/* Its backward pass at the saved values a (gate) and b (up): with
+ * sg = sigmoid(a), dgate = dh * b * sg * (1 + a * (1 - sg)) and dup = dh * a * sg.
+ *   dgate_up  as gate_up, output
+ *   h         h again, from the saved values (the second projection's weight
+ *             gradient needs it), or NULL */
+int moe_swiglu_backward(int32_t act_dtype, int32_t groups, int64_t max_rows, int64_t hidden, const void* dh,
+                        int64_t dh_stride_bytes, const moe_mx_rows* saved, const int32_t* counts, void* dgate_up,
+                        int64_t dgate_up_stride_bytes, void* h, int64_t h_stride_bytes, void* stream);
 
 #ifdef __cplusplus
 }

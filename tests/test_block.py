@@ -1,0 +1,504 @@
+"""Norm, choice of experts, MX-FP8 rows and SwiGLU with its checkpoint on the GPU against 64-bit arithmetic."""
+
+import copy
+import math
+import pickle
+
+import pytest
+import torch
+
+import block_ref as R
+from grouped_expert_ffn_router_amd import binding as B, block, runner
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda"
+U = 2.0 ** -24                    # half a step of fp32, relative
+ACTS = [torch.bfloat16, torch.float32]
+
+
+def _gen(seed):
+    return torch.Generator().manual_seed(seed)
+
+
+def _rand(gen, shape, dtype, spread=0.0, pad=0):
+    x = torch.randn(tuple(shape[:-1]) + (shape[-1] + pad,), generator=gen)
+    if spread:
+        x = x * torch.exp(torch.randn((shape[-1] + pad,), generator=gen) * spread)
+    return x.to(dtype).to(DEV)[..., :shape[-1]]
+
+
+def _within(got, want, slack, what=""):
+    """Element by element: the rounding of the output type, `slack` (float64) and what underflows."""
+    got64 = R.bits64(got)
+    tol = want.abs() * (torch.finfo(got.dtype).eps / 2) + slack * (1 + 2.0 ** -7) + 2.0 ** -130
+    bad = ~((got64 - want).abs() <= tol)
+    assert not bad.any(), (what, int(bad.sum()), float((got64 - want).abs().max()), float(((got64 - want).abs() / tol).max()))
+
+
+# ---------------------------------------------------------------- MX-FP8 rows
+
+@pytest.mark.parametrize("dtype", ACTS)
+@pytest.mark.parametrize("rows,cols,pad", [(1, 32, 0), (3, 64, 8), (65, 544, 0), (257, 2080, 40), (1000, 96, 0)])
+def test_rows_to_mx8_and_back(rows, cols, pad, dtype):
+    x = _rand(_gen(rows * 7 + cols), (rows, cols), dtype, 1.5, pad)
+    x[rows // 2] = 0
+    q = block.mx8_quantize(x)
+    want, scales = R.grid8(R.bits64(x))
+    assert torch.equal(q.scales[:, :cols // 32].cpu(), scales)
+    assert not q.scales[:, cols // 32:].any()
+    assert torch.equal(R.decode8(q.codes, q.scales), want)
+    assert torch.equal(R.bits64(block.mx8_dequantize(q, torch.float32)), want)
+    _within(block.mx8_dequantize(q, torch.bfloat16), want, torch.zeros(1))
+
+
+def test_every_bf16_pattern_to_mx8_and_back():
+    """Every bf16 magnitude as a block's largest, with values that land on and beside the borders of the codes."""
+    top = torch.arange(0x0000, 0x7f80, dtype=torch.int32).to(torch.int16).view(torch.bfloat16)
+    part = torch.linspace(-1, 1, 31).to(torch.float64)
+    x = torch.cat([top.double()[:, None], (top.double()[:, None] * part).float().bfloat16().double()], 1).to(torch.bfloat16)
+    x = x.clamp(-3.3895e38, 3.3895e38)
+    q = block.mx8_quantize(x.to(DEV))
+    want, scales = R.grid8(x.double())
+    assert torch.equal(q.scales[:, :1].cpu(), scales)
+    assert torch.equal(R.decode8(q.codes, q.scales), want)
+
+
+def test_nearest_code_ties_to_even():
+    """All midpoints between neighbouring codes, and the fp32 values beside them, in a block whose largest is 448."""
+    v = R.code8_values()[:127]
+    mid = (v[1:] + v[:-1]) / 2
+    f = mid.float()
+    x = torch.cat([f, torch.nextafter(f, torch.tensor(0.0)), torch.nextafter(f, torch.tensor(1e9))])
+    x = torch.cat([x, torch.zeros(-len(x) % 31)]).reshape(-1, 31)
+    x = torch.cat([torch.full((len(x), 1), 448.0), x, torch.full((len(x), 1), -448.0), -x], 1)
+    q = block.mx8_quantize(x.to(DEV))
+    want, scales = R.grid8(x.double())
+    assert (scales == 127).all() and torch.equal(R.decode8(q.codes, q.scales), want)
+
+
+def test_every_code_and_scale_back():
+    codes = torch.arange(256, dtype=torch.uint8).reshape(1, 256).repeat(256, 1)
+    scales = torch.arange(256, dtype=torch.uint8)[:, None].repeat(1, 16)
+    q = block.Mx8Rows(codes.to(DEV), scales.to(DEV), 256)
+    want = R.decode8(codes, scales)
+    got = R.bits64(block.mx8_dequantize(q, torch.float32))
+    far = want.abs() >= 2.0 ** 128
+    assert torch.equal(got.isnan(), want.isnan())
+    assert torch.isinf(got[far]).all()
+    near = ~far & ~want.isnan()
+    assert ((got - want).abs()[near] <= 2.0 ** -150).all()   # fp32 has steps of 2^-149 down there
+
+
+def test_nan_and_infinite_blocks():
+    x = torch.ones((4, 96))
+    x[0, 40], x[1, 0], x[2, 95] = math.nan, math.inf, -math.inf
+    for dtype in ACTS:
+        q = block.mx8_quantize(x.to(dtype).to(DEV))
+        assert q.scales.cpu()[:, :3].eq(255).tolist() == [[False, True, False], [True, False, False], [False, False, True],
+                                                          [False, False, False]]
+        back = block.mx8_dequantize(q, dtype).cpu()
+        assert back.isnan().sum() == 96 and (back[~back.isnan()] == 1).all()
+
+
+# ---------------------------------------------------------------- norm
+
+NORM = [(1, 1), (5, 7), (3, 8), (64, 32), (4, 96), (130, 512), (17, 513), (33, 1000), (9, 2048), (7, 2056), (5, 4099), (3, 6144),
+        (2, 8200), (2, 16384)]
+
+
+def _norm_slack(cols):
+    # squares: NC V <= 64 additions in a thread, 6 + 16 across, all of one sign, half of it in the root; root, quotient and mean
+    # one step each; s, s r, (s r) w one each
+    return (0.5 * (64 + 22 + 2) + 8) * U
+
+
+@pytest.mark.parametrize("dtype", ACTS)
+@pytest.mark.parametrize("rows,cols", NORM)
+@pytest.mark.parametrize("residual,pad,wdtype", [(False, 0, None), (True, 0, torch.float32), (True, 3, torch.bfloat16), (True, 8, None)])
+def test_rms_norm(rows, cols, residual, pad, wdtype, dtype):
+    gen = _gen(rows + cols)
+    x, res = _rand(gen, (rows, cols), dtype, 0.5, pad), _rand(gen, (rows, cols), dtype, 0.5, pad) if residual else None
+    w = _rand(gen, (cols,), wdtype or dtype)
+    y, s = block.rms_norm(x, w, residual=res, eps=1e-5)
+    want, s64 = R.norm(R.bits64(x), R.bits64(w), None if res is None else R.bits64(res), 1e-5)
+    _within(y, want, want.abs() * _norm_slack(cols), "y")
+    if residual:
+        _within(s, s64, s64.abs() * U, "s")
+    else:
+        assert s is x
+    if cols % 32 == 0 and pad in (0, 8):
+        q, s2 = block.rms_norm(x, w, residual=res, eps=1e-5, form="mx8")
+        (y3, q3), s3 = block.rms_norm(x, w, residual=res, eps=1e-5, form="both")
+        assert torch.equal(s, s2) and torch.equal(s, s3) and torch.equal(y, y3)
+        assert torch.equal(q.codes, q3.codes) and torch.equal(q.scales, q3.scales)
+        # a value of the grid is off by half a step: 2^-4 of itself, or 2^-10 2^e with 2^e <= 2 max / 448
+        got = R.decode8(q.codes, q.scales)
+        top = want.reshape(rows, -1, 32).abs().amax(-1, keepdim=True).expand(-1, -1, 32).reshape(rows, cols)
+        slack = torch.maximum(want.abs() * 2.0 ** -4, 2.0 ** -10 * 2 * top / 448) + 2 * top * _norm_slack(cols)
+        assert ((got - want).abs() <= slack * (1 + 2.0 ** -10)).all()
+
+
+def test_rms_norm_of_zero_large_and_nan_rows():
+    x = torch.zeros((6, 64))
+    x[1], x[2], x[3, 5], x[4, 5] = 1e18, 1e-30, math.nan, math.inf
+    y, _ = block.rms_norm(x.to(DEV), torch.ones(64, device=DEV), eps=1e-6)
+    y = y.cpu()
+    assert (y[0] == 0).all() and (y[5] == 0).all() and torch.allclose(y[1], torch.ones(64)) and (y[2] <= 1e-26).all()
+    assert y[3].isnan().all() and (y[4].isnan() | (y[4] == 0)).all()
+    q, _ = block.rms_norm(x.to(DEV), torch.ones(64, device=DEV), eps=1e-6, form="mx8")
+    assert (q.scales[3, :2] == 255).all() and (q.scales[5, :2] == 0).all()
+
+
+@pytest.mark.parametrize("dtype", ACTS)
+@pytest.mark.parametrize("rows,cols", NORM + [(300, 96), (70, 6144), (1030, 24), (4100, 40)])
+@pytest.mark.parametrize("beside,pad", [(False, 0), (True, 0), (True, 3)])
+def test_rms_norm_backward(rows, cols, beside, pad, dtype):
+    gen = _gen(rows * 3 + cols)
+    s, dy = _rand(gen, (rows, cols), dtype, 0.5, pad), _rand(gen, (rows, cols), dtype, 0.0, pad)
+    t = _rand(gen, (rows, cols), dtype, 0.0, pad) if beside else None
+    w = _rand(gen, (cols,), dtype)
+    dx, dw = block.rms_norm_backward(dy, s, w, dstream=t, eps=1e-5)
+    s, dy, w, t = R.bits64(s), R.bits64(dy), R.bits64(w), None if t is None else R.bits64(t)
+    want, dw_want = R.norm_backward(dy, s, w, t, 1e-5)
+    r = ((s * s).mean(-1, keepdim=True) + 1e-5) ** -0.5
+    n, g = (s * r).abs(), (dy * w).abs()
+    rel = _norm_slack(cols)
+    # r and n off by `rel`, the mean by its 88 additions and theirs; then four more steps
+    slack = r * (g * (rel + 6 * U) + n * (g * n).mean(-1, keepdim=True) * (4 * rel + 100 * U)) + want.abs() * 2 * U
+    if t is not None:
+        slack = slack + t.abs() * 2 * U
+    _within(dx, want, slack, "dx")
+    # a partial sum takes at most rows / parts rows, 32 threads add parts / 32 each, and those 32 are added
+    steps = rows / max(1, min(1024, rows // 16)) + 1024 / 32 + 32 + 4
+    assert ((R.bits64(dw) - dw_want).abs() <= (dy.abs() * n).sum(0) * (rel + steps * U) + dw_want.abs() * U).all()
+
+
+def test_rms_norm_gradient_by_differences():
+    gen = _gen(5)
+    x, w, dy = (torch.randn(s, generator=gen, dtype=torch.float64) for s in ((4, 40), (40,), (4, 40)))
+    dx, dw = block.rms_norm_backward(dy.float().to(DEV), x.float().to(DEV), w.float().to(DEV), eps=1e-3)
+    x, w, dy = x.float().double(), w.float().double(), dy.float().double()
+    loss = lambda x, w: float((R.norm(x, w, eps=1e-3)[0] * dy).sum())  # noqa: E731
+    step = 1e-5   # the differences are off by its square and by 2^-52 / step
+    for i, j in ((0, 0), (1, 7), (3, 39)):
+        d = torch.zeros_like(x)
+        d[i, j] = step
+        assert abs((loss(x + d, w) - loss(x - d, w)) / (2 * step) - float(dx[i, j])) < 1e-5
+        d = torch.zeros_like(w)
+        d[j] = step
+        assert abs((loss(x, w + d) - loss(x, w - d)) / (2 * step) - float(dw[j])) < 1e-5
+
+
+def test_rms_norm_in_place():
+    """The sum over the residual, the norm over x; the gradient over either of its inputs."""
+    gen = _gen(8)
+    for cols, dtype in ((512, torch.bfloat16), (513, torch.bfloat16), (6144, torch.float32)):
+        x, res, w = (_rand(gen, s, dtype) for s in ((40, cols), (40, cols), (cols,)))
+        y, s = block.rms_norm(x, w, residual=res)
+        code, ld = runner._DTYPE[dtype], cols * x.element_size()
+        x2, r2 = x.clone(), res.clone()
+        B.rms_norm(code, 40, cols, x2, ld, r2, ld, w, code, 1e-6, r2, ld, x2, ld, None)
+        assert torch.equal(x2, y) and torch.equal(r2, s)
+        dx, dw = block.rms_norm_backward(x, s, w, dstream=res)
+        for over in range(3):
+            a, b, c = x.clone(), s.clone(), res.clone()
+            ws = torch.empty(B.rms_norm_workspace_size(40, cols), dtype=torch.uint8, device=DEV)
+            dw2 = torch.empty_like(dw)
+            B.rms_norm_backward(code, 40, cols, a, ld, b, ld, w, code, 1e-6, c, ld, (a, b, c)[over], ld, dw2, ws)
+            assert torch.equal((a, b, c)[over], dx) and torch.equal(dw2, dw)
+
+
+def test_no_rows():
+    w = torch.ones(64, device=DEV)
+    for dtype in ACTS:
+        x = torch.empty((0, 64), dtype=dtype, device=DEV)
+        y, s = block.rms_norm(x, w, residual=x, form="both")
+        assert y[0].shape == (0, 64) and s.shape == (0, 64)
+        dx, dw = block.rms_norm_backward(x, x, w)
+        assert dx.shape == (0, 64) and (dw == 0).all()
+        assert block.mx8_dequantize(block.mx8_quantize(x)).shape == (0, 64)
+        h, saved = block.swiglu_checkpoint(x)
+        assert h.shape == (0, 32) and block.swiglu_backward(h, saved)[0].shape == (0, 64)
+    logits = torch.empty((0, 8), device=DEV)
+    rule = block.RouterRule(2)
+    idx, wt = block.select_experts(logits, rule)
+    assert idx.shape == (0, 2) and block.select_experts_backward(wt, wt, idx, logits, rule).shape == (0, 8)
+
+
+# ---------------------------------------------------------------- choice of experts
+
+def _weights_within(w, want, logits):
+    """expf's two steps and its argument's (at most the row's spread), the k terms of the sum, quotient and scale."""
+    finite = torch.where(logits.isinf(), torch.zeros_like(logits), logits)
+    spread = (finite.amax(1) - finite.amin(1) + finite.abs().amax(1))[:, None]
+    _within(w, want, want * (48 + 2 * spread) * U + 2.0 ** -126)
+
+
+RULES = [
+    dict(score="softmax"), dict(score="softmax", renormalise=False, scale=2.5), dict(score="sigmoid"),
+    dict(score="sigmoid", renormalise=False), dict(score="sigmoid", balance=True, scale=2.5),
+    dict(score="softmax", balance=True), dict(score="softmax", balance=True, renormalise=False),
+    dict(score="sigmoid", balance=True, groups=4, top_groups=2), dict(score="softmax", groups=4, top_groups=3, group_best=1),
+    dict(score="sigmoid", groups=4, top_groups=1), dict(score="softmax", balance=True, groups=4, top_groups=2, renormalise=False),
+]
+
+
+@pytest.mark.parametrize("rule", RULES, ids=lambda r: "-".join(str(v) for v in r.values()))
+@pytest.mark.parametrize("T,E,k", [(1, 8, 2), (37, 24, 4), (50, 64, 8), (41, 100, 5), (33, 384, 8), (17, 516, 16), (9, 1000, 3),
+                                   (5, 2048, 32)])
+def test_select_and_its_gradient(T, E, k, rule):
+    rule = dict(rule)
+    groups = rule.get("groups", 1)
+    if E % groups or rule.get("top_groups", 1) * (E // groups) < k:
+        pytest.skip("a rule this shape has no room for")
+    gen = _gen(T * 31 + E)
+    logits = torch.randn((T, E), generator=gen) * 2
+    masked = torch.zeros((T, E), dtype=torch.bool)
+    if T > 4:
+        masked[1, ::2], masked[2], masked[3, 1:] = True, True, True
+        masked[4, :E // 2] = True
+    logits = logits.masked_fill(masked, -math.inf)
+    balance = torch.randn((E,), generator=gen) * 0.1 if rule.pop("balance", False) else None
+    r = block.RouterRule(k, balance=None if balance is None else balance.to(DEV), **rule)
+    dev = logits.to(DEV)
+    idx, w = block.select_experts(dev, r)
+    want_idx, want_w = R.select(logits.double(), k, balance=None if balance is None else balance.double(), **rule)
+    assert torch.equal(idx.cpu(), want_idx)
+    _weights_within(w, want_w, logits.double())
+
+    dw = torch.randn((T, k), generator=gen)
+    got = R.bits64(block.select_experts_backward(dw.to(DEV), w, idx, dev, r))
+    leaf = logits.double().clamp(min=-1e4).requires_grad_()   # -infinity has no gradient, -1e4 one of 0
+    out = want_w == 0
+    args = rule.get("score", "softmax"), rule.get("renormalise", True), rule.get("scale", 1.0)
+    (R.select_weights(leaf, want_idx, out, *args) * dw.double()).sum().backward()
+    want = leaf.grad
+    # every term is a product of the weights (off by a few steps) with differences of gradients
+    size = (want_w.abs() * dw.double().abs()).sum(1, keepdim=True) + dw.double().abs().amax(1, keepdim=True) * want_w.abs().amax(1, keepdim=True)
+    spread = (leaf.detach().clamp(min=-50).amax(1, keepdim=True) + 60)
+    assert ((got - want).abs() <= size * (64 + 2 * spread) * U + 2.0 ** -126).all()
+
+
+def test_select_strided_logits():
+    wide = torch.randn((70, 120), generator=_gen(2)).to(DEV)
+    rule = block.RouterRule(3, score="sigmoid", balance=torch.zeros(101, device=DEV))
+    part = wide[:, 7:108]
+    idx, w = block.select_experts(part, rule)
+    idx2, w2 = block.select_experts(part.contiguous(), rule)
+    assert torch.equal(idx, idx2) and torch.equal(w, w2)
+    assert torch.equal(block.select_experts_backward(w, w, idx, part, rule),
+                       block.select_experts_backward(w, w, idx, part.contiguous(), rule))
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("groups", [1, 6])
+def test_equal_and_nearly_equal_scores(score, groups):
+    """Ties go to the lower expert; ranks that differ by less than fp32 scores resolve are ordered as 64 bits order them."""
+    T, E, k = 60, 96, 8
+    gen = _gen(groups)
+    base = torch.randn((T, 6), generator=gen).repeat(1, 16)
+    steps = torch.randint(0, 3, (T, E), generator=gen)
+    logits = base.clone()
+    for i in range(2):   # up to two fp32 neighbours up
+        logits = torch.where(steps > i, torch.nextafter(logits, torch.tensor(9.0)), logits)
+    logits[0], logits[1] = 0.0, -3.0
+    logits[2] = torch.where(torch.arange(E) % 2 == 0, 0.0, -0.0)
+    balance = torch.tensor([0.25, -0.5, 0.125])[torch.arange(E) % 3]
+    balance[:6] = balance[6:12]
+    kw = dict(score=score, groups=groups, top_groups=max(1, groups // 2))
+    for b in (balance, balance * 0, None):
+        idx, w = block.select_experts(logits.to(DEV), block.RouterRule(k, balance=None if b is None else b.to(DEV), **kw))
+        want_idx, want_w = R.select(logits.double(), k, balance=None if b is None else b.double(), **kw)
+        assert torch.equal(idx.cpu(), want_idx)
+        _weights_within(w, want_w, logits.double())
+
+
+def test_many_tokens_are_ordered_as_in_64_bits():
+    """Enough tokens that some neighbours are closer than fp32 scores tell apart."""
+    logits = torch.randn((40000, 384), generator=_gen(4)) * 1.5
+    balance = torch.randn((384,), generator=_gen(5)) * 0.05
+    for score in ("sigmoid", "softmax"):
+        rule = block.RouterRule(8, score=score, balance=balance.to(DEV), groups=8, top_groups=4)
+        idx, _ = block.select_experts(logits.to(DEV), rule)
+        s = torch.sigmoid(logits.double()) if score == "sigmoid" else torch.softmax(logits.double(), 1)
+        rank = s + balance.double()
+        best = rank.view(-1, 8, 48).topk(2, -1).values.sum(-1)
+        kept = torch.zeros_like(best, dtype=torch.bool).scatter_(1, best.sort(dim=1, descending=True, stable=True).indices[:, :4], True)
+        rank = rank.view(-1, 8, 48).masked_fill(~kept[..., None], -math.inf).view(-1, 384)
+        assert torch.equal(idx.cpu(), rank.sort(dim=1, descending=True, stable=True).indices[:, :8].int())
+
+
+def test_nan_and_infinite_logits():
+    logits = torch.randn((5, 40), generator=_gen(1))
+    logits[0, 7] = math.nan
+    logits[1, 9] = math.inf
+    logits[2] = -math.inf
+    logits[3, 3], logits[3, 4] = -math.nan, -math.inf
+    for score in ("softmax", "sigmoid"):
+        for balance in (None, torch.zeros(40)):
+            rule = block.RouterRule(4, score=score, balance=None if balance is None else balance.to(DEV))
+            idx, w = (t.cpu() for t in block.select_experts(logits.to(DEV), rule))
+            first = [0, 1, 2, 3]
+            assert idx[0].tolist() == first and w[0].isnan().all() and idx[3].tolist() == first and w[3].isnan().all()
+            if score == "softmax":
+                assert idx[1].tolist() == first and w[1].isnan().all()
+            else:
+                assert idx[1, 0] == 9 and abs(float(w[1].sum()) - 1) < 1e-6
+            assert idx[2].tolist() == first and (w[2] == 0).all()
+            assert sorted(set(idx[4].tolist())) == sorted(idx[4].tolist()) and abs(float(w[4].sum()) - 1) < 1e-6
+    balance = torch.zeros(40)
+    balance[5], balance[6] = math.inf, -math.inf   # forced, and out
+    idx, w = (t.cpu() for t in block.select_experts(logits[4:].to(DEV), block.RouterRule(32, balance=balance.to(DEV))))
+    assert idx[0, 0] == 5 and 6 not in idx[0].tolist()
+
+
+def test_gradient_of_an_expert_named_twice_and_of_none():
+    rule = block.RouterRule(4, score="softmax", renormalise=True)
+    logits = torch.randn((1, 12), generator=_gen(3)).to(DEV)
+    idx = torch.tensor([[3, 3, -1, 12]], dtype=torch.int32, device=DEV)
+    w = torch.tensor([[0.25, 0.5, 0.125, 0.125]], device=DEV)
+    dw = torch.tensor([[1.0, 2.0, 4.0, 8.0]], device=DEV)
+    got = block.select_experts_backward(dw, w, idx, logits, rule).cpu()
+    want = torch.zeros(1, 12)
+    want[0, 3] = 0.25 * (1 - 1.25) + 0.5 * (2 - 1.25)   # the mean over the picks that exist: 0.25 + 1
+    assert torch.equal(got, want)
+
+
+# ---------------------------------------------------------------- SwiGLU
+
+def _silu_slack(a):
+    # exp by a scaled power of two (its argument's step, |a| of them), sum, reciprocal, products
+    return (12 + 3 * a.abs()) * U
+
+
+@pytest.mark.parametrize("dtype", ACTS)
+@pytest.mark.parametrize("G,M,H,counts", [(1, 1, 32, None), (1, 37, 352, None), (3, 50, 96, [50, 0, 17]), (6, 41, 544, [41, 1, 0, 30, -3, 99]),
+                                          (2, 130, 2048, [129, 64])])
+def test_swiglu_and_its_gradient(G, M, H, counts, dtype):
+    gen = _gen(G * 100 + M)
+    gate_up, dh = _rand(gen, (G, M, 2 * H), dtype, 0.7), _rand(gen, (G, M, H), dtype)
+    gate_up[0, 0, :5] = torch.tensor([0.0, 30.0, -30.0, 90.0, -90.0], dtype=dtype)
+    n = [M] * G if counts is None else [min(max(c, 0), M) for c in counts]
+    c = None if counts is None else torch.tensor(counts, dtype=torch.int32, device=DEV)
+    mark = torch.full((G, M, H), 7.0, dtype=dtype, device=DEV)
+    saved = block.Mx8Rows.empty((G, M, 2 * H), DEV)
+    saved.codes.fill_(0x55)
+    saved.scales.fill_(0x55)
+    h, q = block.swiglu_checkpoint(gate_up, c, out=mark.clone(), saved=saved)
+    assert q is saved
+    dg, h2 = block.swiglu_backward(dh, saved, c, out=torch.cat([mark, mark], -1), hidden_out=mark.clone())
+    for g in range(G):
+        rest = slice(n[g], M)
+        for t in (h, h2, dg):
+            assert (t[g, rest] == 7).all()
+        assert (saved.codes[g, rest] == 0x55).all() and (saved.scales[g, rest] == 0x55).all()
+        if not n[g]:
+            continue
+        rows = slice(0, n[g])
+        a = R.bits64(gate_up[g, rows])
+        want = R.swiglu(a)
+        _within(h[g, rows], want, want.abs() * _silu_slack(a.chunk(2, -1)[0]) + 2.0 ** -120 * a.abs().amax() ** 2, "h")
+        kept, _ = R.grid8(a)
+        assert torch.equal(R.decode8(saved.codes[g, rows], saved.scales[g, rows]), kept)
+        dwant, hwant = R.swiglu_backward(R.bits64(dh[g, rows]), kept)
+        ka, kb = kept.chunk(2, -1)
+        sg, d = torch.sigmoid(ka), R.bits64(dh[g, rows]).abs()
+        tiny = 2.0 ** -120 * (1 + kept.abs().amax() ** 2)
+        _within(h2[g, rows], hwant, hwant.abs() * _silu_slack(ka) + tiny, "h again")
+        slack = torch.cat([d * kb.abs() * sg * (1 + ka.abs()), d * ka.abs() * sg], -1) * _silu_slack(torch.cat([ka, ka], -1))
+        _within(dg[g, rows], dwant, slack + tiny * (1 + d.max()), "dgate_up")
+    # buffers of the call's own: zeros behind the counts; no h where none is asked for
+    dg2, none = block.swiglu_backward(dh, saved, c, hidden=False)
+    assert none is None
+    for g in range(G):
+        assert torch.equal(dg2[g, :n[g]], dg[g, :n[g]]) and (dg2[g, n[g]:] == 0).all()
+
+
+def test_swiglu_strided_rows_and_two_dimensions():
+    gen = _gen(9)
+    wide = _rand(gen, (20, 2 * 64 + 16), torch.bfloat16)
+    part = wide[:, 8:136]
+    h, saved = block.swiglu_checkpoint(part)
+    h2, saved2 = block.swiglu_checkpoint(part.contiguous())
+    assert torch.equal(h, h2) and torch.equal(saved.codes, saved2.codes)
+    dh = _rand(gen, (20, 72), torch.bfloat16)[:, :64]
+    assert torch.equal(block.swiglu_backward(dh, saved)[0], block.swiglu_backward(dh.contiguous(), saved)[0])
+
+
+def test_swiglu_gradient_by_differences():
+    """At values of the grid the kept values are the values, and the gradient is h's."""
+    gen = _gen(12)
+    a = R.grid8(torch.randn((3, 64), generator=gen, dtype=torch.float64))[0]
+    d = torch.randn((3, 32), generator=gen)
+    _, saved = block.swiglu_checkpoint(a.float().to(DEV))
+    got = block.swiglu_backward(d.to(DEV), saved)[0].cpu().double()
+    step = 1e-5
+    for i, j in ((0, 0), (1, 31), (2, 32), (0, 63)):
+        e = torch.zeros_like(a)
+        e[i, j] = step
+        diff = ((R.swiglu(a + e) - R.swiglu(a - e)) * d.double()).sum() / (2 * step)
+        assert abs(float(diff) - float(got[i, j])) < 1e-5
+
+
+# ---------------------------------------------------------------- streams, graphs, copies
+
+def _calls():
+    """Every operator once, on inputs of its own: (inputs, call that returns tensors)."""
+    gen = _gen(77)
+    x, res, w, dy = (_rand(gen, s, torch.bfloat16) for s in ((200, 512), (200, 512), (512,), (200, 512)))
+    logits, dwt = torch.randn((200, 384), generator=gen).to(DEV), torch.randn((200, 8), generator=gen).to(DEV)
+    rule = block.RouterRule(8, score="sigmoid", balance=(torch.randn((384,), generator=gen) * 0.1).to(DEV), groups=8, top_groups=3)
+    gate_up, dh = _rand(gen, (2, 60, 256), torch.bfloat16), _rand(gen, (2, 60, 128), torch.bfloat16)
+    counts = torch.tensor([60, 31], dtype=torch.int32, device=DEV)
+
+    def call():
+        (y, q), s = block.rms_norm(x, w, residual=res, form="both")
+        dx, dw = block.rms_norm_backward(dy, s, w, dstream=res)
+        idx, wt = block.select_experts(logits, rule)
+        dl = block.select_experts_backward(dwt, wt, idx, logits, rule)
+        h, saved = block.swiglu_checkpoint(gate_up, counts)
+        dg, h2 = block.swiglu_backward(dh, saved, counts)
+        return [y, block.mx8_dequantize(q), block.mx8_dequantize(block.mx8_quantize(x)), s, dx, dw, idx, wt, dl, h, dg, h2]
+
+    return (x, res, dy, logits, gate_up, dh), call
+
+
+def test_captured_calls_replay_on_new_values():
+    inputs, call = _calls()
+    call()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = call()
+    for seed in range(3):
+        gen = torch.Generator(device=DEV).manual_seed(seed)
+        for t in inputs:
+            t.copy_(torch.randn(t.shape, generator=gen, device=DEV))
+        graph.replay()
+        torch.cuda.synchronize()
+        for a, b in zip(out, call()):
+            assert torch.equal(a, b)
+
+
+def test_calls_on_another_stream_and_the_same_bits_again():
+    _, call = _calls()
+    first = call()
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        second = call()
+    third = call()   # beside it
+    side.synchronize()
+    torch.cuda.synchronize()
+    for a, b, c in zip(first, second, third):
+        assert torch.equal(a, b) and torch.equal(a, c)
+
+
+def test_rows_and_rules_can_be_copied():
+    q = block.mx8_quantize(torch.ones((4, 64), device=DEV))
+    for other in (copy.deepcopy(q), pickle.loads(pickle.dumps(q)), q[1:3]):
+        assert isinstance(other, block.Mx8Rows) and (block.mx8_dequantize(other) == 1).all()
+    rule = block.RouterRule(2, score="sigmoid", balance=torch.zeros(8, device=DEV))
+    logits = torch.randn((5, 8), generator=_gen(1)).to(DEV)
+    for other in (copy.deepcopy(rule), pickle.loads(pickle.dumps(rule))):
+        assert torch.equal(block.select_experts(logits, other)[0], block.select_experts(logits, rule)[0])
