@@ -29,7 +29,7 @@ ENTRY_POINTS = ["moe_capacity", "moe_workspace_size", "moe_route", "moe_pack_poo
                 "moe_timing_read",
                 "moe_mx_strides", "moe_mx_quantize", "moe_mx_dequantize", "moe_mx_gemm",
                 "moe_mx_workspace_size", "moe_mx_expert_gemm", "moe_few_workspace_size", "moe_few_tokens",
-                "moe_mxb_strides", "moe_mxb_quantize", "moe_mxb_dequantize", "moe_rms_norm",
+                "moe_mxb_strides", "moe_mxb_quantize", "moe_mxb_dequantize", "moe_mxb_gemm", "moe_rms_norm",
                 "moe_rms_norm_workspace_size", "moe_rms_norm_backward", "moe_select", "moe_select_backward",
                 "moe_swiglu_checkpoint", "moe_swiglu_backward"]
 
@@ -153,6 +153,7 @@ def _load(path):
     L.moe_mxb_strides.argtypes = [_I64, ctypes.POINTER(_I64), ctypes.POINTER(_I64)]
     L.moe_mxb_quantize.argtypes = [_I32, _I64, _I64, _P, _I64, RP, _P]
     L.moe_mxb_dequantize.argtypes = [_I32, _I64, _I64, RP, _P, _I64, _P]
+    L.moe_mxb_gemm.argtypes = [_I32, _I32, _I64, _I64, _I64, RP, _P, RP, _P, _I64, _P]
     L.moe_rms_norm.argtypes = [_I32, _I64, _I64, _P, _I64, _P, _I64, _P, _I32, _F32, _P, _I64, _P, _I64, RP, _P]
     L.moe_rms_norm_workspace_size.argtypes = [_I64, _I64, ctypes.POINTER(ctypes.c_size_t)]
     L.moe_rms_norm_backward.argtypes = [_I32, _I64, _I64, _P, _I64, _P, _I64, _P, _I32, _F32, _P, _I64, _P, _I64, _P, _P, _P]
@@ -351,6 +352,12 @@ def mx8_dequantize(act_dtype, rows, cols, q, out, out_stride_bytes, stream=None)
     """q: MxRowsArg (mx_rows) or None."""
     _check(lib().moe_mxb_dequantize(int(act_dtype), int(rows), int(cols), _ref(q), _ptr(out), int(out_stride_bytes),
                                     _stream(stream)))
+
+
+def mx8_gemm(out_dtype, groups, max_rows, n, k, a, counts, b, out, out_stride_bytes, stream=None):
+    """a, b: MxRowsArg (mx_rows) or None; a of MX-FP8 rows, b of MX-FP4 rows."""
+    _check(lib().moe_mxb_gemm(int(out_dtype), int(groups), int(max_rows), int(n), int(k), _ref(a), _ptr(counts), _ref(b),
+                              _ptr(out), int(out_stride_bytes), _stream(stream)))
 
 
 def rms_norm(act_dtype, rows, cols, x, x_stride_bytes, residual, residual_stride_bytes, weight, weight_dtype, eps, sum_out,

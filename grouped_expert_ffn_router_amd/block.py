@@ -4,7 +4,8 @@
   rows for ``mx8_gemm``, or as both;
 * ``select_experts`` and ``select_experts_backward``: the choice of experts from router logits under a ``RouterRule``;
 * ``swiglu_checkpoint`` and ``swiglu_backward``: the experts' activation, with its inputs kept in 8 bits for the backward pass;
-* ``mx8_quantize``, ``mx8_dequantize``: MX-FP8 rows and back.
+* ``mx8_quantize``, ``mx8_dequantize``: MX-FP8 rows and back; ``mx8_gemm``: their product with MX-FP4 weights
+  (``runner.mx_quantize``), grouped by expert.
 
 Every call works on its tensors' device and that device's current stream, allocates its outputs and scratch with torch's
 allocator (so that it can be captured, and calls on several streams share nothing), and raises ValueError or TypeError for
@@ -96,6 +97,30 @@ def mx8_dequantize(q, dtype=torch.bfloat16):
     with dev:
         out = torch.empty(q.shape, dtype=dtype, device=q.codes.device)
         B.mx8_dequantize(code, q.rows, q.cols, q.arg, out, q.cols * out.element_size(), st)
+    return out
+
+
+def mx8_gemm(a, b, counts=None, out=None, dtype=torch.bfloat16):
+    """out[g] = a[g] . b[g]^T of Mx8Rows a [G, M, K] and runner.MxRows b [G, N, K] (or [M, K] and [N, K]) as bf16 or fp32.
+    counts: int32 [G] rows of each group (the rows of `out` behind them are left as they were; a new `out` has zeros there)."""
+    if not (isinstance(a, Mx8Rows) and isinstance(b, MxRows)):
+        raise TypeError(f"mx8_gemm takes Mx8Rows and MxRows, not {type(a).__name__} and {type(b).__name__}")
+    ca, cb = a.codes, b.codes
+    sa, sb = ca.shape, cb.shape
+    if len(sa) != len(sb) or len(sa) not in (2, 3) or a.cols != b.cols or sa[:-2] != sb[:-2]:
+        raise ValueError(f"mx8_gemm of rows {a.shape} and {b.shape}")
+    G, M = _groups(sa)
+    N = sb[-2]
+    st, dev = _on(ca)
+    _counts(counts, G, ca.device)
+    if cb.device != ca.device:
+        raise ValueError(f"b is on {cb.device}, not on {ca.device}")
+    shape = sa[:-1] + (N,)
+    with dev:
+        if out is None:
+            out = (torch.empty if counts is None else torch.zeros)(shape, dtype=dtype, device=ca.device)
+        _like(out, shape, out.dtype, ca.device, "out")
+        B.mx8_gemm(_code(out, "out"), G, M, N, a.cols, a.arg, counts, b.arg, out, _bytes(out, "out"), st)
     return out
 
 

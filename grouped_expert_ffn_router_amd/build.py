@@ -16,7 +16,7 @@ LIB = os.path.join(PKG, "libmoe.so")
 LIB_DEBUG = os.path.join(PKG, "libmoe_debug.so")
 # block/entry.hip holds the whole C ABI: it includes ops/entry.hip, which includes api.hip
 SOURCES = ["kernels.hip", "block/entry.hip", "ops/mx.hip", "ops/few.hip", "block/rows8.hip", "block/norm.hip",
-           "block/select.hip"]
+           "block/select.hip", "block/mx8_gemm.hip"]
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 FLAGS = [

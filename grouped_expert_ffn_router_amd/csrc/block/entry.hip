@@ -142,6 +142,26 @@ int moe_mxb_dequantize(int32_t act_dtype, int64_t rows, int64_t cols, const moe_
   return MOE_OK;
 }
 
+int moe_mxb_gemm(int32_t out_dtype, int32_t groups, int64_t max_rows, int64_t n, int64_t k, const moe_mx_rows* a,
+                 const int32_t* counts, const moe_mx_rows* b, void* out, int64_t out_stride_bytes, void* stream) {
+  int rc = act_ok(out_dtype);
+  if (rc) return rc;
+  if (groups < 0 || max_rows < 0) return fail(MOE_EINVAL, "groups and max_rows must not be negative");
+  if (n <= 0 || n > (1 << 24)) return fail(MOE_EINVAL, "n must be positive, at most 2^24");
+  if ((rc = mx_cols(k, "k"))) return rc;
+  if (groups > 4096 || max_rows > (1 << 24) || groups * max_rows > (1ll << 30) || groups * n > (1ll << 30) ||
+      groups * ceil_div(max_rows, 256) * ceil_div(n, 256) > (1ll << 21))  // a launch has fewer than 2^32 threads
+    return fail(MOE_EINVAL, "groups, max_rows or n exceed the kernels' index range");
+  if (groups == 0 || max_rows == 0) return MOE_OK;
+  if ((rc = mx8_rows_ok(a, k, "a")) || (rc = mx_rows_ok(b, k, "b"))) return rc;
+  const int64_t size = out_dtype == MOE_ACT_BF16 ? 2 : 4;
+  if ((rc = rows_ok(out, out_stride_bytes, n, size, size, "out"))) return rc;
+  if (counts && ((uintptr_t)counts & 3)) return fail(MOE_EALIGN, "counts is not 4-byte aligned");
+  const MxGemmArgs q{mx_view(a), mx_view(b), counts, groups, (int)max_rows, (int)n, (int)k, out_stride_bytes, out, size == 2};
+  LAUNCH("mx8_gemm", launch_mx8_gemm(q, cu_count(), (hipStream_t)stream), "moe_mxb_gemm");
+  return MOE_OK;
+}
+
 int moe_rms_norm(int32_t act_dtype, int64_t rows, int64_t cols, const void* x, int64_t x_stride_bytes,
                  const void* residual, int64_t residual_stride_bytes, const void* weight, int32_t weight_dtype, float eps,
                  void* sum, int64_t sum_stride_bytes, void* y, int64_t y_stride_bytes, const moe_mx_rows* y8, void* stream) {

@@ -471,6 +471,18 @@ int moe_mxb_quantize(int32_t act_dtype, int64_t rows, int64_t cols, const void* 
 int moe_mxb_dequantize(int32_t act_dtype, int64_t rows, int64_t cols, const moe_mx_rows* q, void* out,
                        int64_t out_stride_bytes, void* stream);
 
+/* Grouped product of MX-FP8 rows with MX-FP4 rows (8-bit activations, 4-bit
+ * weights): as moe_mx_gemm, with
+ *   a        groups * max_rows MX-FP8 rows of k values
+ *   b        groups * n MX-FP4 rows of k values
+ * and its other arguments, limits and errors.  Sums are fp32, but for what the
+ * matrix unit cuts off where it adds eight products: what is 2^-13 and less of
+ * the largest of the eight with a bf16 output (1e-4 of an output's RMS on
+ * normal values), of 2^-19 of the block's largest possible product with an
+ * fp32 one. */
+int moe_mxb_gemm(int32_t out_dtype, int32_t groups, int64_t max_rows, int64_t n, int64_t k, const moe_mx_rows* a,
+                 const int32_t* counts, const moe_mx_rows* b, void* out, int64_t out_stride_bytes, void* stream);
+
 /* ------------------------------------------------------------ norm
  * Root-mean-square norm of rows, with the residual stream's addition before it
  * (a block's norm in front of the layer):
