@@ -16,22 +16,40 @@ namespace {
 template <int TPR_, int NC_>
 struct RowCfg {
   static constexpr int TPR = TPR_, NC = NC_, NT = TPR > 256 ? TPR : 256, RPB = NT / TPR;
+  static_assert(TPR % 64 == 0 && NT % TPR == 0, "whole waves to a row, whole rows to a workgroup");
 };
 
-// Sum over the TPR threads of a row, in all of them, in a fixed order.
-// part: NT / 64 values of LDS, used alternately (slot) by the block's rows.
-template <class C>
-__device__ __forceinline__ float row_sum(float v, float (*part)[C::NT / 64], int slot) {
+// Sums over a wave's lanes, in all of them, in a fixed order: DPP steps inside
+// the rows of 16 lanes, then the rows' sums as scalars.
+__device__ __forceinline__ float wave_total(float v) {
+  auto add = [&](uint32_t moved) { v += __uint_as_float(moved); };
+  add(dpp_move<0xB1>(__float_as_uint(v)));
+  add(dpp_move<0x4E>(__float_as_uint(v)));
+  add(dpp_move<0x141>(__float_as_uint(v)));
+  add(dpp_move<0x140>(__float_as_uint(v)));
+  auto row = [&](int lane) { return __uint_as_float((uint32_t)__builtin_amdgcn_readlane((int)__float_as_uint(v), lane)); };
+  return (row(0) + row(16)) + (row(32) + row(48));
+}
+
+// Sums of K values over the TPR threads of a row, in all of them, with one
+// barrier.  part: K x waves of LDS that the block's next sum must not use.
+template <class C, int K>
+__device__ __forceinline__ void row_sums(float (&v)[K], float (*part)[C::NT / 64]) {
 #pragma unroll
-  for (int off = 32; off > 0; off >>= 1) v += __shfl_xor(v, off);
+  for (int i = 0; i < K; ++i) v[i] = wave_total(v[i]);
   if constexpr (C::TPR > 64) {
-    if ((threadIdx.x & 63) == 0) part[slot][threadIdx.x >> 6] = v;
-    __syncthreads();
-    v = 0.f;
+    if ((threadIdx.x & 63) == 0)
 #pragma unroll
-    for (int i = 0; i < C::TPR / 64; ++i) v += part[slot][i];
+      for (int i = 0; i < K; ++i) part[i][threadIdx.x >> 6] = v[i];
+    __syncthreads();
+    const int first = threadIdx.x / C::TPR * (C::TPR / 64);
+#pragma unroll
+    for (int i = 0; i < K; ++i) {
+      v[i] = 0.f;
+#pragma unroll
+      for (int j = 0; j < C::TPR / 64; ++j) v[i] += part[i][first + j];
+    }
   }
-  return v;
 }
 
 template <class C, class T, int V>
@@ -52,7 +70,7 @@ rms_norm_kernel(NormArgs a) {
     px[i] = have ? piece_load<T, V>(x + (int64_t)c * (V * sizeof(T))) : piece_zero<T, V>();
     pr[i] = have && a.residual ? piece_load<T, V>(res + (int64_t)c * (V * sizeof(T))) : piece_zero<T, V>();
   }
-  float s[C::NC][V], sum = 0.f;
+  float s[C::NC][V], sums[1] = {0.f};
 #pragma unroll
   for (int i = 0; i < C::NC; ++i) {
     float r[V];
@@ -61,11 +79,11 @@ rms_norm_kernel(NormArgs a) {
 #pragma unroll
     for (int v = 0; v < V; ++v) {
       s[i][v] += r[v];
-      sum += s[i][v] * s[i][v];
+      sums[0] += s[i][v] * s[i][v];
     }
   }
-  sum = row_sum<C>(sum, part, 0);
-  const float scale = 1.0f / sqrtf(sum / (float)a.cols + a.eps);
+  row_sums<C>(sums, part);
+  const float scale = 1.0f / sqrtf(sums[0] / (float)a.cols + a.eps);
 #pragma unroll
   for (int i = 0; i < C::NC; ++i) {
     const int c = tid + C::TPR * i;
@@ -95,74 +113,80 @@ rms_norm_kernel(NormArgs a) {
   }
 }
 
-// Workgroup b takes rows b RPB .., b RPB + gridDim RPB .., and keeps the weight's
-// gradient of its threads' columns in registers; one row of partial sums for
-// each RPB-th of a workgroup.
+// Workgroup b takes rows b RPB .., (b + gridDim) RPB .., and keeps the weight and
+// the weight's gradient of its threads' columns in registers; one row of partial
+// sums for each RPB-th of a workgroup.  The next row's values are loaded before
+// this row's sums are waited for (AHEAD; not where a thread has so many pieces
+// that registers would run out).
 template <class C, class T, int V>
 __global__ void __launch_bounds__(C::NT)
 rms_norm_backward_kernel(NormBackArgs a) {
+  constexpr bool AHEAD = C::NC <= 2 && C::NT < 1024;
   __shared__ float part[4][C::NT / 64];
   const int tid = threadIdx.x % C::TPR, sub = threadIdx.x / C::TPR;
   const int pieces = (int)(a.cols / V);
-  float dw[C::NC][V];
+  const int64_t stride = (int64_t)gridDim.x * C::RPB;
+  float dw[C::NC][V], w[C::NC][V];
 #pragma unroll
-  for (int i = 0; i < C::NC; ++i)
+  for (int i = 0; i < C::NC; ++i) {
+    const int c = tid + C::TPR * i;
 #pragma unroll
-    for (int v = 0; v < V; ++v) dw[i][v] = 0.f;
-  int slot = 0;
-  for (int64_t row0 = (int64_t)blockIdx.x * C::RPB; row0 < a.rows; row0 += (int64_t)gridDim.x * C::RPB, slot ^= 2) {
-    const int64_t row = row0 + sub;
-    const bool in = row < a.rows;
-    Piece<T, V> pd[C::NC], ps[C::NC], pt[C::NC];
+    for (int v = 0; v < V; ++v) dw[i][v] = w[i][v] = 0.f;
+    if (c < pieces) weight_values<V>(a.weight, a.weight_f32, (int64_t)c * V, w[i]);
+  }
+  struct Row {
+    Piece<T, V> s[C::NC], d[C::NC], t[C::NC];
+  };
+  auto load = [&](Row& x, int64_t row) {
 #pragma unroll
     for (int i = 0; i < C::NC; ++i) {
       const int c = tid + C::TPR * i;
-      const bool have = in && c < pieces;
+      const bool have = row < a.rows && c < pieces;
       const int64_t at = (int64_t)c * (V * sizeof(T));
-      ps[i] = have ? piece_load<T, V>((const char*)a.s + row * a.lds + at) : piece_zero<T, V>();
-      pd[i] = have ? piece_load<T, V>((const char*)a.dy + row * a.lddy + at) : piece_zero<T, V>();
-      pt[i] = have && a.dstream ? piece_load<T, V>((const char*)a.dstream + row * a.ldds + at) : piece_zero<T, V>();
+      x.s[i] = have ? piece_load<T, V>((const char*)a.s + row * a.lds + at) : piece_zero<T, V>();
+      x.d[i] = have ? piece_load<T, V>((const char*)a.dy + row * a.lddy + at) : piece_zero<T, V>();
+      x.t[i] = have && a.dstream ? piece_load<T, V>((const char*)a.dstream + row * a.ldds + at) : piece_zero<T, V>();
     }
-    float square = 0.f, dot = 0.f;
+  };
+  Row x;
+  if (AHEAD) load(x, (int64_t)blockIdx.x * C::RPB + sub);
+  int slot = 0;
+  for (int64_t row0 = (int64_t)blockIdx.x * C::RPB; row0 < a.rows; row0 += stride, slot ^= 2) {
+    const int64_t row = row0 + sub;
+    if (!AHEAD) load(x, row);
+    float sums[2] = {0.f, 0.f};  // of s^2 and of g s
 #pragma unroll
     for (int i = 0; i < C::NC; ++i) {
-      const int c = tid + C::TPR * i;
-      float s[V], d[V], w[V];
-      piece_values<T, V>(ps[i], s);
-      piece_values<T, V>(pd[i], d);
-      if (c < pieces) {
-        weight_values<V>(a.weight, a.weight_f32, (int64_t)c * V, w);
-      } else {
-#pragma unroll
-        for (int v = 0; v < V; ++v) w[v] = 0.f;
-      }
+      float s[V], d[V];
+      piece_values<T, V>(x.s[i], s);
+      piece_values<T, V>(x.d[i], d);
 #pragma unroll
       for (int v = 0; v < V; ++v) {
-        square += s[v] * s[v];
-        dot += d[v] * w[v] * s[v];
+        sums[0] += s[v] * s[v];
+        sums[1] += d[v] * w[i][v] * s[v];
       }
     }
-    square = row_sum<C>(square, part, slot);
-    dot = row_sum<C>(dot, part, slot + 1);
-    const float r = 1.0f / sqrtf(square / (float)a.cols + a.eps);
-    const float mean = dot * r / (float)a.cols;  // of g n
+    Row next;
+    if (AHEAD) load(next, row + stride);
+    row_sums<C>(sums, part + slot);
+    const float r = 1.0f / sqrtf(sums[0] / (float)a.cols + a.eps);
+    const float mean = sums[1] * r / (float)a.cols;  // of g n
 #pragma unroll
     for (int i = 0; i < C::NC; ++i) {
       const int c = tid + C::TPR * i;
-      if (!in || c >= pieces) continue;
-      float s[V], d[V], w[V], t[V];
-      piece_values<T, V>(ps[i], s);
-      piece_values<T, V>(pd[i], d);
-      piece_values<T, V>(pt[i], t);
-      weight_values<V>(a.weight, a.weight_f32, (int64_t)c * V, w);
+      float s[V], d[V], t[V];
+      piece_values<T, V>(x.s[i], s);
+      piece_values<T, V>(x.d[i], d);
+      piece_values<T, V>(x.t[i], t);
 #pragma unroll
       for (int v = 0; v < V; ++v) {
         const float n = s[v] * r;
         dw[i][v] += d[v] * n;
-        t[v] += r * (d[v] * w[v] - n * mean);
+        t[v] += r * (d[v] * w[i][v] - n * mean);
       }
-      piece_store<T, V>((char*)a.dx + row * a.lddx + (int64_t)c * (V * sizeof(T)), t);
+      if (row < a.rows && c < pieces) piece_store<T, V>((char*)a.dx + row * a.lddx + (int64_t)c * (V * sizeof(T)), t);
     }
+    if (AHEAD) x = next;
   }
   float* out = a.part + ((int64_t)blockIdx.x * C::RPB + sub) * a.cols;
 #pragma unroll
@@ -174,21 +198,23 @@ rms_norm_backward_kernel(NormBackArgs a) {
   }
 }
 
-// Column sums of the partial rows, in a fixed order: 32 columns by 32 threads each.
+// Column sums of the partial rows, in a fixed order: 16 columns by 64 threads each.
 __global__ void __launch_bounds__(1024)
 norm_dweight_kernel(const float* __restrict__ part, int64_t parts, int64_t cols, float* __restrict__ dweight) {
-  __shared__ float sums[32][33];
-  const int cx = threadIdx.x & 31, py = threadIdx.x >> 5;
-  const int64_t col = (int64_t)blockIdx.x * 32 + cx;
+  __shared__ float sums[64][17];
+  const int cx = threadIdx.x & 15, py = threadIdx.x >> 4;
+  const int64_t col = (int64_t)blockIdx.x * 16 + cx;
   float s = 0.f;
-  if (col < cols)
-    for (int64_t p = py; p < parts; p += 32) s += part[p * cols + col];
+  if (col < cols) {
+#pragma unroll 8
+    for (int64_t p = py; p < parts; p += 64) s += part[p * cols + col];
+  }
   sums[py][cx] = s;
   __syncthreads();
-  if (py == 0 && col < cols) {
+  if (threadIdx.x < 16 && col < cols) {
     s = 0.f;
 #pragma unroll
-    for (int i = 0; i < 32; ++i) s += sums[i][cx];
+    for (int i = 0; i < 64; ++i) s += sums[i][cx];
     dweight[col] = s;
   }
 }
@@ -198,14 +224,17 @@ template <int V, class F>
 void with_row(int64_t pieces, F f) {
   if constexpr (V == 1) {
     if (pieces <= 256) f(RowCfg<64, 4>());
-    else if (pieces <= 2048) f(RowCfg<256, 8>());
+    else if (pieces <= 2048) f(RowCfg<512, 4>());
     else f(RowCfg<1024, 16>());
   } else {
     if (pieces <= 64) f(RowCfg<64, 1>());
-    else if (pieces <= 256) f(RowCfg<64, 4>());
-    else if (pieces <= 768) f(RowCfg<256, 3>());
-    else if (pieces <= 2048) f(RowCfg<256, 8>());
-    else f(RowCfg<1024, 4>());
+    else if (pieces <= 128) f(RowCfg<64, 2>());
+    else if (pieces <= 256) f(RowCfg<128, 2>());
+    else if (pieces <= 512) f(RowCfg<256, 2>());
+    else if (pieces <= 768) f(RowCfg<384, 2>());
+    else if (pieces <= 1024) f(RowCfg<512, 2>());
+    else if (V == 8 || pieces <= 2048) f(RowCfg<1024, 2>());  // 16,384 values at most
+    else f(RowCfg<1024, V == 8 ? 2 : 4>());
   }
 }
 
@@ -245,12 +274,14 @@ bool wide(bool bf16, int64_t cols, uintptr_t bits) { return cols % (bf16 ? 8 : 4
 
 }  // namespace
 
-// A multiple of 4, the most rows that a workgroup has at once.  1024 workgroups
-// fill the card four times over; 16 rows or more of each keep the partial sums'
-// bytes below an eighth of the rows'.
+// Partial sums, a multiple of 4 (the rows that a workgroup may have at once):
+// one for each row up to 1024, which fill the card, then one for 16 rows or
+// more, and no more than 1024 workgroups need.
 int64_t norm_parts(int64_t rows, int64_t cols) {
-  const int64_t p = (rows + 15) / 16, most = cols <= 2048 ? 4096 : 1024;
-  return p >= most ? most : (p + 3) / 4 * 4;
+  const int64_t most = cols <= 2048 ? 4096 : 1024, few = rows < 1024 ? rows : 1024;
+  int64_t p = (rows + 15) / 16;
+  p = p < few ? few : p > most ? most : p;
+  return (p + 3) / 4 * 4;
 }
 
 hipError_t launch_rms_norm(const NormArgs& a, hipStream_t st) {
@@ -271,7 +302,7 @@ hipError_t launch_rms_norm_backward(const NormBackArgs& a, hipStream_t st) {
 }
 
 hipError_t launch_norm_dweight(const NormBackArgs& a, hipStream_t st) {
-  launch(norm_dweight_kernel, dim3((unsigned)((a.cols + 31) / 32)), dim3(1024), 0, st, a.part, a.parts, a.cols, a.dweight);
+  launch(norm_dweight_kernel, dim3((unsigned)((a.cols + 15) / 16)), dim3(1024), 0, st, a.part, a.parts, a.cols, a.dweight);
   return hipGetLastError();
 }
 

@@ -27,34 +27,36 @@ __device__ __forceinline__ float rank_value(uint32_t key) {
 }
 constexpr uint32_t OUT_KEY = 0x007fffffu;  // of -infinity: an expert that is out
 
-// Largest value of the wave, in every lane: rotations inside each row of 16
-// lanes, then the four rows' maxima as scalars.
-__device__ __forceinline__ uint32_t wave_max(uint32_t v) {
-  v = max(v, dpp_move<0x128>(v));
-  v = max(v, dpp_move<0x124>(v));
-  v = max(v, dpp_move<0x122>(v));
-  v = max(v, dpp_move<0x121>(v));
-  const uint32_t a = max((uint32_t)__builtin_amdgcn_readlane((int)v, 0), (uint32_t)__builtin_amdgcn_readlane((int)v, 16));
-  const uint32_t b = max((uint32_t)__builtin_amdgcn_readlane((int)v, 32), (uint32_t)__builtin_amdgcn_readlane((int)v, 48));
-  return max(a, b);
-}
+// Sums over the wave in a fixed order, in every lane.
 __device__ __forceinline__ float wave_sum(float v) {
-#pragma unroll
-  for (int off = 32; off > 0; off >>= 1) v += __shfl_xor(v, off);
-  return v;
+  auto add = [&](uint32_t moved) { v += __uint_as_float(moved); };
+  add(dpp_move<0xB1>(__float_as_uint(v)));
+  add(dpp_move<0x4E>(__float_as_uint(v)));
+  add(dpp_move<0x141>(__float_as_uint(v)));
+  add(dpp_move<0x140>(__float_as_uint(v)));
+  auto row = [&](int lane) { return __uint_as_float((uint32_t)__builtin_amdgcn_readlane((int)__float_as_uint(v), lane)); };
+  return (row(0) + row(16)) + (row(32) + row(48));
 }
 __device__ __forceinline__ double wave_sum(double v) {
 #pragma unroll
   for (int off = 32; off > 0; off >>= 1) v += __shfl_xor(v, off);
   return v;
 }
+template <int CTRL>
+__device__ __forceinline__ uint64_t dpp_move64(uint64_t x) {
+  return ((uint64_t)dpp_move<CTRL>((uint32_t)(x >> 32)) << 32) | dpp_move<CTRL>((uint32_t)x);
+}
+__device__ __forceinline__ uint64_t larger(uint64_t a, uint64_t b) { return a > b ? a : b; }
 __device__ __forceinline__ uint64_t wave_max64(uint64_t v) {
-#pragma unroll
-  for (int off = 32; off > 0; off >>= 1) {
-    const uint64_t o = __shfl_xor((unsigned long long)v, off);
-    v = o > v ? o : v;
-  }
-  return v;
+  v = larger(v, dpp_move64<0x128>(v));
+  v = larger(v, dpp_move64<0x124>(v));
+  v = larger(v, dpp_move64<0x122>(v));
+  v = larger(v, dpp_move64<0x121>(v));
+  auto row = [&](int lane) {
+    return ((uint64_t)(uint32_t)__builtin_amdgcn_readlane((int)(v >> 32), lane) << 32) |
+           (uint32_t)__builtin_amdgcn_readlane((int)v, lane);
+  };
+  return larger(larger(row(0), row(16)), larger(row(32), row(48)));
 }
 __device__ __forceinline__ uint64_t rank_key64(double v) {
   const uint64_t u = (uint64_t)__double_as_longlong(v + 0.0);
@@ -65,17 +67,26 @@ __device__ __forceinline__ double rank_value64(uint64_t key) {
 }
 constexpr uint64_t OUT_KEY64 = 0x000fffffffffffffull;
 
+// e^x to about an ulp (results below 2^-126 are 0): the argument's product with
+// log2 e keeps its rounding error, which the power of two is corrected by.
+__device__ __forceinline__ float exp_of(float x) {
+  x = fminf(fmaxf(x, -200.0f), 200.0f);
+  const float hi = x * 1.44269504f;
+  const float lo = fmaf(x, 1.92596299e-8f, fmaf(x, 1.44269504f, -hi));
+  return __builtin_amdgcn_exp2f(hi) * fmaf(lo, 0.693147181f, 1.0f);
+}
+
 struct GroupDiv {  // expert -> group; exact below 2048
   float inv;
   __device__ int of(int e) const { return (int)(((float)e + 0.5f) * inv); }
 };
 
-// One token in fp64: its k picks, pick r in lane r.  Nearly every token is
-// settled by the fp32 scores, so this is written for few registers.
+// One token in fp64: its k picks, pick r in lane r, an expert that is out as its
+// complement.  The lanes have the experts as in the kernel below.
 template <int EPL>
 __device__ __forceinline__ int select_exactly(const SelectRule& r, const float* row, const float* balance, int E, int k,
                                            GroupDiv div) {
-  const int lane = lane_id();
+  const int lane = lane_id(), e0 = lane * EPL;
   double top = 0, inv_sum = 1;
   if (r.score == SOFTMAX) {
     float m = -INFINITY;
@@ -87,110 +98,178 @@ __device__ __forceinline__ int select_exactly(const SelectRule& r, const float* 
     for (int e = lane; e < E; e += 64) s += exp((double)row[e] - top);
     inv_sum = 1.0 / wave_sum(s);
   }
-  auto key_of = [&](int e) -> uint64_t {
-    if (e >= E) return 0;
-    const float l = row[e];
-    if (l == -INFINITY) return OUT_KEY64;
-    const double s = r.score == SOFTMAX ? exp((double)l - top) * inv_sum : 1.0 / (1.0 + exp(-(double)l));
-    return rank_key64(balance ? s + (double)balance[e] : s);
-  };
-  uint64_t kept = ~0ull;
+  uint64_t key[EPL];
+#pragma unroll
+  for (int j = 0; j < EPL; ++j) {
+    const int e = min(e0 + j, E - 1);
+    const double l = row[e];
+    const double s = r.score == SOFTMAX ? exp(l - top) * inv_sum : 1.0 / (1.0 + exp(-l));
+    key[j] = l == -INFINITY ? OUT_KEY64 : rank_key64(balance ? s + (double)balance[e] : s);
+    if (e0 + j >= E) key[j] = 0;
+    __builtin_amdgcn_sched_barrier(0);  // one after the other: side by side they take hundreds of registers
+  }
   if (r.top_groups < r.groups) {
-    // lane g ends up with the score of group g
-    uint64_t mine = 0;
+    uint64_t mine = 0;  // lane g: the score of group g
     for (int g = 0; g < r.groups; ++g) {
       uint64_t a = 0, b = 0;  // this lane's two best of the group
+#pragma unroll
       for (int j = 0; j < EPL; ++j) {
-        const int e = lane + 64 * j;
-        if (e < E && div.of(e) == g) {
-          const uint64_t x = key_of(e);
-          if (x > a) { b = a; a = x; }
-          else if (x > b) b = x;
-        }
+        const uint64_t x = div.of(e0 + j) == g ? key[j] : 0;
+        if (x > a) { b = a; a = x; }
+        else if (x > b) b = x;
       }
       const uint64_t first = wave_max64(a);
-      const uint64_t owner = __ballot(a == first);
-      const uint64_t second = wave_max64(lane == __ffsll((unsigned long long)owner) - 1 ? b : a);
+      const int owner = __ffsll((unsigned long long)__ballot(a == first)) - 1;
+      const uint64_t second = wave_max64(lane == owner ? b : a);
       uint64_t score = first;
       if (r.group_best > 1 && second > OUT_KEY64) score = rank_key64(rank_value64(first) + rank_value64(second));
       if (lane == g) mine = score;
     }
     int better = 0;
     for (int g = 0; g < r.groups; ++g) {
-      const uint64_t other = __shfl((unsigned long long)mine, g);
+      const uint64_t other = ((uint64_t)(uint32_t)__builtin_amdgcn_readlane((int)(mine >> 32), g) << 32) |
+                             (uint32_t)__builtin_amdgcn_readlane((int)mine, g);
       better += other > mine || (other == mine && g < lane);
     }
-    kept = __ballot(lane < r.groups && better < r.top_groups);
+    const uint64_t kept = __ballot(lane < r.groups && better < r.top_groups);
+#pragma unroll
+    for (int j = 0; j < EPL; ++j) {
+      const int e = e0 + j;
+      if (e >= E) continue;
+      if (!(kept >> div.of(e) & 1)) key[j] = OUT_KEY64;
+      else if (!balance) key[j] = rank_key64((double)row[e]);
+    }
   }
-  uint32_t picked = 0;  // bit j: this lane's expert lane + 64 j
   int my = 0;
   for (int i = 0; i < k; ++i) {
     uint64_t best = 0;
     int at = 0;
-    for (int j = 0; j < EPL; ++j) {
-      const int e = lane + 64 * j;
-      if (e >= E || (picked >> j & 1)) continue;
-      uint64_t x = balance ? key_of(e) : rank_key64((double)row[e]);
-      if (!(kept >> div.of(e) & 1)) x = OUT_KEY64;
-      if (x > best) { best = x; at = j; }
-    }
-    const uint64_t top_key = wave_max64(best);
-    int e = best == top_key ? lane + 64 * at : 1 << 30;
 #pragma unroll
-    for (int off = 32; off > 0; off >>= 1) e = min(e, __shfl_xor(e, off));
-    if ((e & 63) == lane) picked |= 1u << (e >> 6);
-    // an expert that is out is marked by its sign
-    if (lane == i) my = top_key == OUT_KEY64 ? ~e : e;
+    for (int j = 0; j < EPL; ++j)
+      if (key[j] > best) { best = key[j]; at = j; }
+    const uint64_t top_key = wave_max64(best);
+    const int owner = __ffsll((unsigned long long)__ballot(best == top_key)) - 1;
+    const int e = owner * EPL + __builtin_amdgcn_readlane(at, owner);
+#pragma unroll
+    for (int j = 0; j < EPL; ++j)
+      if (e0 + j == e) key[j] = 0;
+    if (lane == i) my = top_key <= OUT_KEY64 ? ~e : e;
   }
   return my;
 }
 
-// One wave per token.  A lane has the experts lane + 64 j; EPL = how many.
+// Largest value of the wave as a scalar: rotations inside each row of 16 lanes,
+// then row 0 (2) into row 1 (3) and rows 0 and 1 into 2 and 3.
+__device__ __forceinline__ uint32_t wave_top(uint32_t v) {
+  v = max(v, dpp_move<0x128>(v));
+  v = max(v, dpp_move<0x124>(v));
+  v = max(v, dpp_move<0x122>(v));
+  v = max(v, dpp_move<0x121>(v));
+  v = max(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x142, 0xa, 0xf, false));
+  v = max(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x143, 0xc, 0xf, false));
+  return (uint32_t)__builtin_amdgcn_readlane((int)v, 63);
+}
+
+// Descending order of N registers: Batcher's odd-even merge sort of the next
+// power of two, without the exchanges that would reach past N.
+template <int N>
+__device__ __forceinline__ void sort_down(uint32_t (&v)[N]) {
+  constexpr int P = N <= 1 ? 1 : N <= 2 ? 2 : N <= 4 ? 4 : N <= 8 ? 8 : N <= 16 ? 16 : 32;
+#pragma unroll
+  for (int p = 1; p < P; p *= 2)
+#pragma unroll
+    for (int q = p; q >= 1; q /= 2)
+#pragma unroll
+      for (int j = q % p; j + q < P; j += 2 * q)
+#pragma unroll
+        for (int i = 0; i < q; ++i)
+          if ((i + j) / (2 * p) == (i + j + q) / (2 * p) && i + j + q < N) {
+            const uint32_t a = v[i + j], b = v[i + j + q];
+            v[i + j] = max(a, b);
+            v[i + j + q] = min(a, b);
+          }
+}
+
+// The two largest of this lane's and another lane's pair.
+__device__ __forceinline__ void merge_two(uint32_t& a, uint32_t& b, uint32_t a2, uint32_t b2) {
+  b = max(max(b, b2), min(a, a2));
+  a = max(a, a2);
+}
+
+// One wave per token.  A lane has the experts EPL lane .. EPL lane + EPL - 1, so
+// that of equal keys the lower lane's, and in a lane the lower register's, is
+// the lower expert's.  Each lane sorts its keys once; a round of the choice is
+// then a maximum over the lanes' first keys (6 DPP steps), the lane that holds
+// it, and a shift of that lane's keys.  Which expert a key was is looked up
+// once at the end.
+//
+// Bound by instructions (about 250 a wave without groups and bias), not by the
+// 4 E bytes a token.  `wide`: rows may be read 8 or 16 bytes at a time.
 template <int EPL>
 __global__ void __launch_bounds__(256)
 select_rule_kernel(SelectRule r, const float* __restrict__ logits, int64_t ld, const float* __restrict__ balance, int64_t T,
-                   int E, int k, int32_t* __restrict__ idx, float* __restrict__ w) {
-  const int64_t t = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
-  const int lane = lane_id();
+                   int E, int k, bool wide, int32_t* __restrict__ idx, float* __restrict__ w) {
+  constexpr int W = EPL % 4 == 0 ? 4 : EPL % 2 == 0 ? 2 : 1;
+  const int64_t t = (int64_t)blockIdx.x * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int lane = lane_id(), e0 = lane * EPL;
   if (t >= T) return;
   const float* row = logits + t * ld;
-  const GroupDiv div{(float)r.groups / (float)E};
   const bool grouped = r.top_groups < r.groups;
-  const bool scores = grouped || balance;  // else the logits rank
-  float l[EPL], v[EPL];
+  const bool full = E == 64 * EPL;  // else lanes past the last expert read it again and drop what they read
+  float l[EPL];
+  if (wide) {
+#pragma unroll
+    for (int j = 0; j < EPL; j += W) {
+      const float* at = row + min(e0 + j, E - W);
+      if constexpr (W == 4) {
+        const float4 d = *(const float4*)at;
+        l[j] = d.x; l[j + 1] = d.y; l[j + 2] = d.z; l[j + 3] = d.w;
+      } else if constexpr (W == 2) {
+        const float2 d = *(const float2*)at;
+        l[j] = d.x; l[j + 1] = d.y;
+      } else {
+        l[j] = *at;
+      }
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < EPL; ++j) l[j] = row[min(e0 + j, E - 1)];
+  }
+  if (!full) {
+#pragma unroll
+    for (int j = 0; j < EPL; ++j)
+      if (e0 + j >= E) l[j] = -INFINITY;
+  }
   bool bad = false;
 #pragma unroll
-  for (int j = 0; j < EPL; ++j) {
-    const int e = lane + 64 * j;
-    l[j] = e < E ? row[e] : -INFINITY;
-    bad |= !(l[j] == l[j]);
-  }
+  for (int j = 0; j < EPL; ++j) bad |= !(l[j] == l[j]);
   float top = 0.f, inv_sum = 1.f;
   if (r.score == SOFTMAX) {
     float m = l[0];
 #pragma unroll
     for (int j = 1; j < EPL; ++j) m = fmaxf(m, l[j]);
-    top = rank_value(wave_max(rank_key(m)));
+    top = rank_value(wave_top(rank_key(m)));
     bad |= top == INFINITY;
-    if (scores || !r.renorm) {
+    if (grouped || balance || !r.renorm) {
       float s = 0.f;
 #pragma unroll
-      for (int j = 0; j < EPL; ++j) s += l[j] == -INFINITY ? 0.f : expf(l[j] - top);
+      for (int j = 0; j < EPL; ++j) s += l[j] == -INFINITY ? 0.f : exp_of(l[j] - top);
       inv_sum = 1.0f / wave_sum(s);
     }
   }
-  auto score_of = [&](float x) {
-    if (x == -INFINITY) return 0.f;
-    return r.score == SOFTMAX ? expf(x - top) * inv_sum : 1.0f / (1.0f + expf(-x));
-  };
+  // orig: the keys that rank; the scores where a bias is added to them, else the logits
+  uint32_t orig[EPL];
 #pragma unroll
-  for (int j = 0; j < EPL; ++j) {
-    const int e = lane + 64 * j;
-    v[j] = l[j];
-    if (scores && l[j] != -INFINITY) {
-      v[j] = score_of(l[j]);
-      if (balance) v[j] += balance[e];
-      bad |= !(v[j] == v[j]);
+  for (int j = 0; j < EPL; ++j) orig[j] = rank_key(l[j]);
+  uint32_t score[EPL];
+  if (grouped || balance) {
+#pragma unroll
+    for (int j = 0; j < EPL; ++j) {
+      float v = r.score == SOFTMAX ? __expf(l[j] - top) * inv_sum : __builtin_amdgcn_rcpf(1.0f + __expf(-l[j]));
+      if (balance) v += balance[min(e0 + j, E - 1)];
+      if (l[j] == -INFINITY) v = -INFINITY;
+      bad |= !(v == v);
+      score[j] = rank_key(v);
     }
   }
   if (__any(bad)) {  // no order: the first k experts, their weights NaN
@@ -200,95 +279,141 @@ select_rule_kernel(SelectRule r, const float* __restrict__ logits, int64_t ld, c
     }
     return;
   }
-  uint32_t key[EPL];
+  if (balance) {
 #pragma unroll
-  for (int j = 0; j < EPL; ++j) key[j] = lane + 64 * j < E ? rank_key(v[j]) : 0u;
-  // the largest score bounds how far scores are off (a few units in the last place)
-  const float unit = 0x1p-20f * (r.score == SOFTMAX ? inv_sum : 1.0f);
+    for (int j = 0; j < EPL; ++j) orig[j] = score[j];
+  }
+  if (!full) {  // below every expert's key
+#pragma unroll
+    for (int j = 0; j < EPL; ++j)
+      if (e0 + j >= E) orig[j] = score[j] = 0u;
+  }
+  // How far two scores' difference may be off.  Sigmoid: exp, its argument (times
+  // a derivative of 1/4 at most), sum and reciprocal give 3 2^-24 a score; softmax:
+  // of the largest score, exp and its argument 3 2^-24, the sum EPL + 8.
+  const float unit = r.score == SOFTMAX ? inv_sum * ((EPL + 12) * 0x1p-23f) : 0x1p-21f;
+  const GroupDiv div{(float)r.groups / (float)E};
   bool close = false;
   if (grouped) {
-    uint32_t mine = 0;
-    for (int g = 0; g < r.groups; ++g) {
-      uint32_t a = 0, b = 0;
+    // Groups of whole lanes, a power of two of them, are reduced side by side
+    // in their lanes; others one after the other, group g's score in lane g.
+    const int per = E / r.groups, seg = per / EPL;
+    const bool aligned = seg * EPL == per && (seg & (seg - 1)) == 0;
+    const int gid = aligned ? lane >> (__ffs(seg) - 1) : lane, stride = aligned ? seg : 1;
+    uint32_t a = 0, b = 0;
+    if (aligned) {
 #pragma unroll
       for (int j = 0; j < EPL; ++j) {
-        const uint32_t x = lane + 64 * j < E && div.of(lane + 64 * j) == g ? key[j] : 0u;
-        b = max(b, min(a, x));
-        a = max(a, x);
+        b = max(b, min(a, score[j]));
+        a = max(a, score[j]);
       }
-      const uint32_t first = wave_max(a);
-      const uint64_t owner = __ballot(a == first);
-      const uint32_t second = wave_max(lane == __ffsll((unsigned long long)owner) - 1 ? b : a);
-      uint32_t s = first;
-      if (r.group_best > 1 && second > OUT_KEY) s = rank_key(rank_value(first) + rank_value(second));
-      if (lane == g) mine = s;
+      if (seg > 1) merge_two(a, b, dpp_move<0xB1>(a), dpp_move<0xB1>(b));
+      if (seg > 2) merge_two(a, b, dpp_move<0x4E>(a), dpp_move<0x4E>(b));
+      if (seg > 4) merge_two(a, b, dpp_move<0x141>(a), dpp_move<0x141>(b));
+      if (seg > 8) merge_two(a, b, dpp_move<0x140>(a), dpp_move<0x140>(b));
+      if (seg > 16) merge_two(a, b, (uint32_t)__shfl_xor((int)a, 16), (uint32_t)__shfl_xor((int)b, 16));
+      if (seg > 32) merge_two(a, b, (uint32_t)__shfl_xor((int)a, 32), (uint32_t)__shfl_xor((int)b, 32));
+    } else {
+      for (int g = 0; g < r.groups; ++g) {
+        uint32_t x = 0, y = 0;
+#pragma unroll
+        for (int j = 0; j < EPL; ++j) {
+          const uint32_t s = div.of(e0 + j) == g ? score[j] : 0u;
+          y = max(y, min(x, s));
+          x = max(x, s);
+        }
+        const uint32_t first = wave_top(x);
+        const int owner = __ffsll((unsigned long long)__ballot(x == first)) - 1;
+        const uint32_t second = wave_top(lane == owner ? y : x);
+        if (lane == g) { a = first; b = second; }
+      }
     }
+    uint32_t mine = a;
+    if (r.group_best > 1 && b > OUT_KEY) mine = rank_key(rank_value(a) + rank_value(b));
     int better = 0;
     for (int g = 0; g < r.groups; ++g) {
-      const uint32_t other = (uint32_t)__builtin_amdgcn_readlane((int)mine, g);
-      better += other > mine || (other == mine && g < lane);
+      const uint32_t other = (uint32_t)__builtin_amdgcn_readlane((int)mine, g * stride);
+      better += other > mine || (other == mine && g < gid);
     }
-    const uint64_t kept = __ballot(lane < r.groups && better < r.top_groups);
+    const bool keep = gid < r.groups && better < r.top_groups;
     // the last group kept and the first one dropped; two that are out tie by index
-    const int last = __ffsll((unsigned long long)__ballot(lane < r.groups && better == r.top_groups - 1)) - 1;
-    const int next = __ffsll((unsigned long long)__ballot(lane < r.groups && better == r.top_groups)) - 1;
+    const int last = __ffsll((unsigned long long)__ballot(gid < r.groups && better == r.top_groups - 1)) - 1;
+    const int next = __ffsll((unsigned long long)__ballot(gid < r.groups && better == r.top_groups)) - 1;
     const uint32_t klast = (uint32_t)__builtin_amdgcn_readlane((int)mine, last);
     const uint32_t knext = (uint32_t)__builtin_amdgcn_readlane((int)mine, next);
     if (knext > OUT_KEY) {
-      const float a = rank_value(klast), b = rank_value(knext);
-      close |= !(a - b > 2 * unit + 0x1p-20f * (fabsf(a) + fabsf(b)));
+      const float x = rank_value(klast), y = rank_value(knext);
+      close |= !(x - y > 2 * unit + 0x1p-22f * (fabsf(x) + fabsf(y)));
     }
-#pragma unroll
-    for (int j = 0; j < EPL; ++j) {
-      if (lane + 64 * j >= E) continue;
-      if (!balance) key[j] = rank_key(l[j]);
-      if (!(kept >> div.of(lane + 64 * j) & 1)) key[j] = OUT_KEY;
-    }
-  }
-  // k rounds of a maximum over the wave, and one more to see how near the next one is
-  int my = 0;
-  uint32_t before = 0;
-  const int rounds = balance && k < E ? k + 1 : k;
-  for (int i = 0; i < rounds; ++i) {
-    uint32_t m = key[0];
-#pragma unroll
-    for (int j = 1; j < EPL; ++j) m = max(m, key[j]);
-    m = wave_max(m);
-    if (balance && i > 0 && m > OUT_KEY) {
-      const float a = rank_value(before), b = rank_value(m);
-      close |= !(a - b > unit + 0x1p-20f * (fabsf(a) + fabsf(b)));
-    }
-    before = m;
-    int e = 0;
-    bool found = false;
-#pragma unroll
-    for (int j = 0; j < EPL; ++j) {
-      const uint64_t who = __ballot(key[j] == m);
-      if (who && !found) {
-        e = 64 * j + __ffsll((unsigned long long)who) - 1;
-        found = true;
-      }
-    }
+    const uint64_t kept = __ballot(keep);
 #pragma unroll
     for (int j = 0; j < EPL; ++j)
-      if (lane + 64 * j == e) key[j] = 0u;
-    if (lane == i) my = m == OUT_KEY ? ~e : e;
+      if (!(aligned ? keep : kept >> (div.of(e0 + j) & 63) & 1)) orig[j] = min(orig[j], OUT_KEY);
   }
-  if (close) my = select_exactly<EPL>(r, row, balance, E, k, div);
-  const bool out = my < 0;
-  const int e = out ? ~my : my;
+  // k rounds, and one more to see how near the next key is
+  uint32_t key[EPL];
+#pragma unroll
+  for (int j = 0; j < EPL; ++j) key[j] = orig[j];
+  sort_down<EPL>(key);
+  int from = 0, chosen = 0;  // lane i: the lane that held pick i, and its key
+  const int rounds = balance && k < E ? k + 1 : k;
+  for (int i = 0; i < rounds; ++i) {
+    const uint32_t m = wave_top(key[0]);
+    const int owner = __ffsll((unsigned long long)__ballot(key[0] == m)) - 1;
+    from = lane == i ? owner : from;
+    chosen = lane == i ? (int)m : chosen;
+    const bool pop = lane == owner;
+#pragma unroll
+    for (int j = 0; j < EPL; ++j) {  // (values, not places, to choose from: an array indexed by `pop` would be spelled out)
+      const uint32_t stay = key[j], next = j + 1 < EPL ? key[j + 1] : 0u;
+      key[j] = pop ? next : stay;
+    }
+  }
+  const uint32_t mk = (uint32_t)chosen;
+  if (balance) {
+    const uint32_t after = (uint32_t)__shfl_down(chosen, 1);
+    if (lane + 1 < rounds && after > OUT_KEY) {
+      const float x = rank_value(mk), y = rank_value(after);
+      close |= !(x - y > unit + 0x1p-23f * (fabsf(x) + fabsf(y)));
+    }
+  }
+  int e;
+  bool out;
+  if (__any(close)) {
+    const int my = select_exactly<EPL>(r, row, balance, E, k, div);
+    out = my < 0;
+    e = out ? ~my : my;
+  } else {
+    // a lane's equal keys were taken in the order of its registers
+    int nth = 0;
+    const int from1 = __shfl_up(from, 1), chosen1 = __shfl_up(chosen, 1);
+    if (__any(lane > 0 && lane < k && from1 == from && chosen1 == chosen))
+      for (int d = 1; d < k; ++d) {
+        const int from_d = __shfl(from, lane - d), chosen_d = __shfl(chosen, lane - d);
+        nth += lane >= d && from_d == from && chosen_d == chosen;
+      }
+    int at = 0;
+#pragma unroll
+    for (int j = 0; j < EPL; ++j) {
+      if ((uint32_t)__shfl((int)orig[j], from) == mk) {
+        at = nth == 0 ? j : at;
+        --nth;
+      }
+    }
+    e = from * EPL + at;
+    out = mk <= OUT_KEY;
+  }
   float x = -INFINITY;
   if (lane < k && !out) x = row[e];
+  // a hardware reciprocal where a quotient is wanted: within an ulp
   float s;
-  if (r.score == SOFTMAX && r.renorm) {  // relative to the largest that was chosen
-    const float m = rank_value(wave_max(rank_key(x)));
-    s = x == -INFINITY ? 0.f : expf(x - m);
-  } else {
-    s = score_of(x);
-  }
+  if (r.score == SOFTMAX && r.renorm) s = exp_of(x - rank_value(wave_top(rank_key(x))));  // relative to the largest chosen
+  else if (r.score == SOFTMAX) s = exp_of(x - top) * inv_sum;
+  else s = __builtin_amdgcn_rcpf(1.0f + exp_of(-x));
+  s = x == -INFINITY ? 0.f : s;
   if (r.renorm) {
     const float sum = wave_sum(s);
-    s = sum > 0.f ? s / sum : 0.f;
+    s = sum > 0.f ? s * __builtin_amdgcn_rcpf(sum) : 0.f;
   }
   if (lane < k) {
     idx[t * k + lane] = e;
@@ -386,7 +511,10 @@ hipError_t launch_select_rule(const SelectRule& r, const float* logits, int64_t 
     const float* l = logits + t * ld;
     int32_t* i = idx + t * k;
     float* o = w + t * k;
-#define SEL(N) launch(select_rule_kernel<N>, grid, dim3(256), 0, st, r, l, ld, balance, n, E, k, i, o)
+    // the bytes that a lane reads at a time: 4 values, or 2, where it has a multiple of them
+    const auto wide = [&](int n) { return E % n == 0 && ld % n == 0 && (uintptr_t)l % (4 * n) == 0; };
+#define SEL(N) \
+  launch(select_rule_kernel<N>, grid, dim3(256), 0, st, r, l, ld, balance, n, E, k, wide(N % 4 == 0 ? 4 : N % 2 == 0 ? 2 : 1), i, o)
     if (epl <= 1) SEL(1);
     else if (epl <= 2) SEL(2);
     else if (epl <= 4) SEL(4);
