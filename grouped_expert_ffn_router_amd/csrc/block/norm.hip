@@ -52,7 +52,7 @@ __device__ __forceinline__ void row_sums(float (&v)[K], float (*part)[C::NT / 64
   }
 }
 
-template <class C, class T, int V>
+template <class C, class T, int V, bool STREAM>
 __global__ void __launch_bounds__(C::NT)
 rms_norm_kernel(NormArgs a) {
   __shared__ float part[1][C::NT / 64];
@@ -67,8 +67,8 @@ rms_norm_kernel(NormArgs a) {
   for (int i = 0; i < C::NC; ++i) {
     const int c = tid + C::TPR * i;
     const bool have = in && c < pieces;
-    px[i] = have ? piece_load<T, V>(x + (int64_t)c * (V * sizeof(T))) : piece_zero<T, V>();
-    pr[i] = have && a.residual ? piece_load<T, V>(res + (int64_t)c * (V * sizeof(T))) : piece_zero<T, V>();
+    px[i] = have ? piece_load<T, V, STREAM>(x + (int64_t)c * (V * sizeof(T))) : piece_zero<T, V>();
+    pr[i] = have && a.residual ? piece_load<T, V, STREAM>(res + (int64_t)c * (V * sizeof(T))) : piece_zero<T, V>();
   }
   float s[C::NC][V], sums[1] = {0.f};
 #pragma unroll
@@ -88,7 +88,7 @@ rms_norm_kernel(NormArgs a) {
   for (int i = 0; i < C::NC; ++i) {
     const int c = tid + C::TPR * i;
     const bool have = in && c < pieces;
-    if (have && a.stream) piece_store<T, V>((char*)a.stream + row * a.lds + (int64_t)c * (V * sizeof(T)), s[i]);
+    if (have && a.stream) piece_store<T, V, STREAM>((char*)a.stream + row * a.lds + (int64_t)c * (V * sizeof(T)), s[i]);
     float w[V];
     if (have) {
       weight_values<V>(a.weight, a.weight_f32, (int64_t)c * V, w);
@@ -98,7 +98,7 @@ rms_norm_kernel(NormArgs a) {
     }
 #pragma unroll
     for (int v = 0; v < V; ++v) w[v] = s[i][v] * scale * w[v];
-    if (have && a.y) piece_store<T, V>((char*)a.y + row * a.ldy + (int64_t)c * (V * sizeof(T)), w);
+    if (have && a.y) piece_store<T, V, STREAM>((char*)a.y + row * a.ldy + (int64_t)c * (V * sizeof(T)), w);
     if constexpr (V > 1) {
       if (a.q.codes) {  // from the fp32 values: rounded once
         uint32_t codes[V / 4];
@@ -118,7 +118,7 @@ rms_norm_kernel(NormArgs a) {
 // sums for each RPB-th of a workgroup.  The next row's values are loaded before
 // this row's sums are waited for (AHEAD; not where a thread has so many pieces
 // that registers would run out).
-template <class C, class T, int V>
+template <class C, class T, int V, bool STREAM>
 __global__ void __launch_bounds__(C::NT)
 rms_norm_backward_kernel(NormBackArgs a) {
   constexpr bool AHEAD = C::NC <= 2 && C::NT < 1024;
@@ -143,9 +143,9 @@ rms_norm_backward_kernel(NormBackArgs a) {
       const int c = tid + C::TPR * i;
       const bool have = row < a.rows && c < pieces;
       const int64_t at = (int64_t)c * (V * sizeof(T));
-      x.s[i] = have ? piece_load<T, V>((const char*)a.s + row * a.lds + at) : piece_zero<T, V>();
-      x.d[i] = have ? piece_load<T, V>((const char*)a.dy + row * a.lddy + at) : piece_zero<T, V>();
-      x.t[i] = have && a.dstream ? piece_load<T, V>((const char*)a.dstream + row * a.ldds + at) : piece_zero<T, V>();
+      x.s[i] = have ? piece_load<T, V, STREAM>((const char*)a.s + row * a.lds + at) : piece_zero<T, V>();
+      x.d[i] = have ? piece_load<T, V, STREAM>((const char*)a.dy + row * a.lddy + at) : piece_zero<T, V>();
+      x.t[i] = have && a.dstream ? piece_load<T, V, STREAM>((const char*)a.dstream + row * a.ldds + at) : piece_zero<T, V>();
     }
   };
   Row x;
@@ -184,7 +184,7 @@ rms_norm_backward_kernel(NormBackArgs a) {
         dw[i][v] += d[v] * n;
         t[v] += r * (d[v] * w[i][v] - n * mean);
       }
-      if (row < a.rows && c < pieces) piece_store<T, V>((char*)a.dx + row * a.lddx + (int64_t)c * (V * sizeof(T)), t);
+      if (row < a.rows && c < pieces) piece_store<T, V, STREAM>((char*)a.dx + row * a.lddx + (int64_t)c * (V * sizeof(T)), t);
     }
     if (AHEAD) x = next;
   }
@@ -238,7 +238,7 @@ void with_row(int64_t pieces, F f) {
   }
 }
 
-template <class T, int V>
+template <class T, int V, bool STREAM>
 hipError_t run_norm(const NormArgs& a, hipStream_t st) {
   with_row<V>(a.cols / V, [&](auto cfg) {
     using C = decltype(cfg);
@@ -254,17 +254,17 @@ hipError_t run_norm(const NormArgs& a, hipStream_t st) {
         b.q.codes += r * a.q.ldc;
         b.q.scales += r * a.q.lds;
       }
-      launch((rms_norm_kernel<C, T, V>), dim3((unsigned)((b.rows + C::RPB - 1) / C::RPB)), dim3(C::NT), 0, st, b);
+      launch((rms_norm_kernel<C, T, V, STREAM>), dim3((unsigned)((b.rows + C::RPB - 1) / C::RPB)), dim3(C::NT), 0, st, b);
     }
   });
   return hipGetLastError();
 }
 
-template <class T, int V>
+template <class T, int V, bool STREAM>
 hipError_t run_norm_backward(const NormBackArgs& a, hipStream_t st) {
   with_row<V>(a.cols / V, [&](auto cfg) {
     using C = decltype(cfg);
-    launch((rms_norm_backward_kernel<C, T, V>), dim3((unsigned)(a.parts / C::RPB)), dim3(C::NT), 0, st, a);
+    launch((rms_norm_backward_kernel<C, T, V, STREAM>), dim3((unsigned)(a.parts / C::RPB)), dim3(C::NT), 0, st, a);
   });
   return hipGetLastError();
 }
@@ -289,16 +289,22 @@ hipError_t launch_rms_norm(const NormArgs& a, hipStream_t st) {
   if (a.residual) bits |= (uintptr_t)a.residual | (uintptr_t)a.ldr;
   if (a.stream) bits |= (uintptr_t)a.stream | (uintptr_t)a.lds;
   if (a.y) bits |= (uintptr_t)a.y | (uintptr_t)a.ldy;
-  if (wide(a.bf16, a.cols, bits)) return a.bf16 ? run_norm<bf16_t, 8>(a, st) : run_norm<float, 4>(a, st);
-  return a.bf16 ? run_norm<bf16_t, 1>(a, st) : run_norm<float, 1>(a, st);
+  if (!wide(a.bf16, a.cols, bits)) return a.bf16 ? run_norm<bf16_t, 1, false>(a, st) : run_norm<float, 1, false>(a, st);
+  const int64_t rows = 1 + (a.residual != nullptr) + (a.stream != nullptr) + (a.y != nullptr);
+  if (rows * a.rows * a.cols * (a.bf16 ? 2 : 4) > STREAM_BYTES)
+    return a.bf16 ? run_norm<bf16_t, 8, true>(a, st) : run_norm<float, 4, true>(a, st);
+  return a.bf16 ? run_norm<bf16_t, 8, false>(a, st) : run_norm<float, 4, false>(a, st);
 }
 
 hipError_t launch_rms_norm_backward(const NormBackArgs& a, hipStream_t st) {
   uintptr_t bits = (uintptr_t)a.dy | (uintptr_t)a.lddy | (uintptr_t)a.s | (uintptr_t)a.lds | (uintptr_t)a.dx |
                    (uintptr_t)a.lddx | (uintptr_t)a.weight;
   if (a.dstream) bits |= (uintptr_t)a.dstream | (uintptr_t)a.ldds;
-  if (wide(a.bf16, a.cols, bits)) return a.bf16 ? run_norm_backward<bf16_t, 8>(a, st) : run_norm_backward<float, 4>(a, st);
-  return a.bf16 ? run_norm_backward<bf16_t, 1>(a, st) : run_norm_backward<float, 1>(a, st);
+  if (!wide(a.bf16, a.cols, bits))
+    return a.bf16 ? run_norm_backward<bf16_t, 1, false>(a, st) : run_norm_backward<float, 1, false>(a, st);
+  if ((a.dstream ? 4 : 3) * a.rows * a.cols * (a.bf16 ? 2 : 4) > STREAM_BYTES)
+    return a.bf16 ? run_norm_backward<bf16_t, 8, true>(a, st) : run_norm_backward<float, 4, true>(a, st);
+  return a.bf16 ? run_norm_backward<bf16_t, 8, false>(a, st) : run_norm_backward<float, 4, false>(a, st);
 }
 
 hipError_t launch_norm_dweight(const NormBackArgs& a, hipStream_t st) {

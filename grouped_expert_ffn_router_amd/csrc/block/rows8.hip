@@ -36,7 +36,7 @@ __device__ __forceinline__ void places(int64_t block, int per, Place (&p)[U]) {
 
 constexpr int UNROLL = 2;
 
-template <class T>
+template <class T, bool STREAM>
 __global__ void __launch_bounds__(256)
 mx8_quantize_kernel(const char* __restrict__ x, int64_t ldx, int64_t rows, int64_t block0, int per, Rows8 q) {
   constexpr int V = 16 / sizeof(T), G = MX_BLOCK / V;
@@ -45,7 +45,7 @@ mx8_quantize_kernel(const char* __restrict__ x, int64_t ldx, int64_t rows, int64
   Piece<T, V> d[UNROLL];
 #pragma unroll
   for (int u = 0; u < UNROLL; ++u)
-    d[u] = p[u].row < rows ? piece_load<T, V>(x + p[u].row * ldx + (int64_t)p[u].piece * 16) : piece_zero<T, V>();
+    d[u] = p[u].row < rows ? piece_load<T, V, STREAM>(x + p[u].row * ldx + (int64_t)p[u].piece * 16) : piece_zero<T, V>();
 #pragma unroll
   for (int u = 0; u < UNROLL; ++u) {
     float v[V];
@@ -58,7 +58,7 @@ mx8_quantize_kernel(const char* __restrict__ x, int64_t ldx, int64_t rows, int64
   }
 }
 
-template <class T>
+template <class T, bool STREAM>
 __global__ void __launch_bounds__(256)
 mx8_dequantize_kernel(Rows8 q, int64_t rows, int64_t block0, int per, char* __restrict__ out, int64_t ldo) {
   constexpr int V = 16 / sizeof(T), G = MX_BLOCK / V;
@@ -71,7 +71,8 @@ mx8_dequantize_kernel(Rows8 q, int64_t rows, int64_t block0, int per, char* __re
     const uint8_t* row = q.codes + p[u].row * q.ldc + (int64_t)p[u].piece * V;
     s[u] = in ? q.scales[p[u].row * q.lds + p[u].piece / G] : 0;
 #pragma unroll
-    for (int i = 0; i < V / 4; ++i) c[u][i] = in ? ((const uint32_t*)row)[i] : 0;
+    for (int i = 0; i < V / 4; ++i) c[u][i] = 0;
+    if (in) load_codes(row, c[u]);
   }
 #pragma unroll
   for (int u = 0; u < UNROLL; ++u) {
@@ -79,7 +80,7 @@ mx8_dequantize_kernel(Rows8 q, int64_t rows, int64_t block0, int per, char* __re
     float v[V];
 #pragma unroll
     for (int i = 0; i < V / 4; ++i) mx8_values4(c[u][i], mx_scale(s[u]), v + 4 * i);
-    piece_store<T, V>(out + p[u].row * ldo + (int64_t)p[u].piece * 16, v);
+    piece_store<T, V, STREAM>(out + p[u].row * ldo + (int64_t)p[u].piece * 16, v);
   }
 }
 
@@ -89,7 +90,7 @@ mx8_dequantize_kernel(Rows8 q, int64_t rows, int64_t block0, int per, char* __re
 //   da = dh b sg (1 + a (1 - sg)),  db = dh a sg.
 // Everything between the loads and the stores is fp32.
 
-template <class T>
+template <class T, bool STREAM>
 __global__ void __launch_bounds__(256)
 swiglu_checkpoint_kernel(SwigluArgs a, int64_t block0, int per) {
   constexpr int V = 16 / sizeof(T), G = MX_BLOCK / V;
@@ -103,8 +104,8 @@ swiglu_checkpoint_kernel(SwigluArgs a, int64_t block0, int per) {
   }
   const char* src = (const char*)a.gate_up + row * a.ldg + (int64_t)p[0].piece * 16;
   const int64_t half = a.hidden * sizeof(T);
-  const Piece<T, V> pg = in ? piece_load<T, V>(src) : piece_zero<T, V>();
-  const Piece<T, V> pu = in ? piece_load<T, V>(src + half) : piece_zero<T, V>();
+  const Piece<T, V> pg = in ? piece_load<T, V, STREAM>(src) : piece_zero<T, V>();
+  const Piece<T, V> pu = in ? piece_load<T, V, STREAM>(src + half) : piece_zero<T, V>();
   float g[V], u[V], h[V];
   uint32_t cg[V / 4], cu[V / 4];
   piece_values<T, V>(pg, g);
@@ -113,7 +114,7 @@ swiglu_checkpoint_kernel(SwigluArgs a, int64_t block0, int per) {
   if (!in) return;
 #pragma unroll
   for (int i = 0; i < V; ++i) h[i] = silu(g[i]) * u[i];
-  piece_store<T, V>((char*)a.h + row * a.ldh + (int64_t)p[0].piece * 16, h);
+  piece_store<T, V, STREAM>((char*)a.h + row * a.ldh + (int64_t)p[0].piece * 16, h);
   uint8_t* codes = a.q.codes + row * a.q.ldc + (int64_t)p[0].piece * V;
   store_codes(codes, cg);
   store_codes(codes + a.hidden, cu);
@@ -125,7 +126,7 @@ swiglu_checkpoint_kernel(SwigluArgs a, int64_t block0, int per) {
   }
 }
 
-template <class T>
+template <class T, bool STREAM>
 __global__ void __launch_bounds__(256)
 swiglu_backward_kernel(SwigluArgs a, int64_t block0, int per) {
   constexpr int V = 16 / sizeof(T), G = MX_BLOCK / V;
@@ -139,13 +140,16 @@ swiglu_backward_kernel(SwigluArgs a, int64_t block0, int per) {
   }
   const uint8_t* codes = a.q.codes + row * a.q.ldc + (int64_t)p[0].piece * V;
   const uint8_t* srow = a.q.scales + row * a.q.lds + p[0].piece / G;
-  const Piece<T, V> pd = piece_load<T, V>((const char*)a.dh + row * a.ldd + (int64_t)p[0].piece * 16);
+  const Piece<T, V> pd = piece_load<T, V, STREAM>((const char*)a.dh + row * a.ldd + (int64_t)p[0].piece * 16);
   const float ug = mx_scale(srow[0]), uu = mx_scale(srow[per / G]);
   float g[V], u[V], d[V], h[V];
+  uint32_t cg[V / 4], cu[V / 4];
+  load_codes(codes, cg);
+  load_codes(codes + a.hidden, cu);
 #pragma unroll
   for (int i = 0; i < V / 4; ++i) {
-    mx8_values4(((const uint32_t*)codes)[i], ug, g + 4 * i);
-    mx8_values4(((const uint32_t*)(codes + a.hidden))[i], uu, u + 4 * i);
+    mx8_values4(cg[i], ug, g + 4 * i);
+    mx8_values4(cu[i], uu, u + 4 * i);
   }
   piece_values<T, V>(pd, d);
 #pragma unroll
@@ -156,46 +160,66 @@ swiglu_backward_kernel(SwigluArgs a, int64_t block0, int per) {
     u[i] = dd * act;
   }
   char* out = (char*)a.dgate_up + row * a.ldg + (int64_t)p[0].piece * 16;
-  piece_store<T, V>(out, d);
-  piece_store<T, V>(out + a.hidden * sizeof(T), u);
-  if (a.h) piece_store<T, V>((char*)a.h + row * a.ldh + (int64_t)p[0].piece * 16, h);
+  piece_store<T, V, STREAM>(out, d);
+  piece_store<T, V, STREAM>(out + a.hidden * sizeof(T), u);
+  if (a.h) piece_store<T, V, STREAM>((char*)a.h + row * a.ldh + (int64_t)p[0].piece * 16, h);
 }
 
 int64_t blocks_of(int64_t pieces, int unroll) { return (pieces + 256 * unroll - 1) / (256 * unroll); }
+
+// f<T, STREAM>() by type and by whether the bytes touched go past the caches.
+template <class F>
+void by_form(bool bf16, int64_t bytes, F f) {
+  if (bytes > STREAM_BYTES) {
+    if (bf16) f(bf16_t{}, std::true_type());
+    else f(float{}, std::true_type());
+  } else {
+    if (bf16) f(bf16_t{}, std::false_type());
+    else f(float{}, std::false_type());
+  }
+}
 
 }  // namespace
 
 hipError_t launch_mx8_quantize(bool bf16, int64_t rows, int64_t cols, const void* x, int64_t ldx, const Rows8& q,
                                hipStream_t st) {
-  const int per = (int)(cols * (bf16 ? 2 : 4) / 16);
+  const int size = bf16 ? 2 : 4, per = (int)(cols * size / 16);
   return in_launches(blocks_of(rows * per, UNROLL), [&](int64_t b, dim3 grid) {
-    if (bf16) launch(mx8_quantize_kernel<bf16_t>, grid, dim3(256), 0, st, (const char*)x, ldx, rows, b, per, q);
-    else launch(mx8_quantize_kernel<float>, grid, dim3(256), 0, st, (const char*)x, ldx, rows, b, per, q);
+    by_form(bf16, rows * cols * (size + 1), [&](auto t, auto stream) {
+      launch((mx8_quantize_kernel<decltype(t), decltype(stream)::value>), grid, dim3(256), 0, st, (const char*)x, ldx, rows, b,
+             per, q);
+    });
   });
 }
 
 hipError_t launch_mx8_dequantize(bool bf16, int64_t rows, int64_t cols, const Rows8& q, void* out, int64_t ldo,
                                  hipStream_t st) {
-  const int per = (int)(cols * (bf16 ? 2 : 4) / 16);
+  const int size = bf16 ? 2 : 4, per = (int)(cols * size / 16);
   return in_launches(blocks_of(rows * per, UNROLL), [&](int64_t b, dim3 grid) {
-    if (bf16) launch(mx8_dequantize_kernel<bf16_t>, grid, dim3(256), 0, st, q, rows, b, per, (char*)out, ldo);
-    else launch(mx8_dequantize_kernel<float>, grid, dim3(256), 0, st, q, rows, b, per, (char*)out, ldo);
+    by_form(bf16, rows * cols * (size + 1), [&](auto t, auto stream) {
+      launch((mx8_dequantize_kernel<decltype(t), decltype(stream)::value>), grid, dim3(256), 0, st, q, rows, b, per, (char*)out,
+             ldo);
+    });
   });
 }
 
 hipError_t launch_swiglu_checkpoint(const SwigluArgs& a, hipStream_t st) {
-  const int per = (int)(a.hidden * (a.bf16 ? 2 : 4) / 16);
-  return in_launches(blocks_of(a.groups * a.max_rows * per, 1), [&](int64_t b, dim3 grid) {
-    if (a.bf16) launch(swiglu_checkpoint_kernel<bf16_t>, grid, dim3(256), 0, st, a, b, per);
-    else launch(swiglu_checkpoint_kernel<float>, grid, dim3(256), 0, st, a, b, per);
+  const int size = a.bf16 ? 2 : 4, per = (int)(a.hidden * size / 16);
+  const int64_t rows = a.groups * a.max_rows;
+  return in_launches(blocks_of(rows * per, 1), [&](int64_t b, dim3 grid) {
+    by_form(a.bf16, rows * a.hidden * (3 * size + 2), [&](auto t, auto stream) {
+      launch((swiglu_checkpoint_kernel<decltype(t), decltype(stream)::value>), grid, dim3(256), 0, st, a, b, per);
+    });
   });
 }
 
 hipError_t launch_swiglu_backward(const SwigluArgs& a, hipStream_t st) {
-  const int per = (int)(a.hidden * (a.bf16 ? 2 : 4) / 16);
-  return in_launches(blocks_of(a.groups * a.max_rows * per, 1), [&](int64_t b, dim3 grid) {
-    if (a.bf16) launch(swiglu_backward_kernel<bf16_t>, grid, dim3(256), 0, st, a, b, per);
-    else launch(swiglu_backward_kernel<float>, grid, dim3(256), 0, st, a, b, per);
+  const int size = a.bf16 ? 2 : 4, per = (int)(a.hidden * size / 16);
+  const int64_t rows = a.groups * a.max_rows;
+  return in_launches(blocks_of(rows * per, 1), [&](int64_t b, dim3 grid) {
+    by_form(a.bf16, rows * a.hidden * ((a.h ? 4 : 3) * size + 2), [&](auto t, auto stream) {
+      launch((swiglu_backward_kernel<decltype(t), decltype(stream)::value>), grid, dim3(256), 0, st, a, b, per);
+    });
   });
 }
 
