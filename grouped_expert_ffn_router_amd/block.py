@@ -51,14 +51,27 @@ def _code(t, what):
 
 def _like(t, shape, dtype, device, what):
     """A tensor of the caller's, checked."""
-    if tuple(t.shape) != tuple(shape) or t.dtype != dtype:
+    if t.shape != shape or t.dtype != dtype:
         raise ValueError(f"{what} {tuple(t.shape)} {t.dtype}, expected {tuple(shape)} {dtype}")
     if t.device != device:
         raise ValueError(f"{what} is on {t.device}, not on {device}")
 
 
 def _bytes(t, what):
-    return _row_stride(t, what) * t.element_size()
+    """Bytes from row to row of t [..., rows, cols]."""
+    if t.is_contiguous() and t.dim() >= 2:
+        return t.shape[-1] * t.itemsize
+    return _row_stride(t, what) * t.itemsize
+
+
+def _new(t):
+    """A contiguous tensor like t."""
+    return torch.empty_like(t) if t.is_contiguous() else torch.empty(t.shape, dtype=t.dtype, device=t.device)
+
+
+def _vector(t, n, device, what):
+    if t.shape != (n,) or not t.is_contiguous() or t.device != device:
+        raise ValueError(f"{what} must be contiguous [{n}] on {device}")
 
 
 def _counts(counts, groups, device):
@@ -96,7 +109,7 @@ def mx8_dequantize(q, dtype=torch.bfloat16):
     st, dev = _on(_eight(q, "q").codes)
     with dev:
         out = torch.empty(q.shape, dtype=dtype, device=q.codes.device)
-        B.mx8_dequantize(code, q.rows, q.cols, q.arg, out, q.cols * out.element_size(), st)
+        B.mx8_dequantize(code, q.rows, q.cols, q.arg, out, q.cols * out.itemsize, st)
     return out
 
 
@@ -136,15 +149,14 @@ def rms_norm(x, weight, residual=None, eps=1e-6, form="act"):
     code, wcode = _code(x, "x"), _code(weight, "weight")
     st, dev = _on(x)
     ldx, ldr, cols = _bytes(x, "x"), 0, x.shape[-1]
-    if weight.shape != (cols,) or not weight.is_contiguous() or weight.device != x.device:
-        raise ValueError(f"weight must be contiguous [{cols}] on {x.device}")
+    _vector(weight, cols, x.device, "weight")
     if residual is not None:
         _like(residual, x.shape, x.dtype, x.device, "residual")
         ldr = _bytes(residual, "residual")
-    ld = cols * x.element_size()
+    ld = cols * x.itemsize
     with dev:
-        s = torch.empty(x.shape, dtype=x.dtype, device=x.device) if residual is not None else None
-        y = torch.empty(x.shape, dtype=x.dtype, device=x.device) if form != "mx8" else None
+        s = _new(x) if residual is not None else None
+        y = _new(x) if form != "mx8" else None
         q = Mx8Rows.empty(x.shape, x.device) if form != "act" else None
         B.rms_norm(code, x.numel() // cols if cols else 0, cols, x, ldx, residual, ldr, weight, wcode, eps, s, ld, y, ld,
                    None if q is None else q.arg, st)
@@ -158,17 +170,16 @@ def rms_norm_backward(dy, s, weight, dstream=None, eps=1e-6):
     st, dev = _on(dy)
     cols = dy.shape[-1]
     _like(s, dy.shape, dy.dtype, dy.device, "s")
-    if weight.shape != (cols,) or not weight.is_contiguous() or weight.device != dy.device:
-        raise ValueError(f"weight must be contiguous [{cols}] on {dy.device}")
+    _vector(weight, cols, dy.device, "weight")
     if dstream is not None:
         _like(dstream, dy.shape, dy.dtype, dy.device, "dstream")
     ldy, lds, ldt = _bytes(dy, "dy"), _bytes(s, "s"), 0 if dstream is None else _bytes(dstream, "dstream")
     rows = dy.numel() // cols if cols else 0
     with dev:
-        dx = torch.empty(dy.shape, dtype=dy.dtype, device=dy.device)
+        dx = _new(dy)
         dweight = torch.empty((cols,), dtype=torch.float32, device=dy.device)
         ws = torch.empty((B.rms_norm_workspace_size(rows, cols),), dtype=torch.uint8, device=dy.device)
-        B.rms_norm_backward(code, rows, cols, dy, ldy, s, lds, weight, wcode, eps, dstream, ldt, dx, cols * dy.element_size(),
+        B.rms_norm_backward(code, rows, cols, dy, ldy, s, lds, weight, wcode, eps, dstream, ldt, dx, cols * dy.itemsize,
                             dweight, ws, st)
     return dx, dweight
 
@@ -210,9 +221,9 @@ class RouterRule:
         """Writes the choice for logits [T, E] into idx [T, k] int32 and w [T, k] fp32 (contiguous)."""
         T, E = logits.shape
         if self.balance is not None:
-            _like(self.balance, (E,), torch.float32, logits.device, "balance")
-            if not self.balance.is_contiguous():
-                raise ValueError("balance must be contiguous")
+            if self.balance.dtype != torch.float32:
+                raise ValueError(f"balance is {self.balance.dtype}, not fp32")
+            _vector(self.balance, E, logits.device, "balance")
         B.select(self.arg, T, E, self.top_k, logits, _row_stride(logits, "logits"), self.balance, idx, w, stream)
 
 

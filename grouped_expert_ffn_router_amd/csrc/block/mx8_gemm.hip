@@ -173,7 +173,7 @@ struct Tile {
   static constexpr int FM = WTM / 32, FN = 2, NF = FM + FN;
   static constexpr int A_BYTES = BM * 128, STAGE = A_BYTES + BN * 64;
   static constexpr int SCALES = (BM + BN) * 16;
-  static constexpr int OPERANDS = 2 * STAGE + 2 * SCALES, STAGED = BM * BN * 2;
+  static constexpr int STAGES = 3, OPERANDS = STAGES * STAGE + 2 * SCALES, STAGED = BM * BN * 2;
 };
 
 template <int FM>
@@ -182,11 +182,21 @@ struct Frags {
   i32x4 b[2];
 };
 
+template <int OFFSET>
 __device__ __forceinline__ void read16(i32x4& v, uint32_t addr) {
-  asm volatile("ds_read_b128 %0, %1" : "=v"(v) : "v"(addr) : "memory");
+  asm volatile("ds_read_b128 %0, %1 offset:%2" : "=v"(v) : "v"(addr), "i"(OFFSET) : "memory");
 }
+template <int OFFSET>
 __device__ __forceinline__ void read4(int& v, uint32_t addr) {
-  asm volatile("ds_read_b32 %0, %1" : "=v"(v) : "v"(addr) : "memory");
+  asm volatile("ds_read_b32 %0, %1 offset:%2" : "=v"(v) : "v"(addr), "i"(OFFSET) : "memory");
+}
+// f(0), f(1) .. f(N - 1) with each index a constant.
+template <int N, class F>
+__device__ __forceinline__ void each(F f) {
+  if constexpr (N > 0) {
+    each<N - 1>(f);
+    f(std::integral_constant<int, N - 1>());
+  }
 }
 // Every LDS read so far has landed; the registers pass through, so that their
 // consumers stay behind it.
@@ -299,14 +309,14 @@ mx8_gemm_tile(Operand a, Operand b, Out<T> out, const int32_t* counts, int max_r
   const int lrow = lane >> 3, lcol = lane & 7;
   const int acol = lcol ^ swz(wave * 32 + lrow);  // rows 8 further: ^ 4
   const int bcol = lcol ^ swz(wave * 16 + lrow);  // lines 8 further: ^ 4, the line's other row
-  const uint8_t *pa[4], *pb[2];
+  const uint8_t *pa[4], *pb[2];                   // where the next step to load has them
 #pragma unroll
   for (int d = 0; d < 4; ++d)
-    pa[d] = a.v.codes + (arow + min(m0 + wave * 32 + d * 8 + lrow, M - 1)) * a.v.ldc - 1024 * d;
+    pa[d] = a.v.codes + (arow + min(m0 + wave * 32 + d * 8 + lrow, M - 1)) * a.v.ldc + (acol ^ (d & 1) * 4) * 16 - 1024 * d;
 #pragma unroll
   for (int d = 0; d < 2; ++d) {
     const int row = 2 * (wave * 16 + d * 8 + lrow) + ((bcol >> 2) ^ d);
-    pb[d] = b.v.codes + (brow + min(n0 + row, N - 1)) * b.v.ldc - 1024 * d;
+    pb[d] = b.v.codes + (brow + min(n0 + row, N - 1)) * b.v.ldc + (bcol & 3) * 16 - 1024 * d;
   }
   // scales: thread tid brings in row tid of A (below BM) or of B
   const uint8_t* ps = tid < C::BM ? a.v.scales + (arow + min(m0 + tid, M - 1)) * a.v.lds
@@ -314,11 +324,19 @@ mx8_gemm_tile(Operand a, Operand b, Out<T> out, const int32_t* counts, int max_r
 
   const int frow = lane & 31, half = lane >> 5;
   const uint32_t lds0 = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) char*)smem;
-  const uint32_t fa_base = lds0 + (wm * C::WTM + frow) * 128;
-  const uint32_t fb_base = lds0 + C::A_BYTES + (wn * C::WTN + frow) / 2 * 128;
+  // Where a lane's fragments are in buffer 0: of A by substep and half of the
+  // operand, of B by substep (32 rows further: 32 lines of A, 16 of B).
   const int fa_swz = swz(frow), fb_swz = swz(frow >> 1) ^ ((frow & 1) << 2);
-  const uint32_t sa_base = lds0 + 2 * C::STAGE + (wm * C::WTM + frow) * 16;
-  const uint32_t sb_base = lds0 + 2 * C::STAGE + (C::BM + wn * C::WTN + frow) * 16;
+  uint32_t fa[2][2], fb[2];
+#pragma unroll
+  for (int ks = 0; ks < 2; ++ks) {
+#pragma unroll
+    for (int p = 0; p < 2; ++p)
+      fa[ks][p] = lds0 + (wm * C::WTM + frow) * 128 + (uint32_t)(((ks * 4 + p * 2 + half) ^ fa_swz) << 4);
+    fb[ks] = lds0 + C::A_BYTES + (wn * C::WTN + frow) / 2 * 128 + (uint32_t)(((ks * 2 + half) ^ fb_swz) << 4);
+  }
+  const uint32_t sa = lds0 + C::STAGES * C::STAGE + (wm * C::WTM + frow) * 16;
+  const uint32_t sb = lds0 + C::STAGES * C::STAGE + (C::BM + wn * C::WTN + frow) * 16;
 
   f32x16 acc[FM][FN];
 #pragma unroll
@@ -330,27 +348,34 @@ mx8_gemm_tile(Operand a, Operand b, Out<T> out, const int32_t* counts, int max_r
 
   Frags<FM> F[2];
   int raw[NF], sc[NF];  // a step's scale bytes as read, and those of its substeps as bytes 0 and 2
-  auto read_codes = [&](Frags<FM>& f, int kt, int ks, int q) {  // q in [0, NF)
-    const uint32_t st = (uint32_t)((kt & 1) * C::STAGE);
-    if (q < FM) {  // the two halves of a register tuple
+  // Fragment q in [0, NF) of a substep; at: its buffer's place.
+  auto read_codes = [&](Frags<FM>& f, uint32_t at, auto ks_tag, auto q_tag) {
+    constexpr int ks = decltype(ks_tag)::value, q = decltype(q_tag)::value;
+    if constexpr (q < FM) {  // the two halves of a register tuple
       i32x4 lo, hi;
-      read16(lo, fa_base + st + q * 32 * 128 + (uint32_t)(((ks * 4 + half) ^ fa_swz) << 4));
-      read16(hi, fa_base + st + q * 32 * 128 + (uint32_t)(((ks * 4 + 2 + half) ^ fa_swz) << 4));
+      read16<q * 32 * 128>(lo, fa[ks][0] + at);
+      read16<q * 32 * 128>(hi, fa[ks][1] + at);
       f.a[q] = fp8_operand(lo, hi);
     } else {
-      read16(f.b[q - FM], fb_base + st + (q - FM) * 16 * 128 + (uint32_t)(((ks * 2 + half) ^ fb_swz) << 4));
+      read16<(q - FM) * 16 * 128>(f.b[q - FM], fb[ks] + at);
     }
   };
-  auto read_scales = [&](int kt, int q) {  // q in [0, NF)
-    const uint32_t st = (uint32_t)(((kt >> 2) & 1) * C::SCALES + (kt & 3) * 4);
-    if (q < FM) read4(raw[q], sa_base + st + q * 32 * 16);
-    else read4(raw[q], sb_base + st + (q - FM) * 32 * 16);
+  auto read_scales = [&](uint32_t at, auto q_tag) {  // q in [0, NF)
+    constexpr int q = decltype(q_tag)::value;
+    if constexpr (q < FM) read4<q * 32 * 16>(raw[q], sa + at);
+    else read4<(q - FM) * 32 * 16>(raw[q], sb + at);
   };
-  auto load_codes = [&](int kt, int d) {  // d in [0, 6)
+  auto scales_at = [&](int kt) { return (uint32_t)(((kt >> 2) & 1) * C::SCALES + (kt & 3) * 4); };
+  // Load d in [0, 6) of step kt, the next one in order.  LAST: it may be the
+  // last step, whose chunks past K are the row's last one in their place.
+  auto load_codes = [&](int kt, int buf, int d, auto last_tag) {
     const int dd = d < 4 ? d : d - 4;
-    const void* gp = d < 4 ? (const void*)(pa[dd] + (int64_t)min(kt * 8 + (acol ^ (dd & 1) * 4), nc - 1) * 16)
-                           : (const void*)(pb[dd] + (int64_t)min(kt * 4 + (bcol & 3), nb - 1) * 16);
-    auto lp = (__attribute__((address_space(3))) void*)(smem + (kt & 1) * C::STAGE +
+    const uint8_t*& p = d < 4 ? pa[dd] : pb[dd];
+    int64_t back = 0;
+    if constexpr (decltype(last_tag)::value)
+      back = 16 * (int64_t)(d < 4 ? min(0, nc - 1 - (kt * 8 + (acol ^ (dd & 1) * 4))) : min(0, nb - 1 - (kt * 4 + (bcol & 3))));
+    const void* gp = p + back;
+    auto lp = (__attribute__((address_space(3))) void*)(smem + buf * C::STAGE +
                                                          (d < 4 ? wave * 32 * 128 : C::A_BYTES + wave * 16 * 128));
     switch (dd) {
       case 0: __builtin_amdgcn_global_load_lds(gp, lp, 16, 0, 0); break;
@@ -358,86 +383,101 @@ mx8_gemm_tile(Operand a, Operand b, Out<T> out, const int32_t* counts, int max_r
       case 2: __builtin_amdgcn_global_load_lds(gp, lp, 16, 2048, 0); break;
       default: __builtin_amdgcn_global_load_lds(gp, lp, 16, 3 * 1024, 0); break;
     }
+    p += d < 4 ? 128 : 64;
   };
   auto load_scales = [&](int four) {  // steps 4 four .. 4 four + 3
-    auto lp = (__attribute__((address_space(3))) void*)(smem + 2 * C::STAGE + (four & 1) * C::SCALES + wave * 1024);
+    auto lp = (__attribute__((address_space(3))) void*)(smem + C::STAGES * C::STAGE + (four & 1) * C::SCALES + wave * 1024);
     __builtin_amdgcn_global_load_lds((const void*)(ps + (int64_t)four * 16), lp, 16, 0, 0);
   };
+  i32x8 large, small;  // SPLIT: the two parts of the fragment of A in use
   auto mma = [&](Frags<FM>& f, int i, int j, auto sel_tag) {
     constexpr int SEL = decltype(sel_tag)::value;
-    i32x8 av = f.a[i];
     if constexpr (SPLIT) {
-      const i32x8 large = fp8_large(av);
+      if (j == 0) {
+        large = fp8_large(f.a[i]);
+        small = f.a[i] ^ large;
+      }
       acc[i][j] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(fp4_operand(f.b[j]), large, acc[i][j], 4, 0, SEL, sc[FM + j],
                                                                   SEL, sc[i]);
-      av ^= large;
+      acc[i][j] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(fp4_operand(f.b[j]), small, acc[i][j], 4, 0, SEL, sc[FM + j],
+                                                                  SEL, sc[i]);
+    } else {
+      acc[i][j] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(fp4_operand(f.b[j]), f.a[i], acc[i][j], 4, 0, SEL, sc[FM + j],
+                                                                  SEL, sc[i]);
     }
-    acc[i][j] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(fp4_operand(f.b[j]), av, acc[i][j], 4, 0, SEL, sc[FM + j], SEL,
-                                                                sc[i]);
   };
-  // MODE 0: issues the loads of step kt + 2; 1: no new loads; 2: the last step.
-  auto step = [&](int kt, auto mode_tag) {
-    constexpr int MODE = decltype(mode_tag)::value;
-    // The scales of the four steps from kt + 2 on, into the buffer whose last
-    // step was kt - 3.  (A branch further down would let the compiler move the
+  // Step kt out of buffer buf, the next one out of nbuf.  LEFT: steps that follow
+  // it, 4 for four and more: with three and more the loads of step kt + 3 are issued.
+  auto step = [&](int kt, int buf, int nbuf, auto left_tag) {
+    constexpr int LEFT = decltype(left_tag)::value;
+    // The scales of the four steps from kt + 3 on, into the buffer whose last
+    // step was kt - 2.  (A branch further down would let the compiler move the
     // matrix instructions past it, away from the reads they hide.)
-    if constexpr (MODE == 0)
-      if (((kt + 2) & 3) == 0) load_scales((kt + 2) >> 2);
+    if constexpr (LEFT >= 3)
+      if (((kt + 3) & 3) == 0) load_scales((kt + 3) >> 2);
     // A lane's bytes of the step's scales come down to bytes 0 and 2; those of
     // blocks that K does not have are cleared.
     uint32_t keep = 0xff00ffu;
-    if constexpr (MODE == 2) {
+    if constexpr (LEFT == 0) {
       const int have = nb - kt * 4 - half;  // blocks from this lane's first one on
       keep = (have > 0 ? 0xffu : 0u) | (have > 2 ? 0xff0000u : 0u);
     }
 #pragma unroll
     for (int q = 0; q < NF; ++q) sc[q] = (int)(((uint32_t)raw[q] >> (8 * half)) & keep);
-#pragma unroll
-    for (int q = 0; q < NMMA; ++q) {
+    const uint32_t at = (uint32_t)(buf * C::STAGE), nat = (uint32_t)(nbuf * C::STAGE), sat = scales_at(kt + 1);
+    each<NMMA>([&](auto q) {
       mma(F[0], q / FN, q % FN, std::integral_constant<int, 0>());
-      if (q < NF) read_codes(F[1], kt, 1, q);
+      if constexpr (q < NF) read_codes(F[1], at, std::integral_constant<int, 1>(), q);
       __builtin_amdgcn_sched_barrier(0);
-    }
+    });
     wait_reads(F[1]);
-    if constexpr (MODE != 2) {
-      vm_wait<0>();   // step kt + 1's codes and scales (this lane's part)
+    if constexpr (LEFT > 0) {
+      // step kt + 1's codes and scales (this lane's part); step kt + 2's 6 loads may be under way
+      vm_wait<(LEFT > 1 ? 6 : 0)>();
       lds_barrier();  // ... every lane's; every wave is done with step kt's buffer
     }
-#pragma unroll
-    for (int q = 0; q < NMMA; ++q) {
+    each<NMMA>([&](auto q) {
       mma(F[1], q / FN, q % FN, std::integral_constant<int, 2>());
-      if constexpr (MODE != 2) {
-        if (q < NF) {
-          read_codes(F[0], kt + 1, 0, q);
-          read_scales(kt + 1, q);
-        }
+      if constexpr (LEFT > 0 && q < NF) {
+        read_codes(F[0], nat, std::integral_constant<int, 0>(), q);
+        read_scales(sat, q);
       }
-      if constexpr (MODE == 0) {
-        if (q < 6) load_codes(kt + 2, q);
-        if (q + NMMA < 6) load_codes(kt + 2, q + NMMA);
+      if constexpr (LEFT >= 3) {
+        using Last = std::integral_constant<bool, LEFT == 3>;
+        if (q < 6) load_codes(kt + 3, buf, q, Last());
+        if (q + NMMA < 6) load_codes(kt + 3, buf, q + NMMA, Last());
       }
       __builtin_amdgcn_sched_barrier(0);
-    }
-    if constexpr (MODE != 2) wait_reads(F[0], raw);
+    });
+    if constexpr (LEFT > 0) wait_reads(F[0], raw);
   };
   load_scales(0);
+  for (int t = 0; t < 3; ++t)
+    if (t < nk) {
 #pragma unroll
-  for (int d = 0; d < 6; ++d) load_codes(0, d);
-  vm_wait<0>();
+      for (int d = 0; d < 6; ++d) load_codes(t, t, d, std::true_type());
+    }
+  if (nk > 2) vm_wait<12>();
+  else if (nk > 1) vm_wait<6>();
+  else vm_wait<0>();
   lds_barrier();
-  if (nk > 1) {
-#pragma unroll
-    for (int d = 0; d < 6; ++d) load_codes(1, d);
-  }
-#pragma unroll
-  for (int q = 0; q < NF; ++q) {
-    read_codes(F[0], 0, 0, q);
+  each<NF>([&](auto q) {
+    read_codes(F[0], 0, std::integral_constant<int, 0>(), q);
     read_scales(0, q);
-  }
+  });
   wait_reads(F[0], raw);
-  for (int kt = 0; kt + 2 < nk; ++kt) step(kt, std::integral_constant<int, 0>());
-  if (nk > 1) step(nk - 2, std::integral_constant<int, 1>());
-  step(nk - 1, std::integral_constant<int, 2>());
+  int kt = 0, buf = 0;
+  auto go = [&](auto left_tag) {
+    const int next = buf == 2 ? 0 : buf + 1;
+    step(kt, buf, next, left_tag);
+    buf = next;
+    ++kt;
+  };
+  while (kt + 4 < nk) go(std::integral_constant<int, 4>());
+  if (nk > 3) go(std::integral_constant<int, 3>());
+  if (nk > 2) go(std::integral_constant<int, 2>());
+  if (nk > 1) go(std::integral_constant<int, 1>());
+  go(std::integral_constant<int, 0>());
 
   if constexpr (!SPLIT) {
     store_staged<C>(out, arow + m0, m0, n0, M, N, smem, acc);
