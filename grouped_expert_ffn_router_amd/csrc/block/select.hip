@@ -428,18 +428,26 @@ select_rule_kernel(SelectRule r, const float* __restrict__ logits, int64_t ld, c
 //   sigmoid                 dl_i = w_i (1 - sigmoid(l_i)) dw_i
 //   softmax, renormalised   dl_i = w_i (dw_i - m)
 //   softmax                 dl_e = w_e dw_e [e chosen] - scale m p_e   (p: the softmax over all)
-// and 0 elsewhere.  One wave per token; each pick's term is added in the lane
-// that writes its expert, so picks of one expert add up in order.
+// and 0 elsewhere.  One wave per token: its row of terms is laid out in LDS
+// (zeros, then each pick's term) and stored whole, so that the time is that of
+// writing the row.  Picks of one expert are added up in their order; that there
+// are some shows where a pick does not read its own mark back.
+
+// LDS written by the wave's lanes so far may be read by its other lanes.
+__device__ __forceinline__ void wave_lds() { __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront"); }
 
 template <int V>
 __global__ void __launch_bounds__(256)
 select_backward_kernel(SelectRule r, const float* __restrict__ dw, const float* __restrict__ w,
                        const int32_t* __restrict__ idx, const float* __restrict__ logits, int64_t ld, int64_t T, int E,
                        int k, float* __restrict__ dlogits, int64_t ldd) {
-  const int64_t t = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
-  const int lane = lane_id();
+  extern __shared__ float lds[];
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = lane_id();
+  const int64_t t = (int64_t)blockIdx.x * 4 + wave;
   if (t >= T) return;
   const float* row = logits + t * ld;
+  const int width = (E + 64 * V - 1) / (64 * V) * (64 * V);
+  float* terms = lds + wave * width;
   int e = -1;
   float wi = 0.f, di = 0.f;
   if (lane < k) {
@@ -448,13 +456,36 @@ select_backward_kernel(SelectRule r, const float* __restrict__ dw, const float* 
     di = dw[t * k + lane];
   }
   if (e < 0 || e >= E) { e = -1; wi = 0.f; di = 0.f; }
+  const bool dense = r.score == SOFTMAX && !r.renorm;
+  for (int c = lane * V; c < width; c += 64 * V) {
+    if constexpr (V == 4) *(float4*)(terms + c) = make_float4(0.f, 0.f, 0.f, 0.f);
+    else terms[c] = 0.f;
+  }
   // a weight of 0 (an expert that is out) takes no part, whatever its gradient
   const float wd = wi == 0.f ? 0.f : wi * di;
   const float sum = wave_sum(wd);
-  const bool dense = r.score == SOFTMAX && !r.renorm;
   float term = wd;
   if (r.renorm) term = wi == 0.f ? 0.f : wi * (di - sum / r.scale);
-  if (r.score != SOFTMAX && wi != 0.f) term *= 1.0f / (1.0f + expf(row[e]));
+  if (r.score != SOFTMAX && wi != 0.f) term *= __builtin_amdgcn_rcpf(1.0f + exp_of(row[e]));
+  wave_lds();
+  if (e >= 0) terms[e] = __int_as_float(lane);
+  wave_lds();
+  const bool mine = e < 0 || __float_as_int(terms[e]) == lane;
+  wave_lds();
+  if (__all(mine)) {
+    if (e >= 0) terms[e] = term;
+  } else {  // each expert's first pick adds up all of them
+    float all = 0.f;
+    int first = lane;
+    for (int p = k - 1; p >= 0; --p)
+      if (__builtin_amdgcn_readlane(e, p) == e) first = p;
+    for (int p = 0; p < k; ++p) {
+      const float tp = __uint_as_float((uint32_t)__builtin_amdgcn_readlane((int)__float_as_uint(term), p));
+      if (__builtin_amdgcn_readlane(e, p) == e) all += tp;
+    }
+    if (e >= 0 && first == lane) terms[e] = all;
+  }
+  wave_lds();
   float top = 0.f, factor = 0.f;
   if (dense) {
     float m = -INFINITY;
@@ -463,31 +494,26 @@ select_backward_kernel(SelectRule r, const float* __restrict__ dw, const float* 
     for (int off = 32; off > 0; off >>= 1) m = fmaxf(m, __shfl_xor(m, off));
     top = m;
     float s = 0.f;
-    for (int c = lane; c < E; c += 64) s += row[c] == -INFINITY ? 0.f : expf(row[c] - top);
+    for (int c = lane; c < E; c += 64) s += row[c] == -INFINITY ? 0.f : exp_of(row[c] - top);
     s = wave_sum(s);
     factor = s > 0.f ? -sum / s : 0.f;
   }
   float* out = dlogits + t * ldd;
-  for (int c0 = 0; c0 < E; c0 += 64 * V) {
-    const int c = c0 + lane * V;
+  for (int c = lane * V; c < E; c += 64 * V) {
     float v[V];
-#pragma unroll
-    for (int i = 0; i < V; ++i) {
-      v[i] = 0.f;
-      if (dense && c + i < E && row[c + i] != -INFINITY) v[i] = factor * expf(row[c + i] - top);
+    if constexpr (V == 4) {
+      const float4 d = *(const float4*)(terms + c);
+      v[0] = d.x; v[1] = d.y; v[2] = d.z; v[3] = d.w;
+    } else {
+      v[0] = terms[c];
     }
-    for (int p = 0; p < k; ++p) {
-      const int ep = __builtin_amdgcn_readlane(e, p);
-      const float tp = __uint_as_float((uint32_t)__builtin_amdgcn_readlane((int)__float_as_uint(term), p));
+    if (dense) {
 #pragma unroll
       for (int i = 0; i < V; ++i)
-        if (c + i == ep) v[i] += tp;
+        if (row[c + i] != -INFINITY) v[i] += factor * exp_of(row[c + i] - top);
     }
-    if constexpr (V == 4) {
-      if (c < E) *(float4*)(out + c) = make_float4(v[0], v[1], v[2], v[3]);
-    } else {
-      if (c < E) out[c] = v[0];
-    }
+    if constexpr (V == 4) *(float4*)(out + c) = make_float4(v[0], v[1], v[2], v[3]);
+    else out[c] = v[0];
   }
 }
 
@@ -530,13 +556,14 @@ hipError_t launch_select_backward(const SelectRule& r, const float* dw, const fl
                                   const float* logits, int64_t ld, int64_t T, int E, int k, float* dlogits, int64_t ldd,
                                   hipStream_t st) {
   const bool wide = E % 4 == 0 && ldd % 4 == 0 && (uintptr_t)dlogits % 16 == 0;
+  const int lane_values = wide ? 256 : 64, lds = 4 * 4 * ((E + lane_values - 1) / lane_values * lane_values);
   return by_tokens(T, [&](int64_t t, int64_t n, dim3 grid) {
     const int64_t at = t * k;
     if (wide)
-      launch(select_backward_kernel<4>, grid, dim3(256), 0, st, r, dw + at, w + at, idx + at, logits + t * ld, ld, n, E, k,
+      launch(select_backward_kernel<4>, grid, dim3(256), lds, st, r, dw + at, w + at, idx + at, logits + t * ld, ld, n, E, k,
              dlogits + t * ldd, ldd);
     else
-      launch(select_backward_kernel<1>, grid, dim3(256), 0, st, r, dw + at, w + at, idx + at, logits + t * ld, ld, n, E, k,
+      launch(select_backward_kernel<1>, grid, dim3(256), lds, st, r, dw + at, w + at, idx + at, logits + t * ld, ld, n, E, k,
              dlogits + t * ldd, ldd);
   });
 }

@@ -79,6 +79,20 @@ def _expert_form(experts):
     return experts
 
 
+def _rule_of(rule, shape):
+    if rule is not None and rule.top_k != shape.top_k:
+        raise ValueError(f"the rule chooses {rule.top_k} experts, the layer {shape.top_k}")
+    return rule
+
+
+def _route(rule, dims, x, w_router, w_down, bias, bias_row_tokens, logits, z, idx, w, ws, stream=None):
+    """Router and latent projection; a rule (block.RouterRule) chooses and weights the experts in the place of the softmax
+    over the k largest logits."""
+    B.route(dims, x, w_router, w_down, bias, bias_row_tokens, logits, z, idx, w, ws, stream)
+    if rule is not None:
+        rule.choose(logits, idx, w, stream)
+
+
 def _expert_gemm(dims, wave, wave_buf, pools, src_stride, row_src, wave_count, w13, w2, ret, ret_stride, ws, ws_mx,
                  stream):
     """The expert FFNs of one wave, by the form of the weights (tensors or MxRows)."""
@@ -93,12 +107,14 @@ class OneRankLayer:
     """One EP rank's layer.  ``inp`` is a workload.gen.generate() dict.
     experts="mx" quantises the routed experts to MX-FP4 rows and runs their
     products on them (moe_mx_expert_gemm), which rounds the tokens' rows and
-    the hidden rows to 4 bits too."""
+    the hidden rows to 4 bits too.  rule: a block.RouterRule by which the
+    experts are chosen and weighted, here and in the layers below (None: the
+    softmax over the k largest logits)."""
 
     def __init__(self, shape, inp, device="cuda", gather="fused", keep_source_logits=False, live_waves=0,
-                 experts="act"):
+                 experts="act", rule=None):
         self.shape, self.device = shape, device
-        self.experts = _expert_form(experts)
+        self.experts, self.rule = _expert_form(experts), _rule_of(rule, shape)
         self.gather = gather
         # waves whose scratch (hidden rows, partial tiles) the workspace holds at once
         self.live_waves = live_waves if live_waves else shape.waves
@@ -169,8 +185,8 @@ class OneRankLayer:
     def _route_one(self, s, host_x):
         xs = upload(host_x, self.device)
         d = self.dims
-        B.route(d, xs, self.w_router, self.w_down, self.bias, self.bias_row_tokens, self.logits, self.z,
-                self.idx, self.w, self.ws)
+        _route(self.rule, d, xs, self.w_router, self.w_down, self.bias, self.bias_row_tokens, self.logits, self.z,
+               self.idx, self.w, self.ws)
         B.pack_pools(d, self.z, self.idx, self.send_pools, self.scap * self.prow, self.slot_of, self.send_count,
                      self.ws)
         self.recv_pools[s].copy_(self.send_pools[self.rank])
@@ -186,7 +202,7 @@ class OneRankLayer:
 
     def dispatch(self, stream=None):
         d = self.dims
-        B.route(d, self.x, self.w_router, self.w_down, self.bias, self.bias_row_tokens, self.logits, self.z,
+        _route(self.rule, d, self.x, self.w_router, self.w_down, self.bias, self.bias_row_tokens, self.logits, self.z,
                 self.idx, self.w, self.ws, stream)
         B.pack_pools(d, self.z, self.idx, self.send_pools, self.scap * self.prow, self.slot_of,
                      self.send_count, self.ws, stream)
@@ -300,9 +316,9 @@ class RaggedOneRankLayer(OneRankLayer):
     expert has a bank of expert_rows rows."""
 
     def __init__(self, shape, inp, expert_rows, device="cuda", gather="fused", ragged_banks=True, live_waves=2,
-                 experts="act"):
+                 experts="act", rule=None):
         from workload.configs import exact_fit
-        self.experts = _expert_form(experts)
+        self.experts, self.rule = _expert_form(experts), _rule_of(rule, shape)
         if "sources" not in inp:
             raise ValueError("the ragged layer needs a workload whose other ranks route their own tokens")
         self.shape, self.device, self.gather = shape, device, gather
@@ -341,7 +357,7 @@ class RaggedOneRankLayer(OneRankLayer):
         for s in range(R):
             host_x = inp["x"] if s == r else inp["sources"](s)
             xs = upload(host_x, dev)
-            B.route(setup_dims, xs, self.w_router, self.w_down, self.bias, self.bias_row_tokens, self.logits,
+            _route(self.rule, setup_dims, xs, self.w_router, self.w_down, self.bias, self.bias_row_tokens, self.logits,
                     self.z, self.idx, self.w, ws_setup)
             B.pack_ragged(setup_dims, self.z, self.idx, self.send_rows, self.send_off, self.slot_of,
                           self.send_count, ws_setup)
@@ -400,7 +416,7 @@ class RaggedOneRankLayer(OneRankLayer):
 
     def dispatch(self, stream=None):
         d, r = self.dims, self.rank
-        B.route(d, self.x, self.w_router, self.w_down, self.bias, self.bias_row_tokens, self.logits, self.z,
+        _route(self.rule, d, self.x, self.w_router, self.w_down, self.bias, self.bias_row_tokens, self.logits, self.z,
                 self.idx, self.w, self.ws, stream)
         B.pack_ragged(d, self.z, self.idx, self.send_rows, self.send_off, self.slot_of, self.send_count, self.ws,
                       stream)
@@ -457,9 +473,9 @@ class AllRanksLayer:
     """Every rank of a small EP domain on one device (zero-copy exchanges).
     experts="mx": the routed experts as MX-FP4 rows."""
 
-    def __init__(self, shape, inp, device="cuda", gather="fused", experts="act"):
+    def __init__(self, shape, inp, device="cuda", gather="fused", experts="act", rule=None):
         self.shape, self.device, self.gather = shape, device, gather
-        self.experts = _expert_form(experts)
+        self.experts, self.rule = _expert_form(experts), _rule_of(rule, shape)
         T, D, L, E, k, R = shape.tokens, shape.d_model, shape.latent, shape.n_experts, shape.top_k, shape.n_ranks
         X, W = shape.local_experts, shape.waves
         WX = X // W
@@ -509,7 +525,7 @@ class AllRanksLayer:
         for s in range(R):
             d = self.dims[s]
             bias = None if self.bias is None else self.bias[s]
-            B.route(d, self.x[s], self.w_router, self.w_down, bias, self.bias_row_tokens, self.logits[s],
+            _route(self.rule, d, self.x[s], self.w_router, self.w_down, bias, self.bias_row_tokens, self.logits[s],
                     self.z[s], self.idx[s], self.w[s], self.ws[s], stream)
             B.pack_pools(d, self.z[s], self.idx[s], self.pools[s], pool_bytes, self.slot_of[s],
                          self.send_count[s], self.ws[s], stream)
@@ -556,9 +572,9 @@ class RaggedAllRanksLayer:
     to the rows that receiver's fullest wave keeps (per-expert arrival counts
     at set-up, see RaggedOneRankLayer); a number forces that bank size."""
 
-    def __init__(self, shape, inp, expert_rows, device="cuda", gather="fused", wave_rows=None, experts="act"):
+    def __init__(self, shape, inp, expert_rows, device="cuda", gather="fused", wave_rows=None, experts="act", rule=None):
         from workload.configs import exact_fit
-        self.experts = _expert_form(experts)
+        self.experts, self.rule = _expert_form(experts), _rule_of(rule, shape)
         self.wave_rows_arg = wave_rows
         self.shape, self.device, self.gather = shape, device, gather
         T, D, L, E, k, R = shape.tokens, shape.d_model, shape.latent, shape.n_experts, shape.top_k, shape.n_ranks
@@ -611,7 +627,7 @@ class RaggedAllRanksLayer:
         for s in range(R):
             d = self.send_dims[s]
             bias = None if self.bias is None else self.bias[s]
-            B.route(d, self.x[s], self.w_router, self.w_down, bias, self.bias_row_tokens, self.logits[s],
+            _route(self.rule, d, self.x[s], self.w_router, self.w_down, bias, self.bias_row_tokens, self.logits[s],
                     self.z[s], self.idx[s], self.w[s], self.ws_send[s], stream)
             B.pack_ragged(d, self.z[s], self.idx[s], self.send_rows[s], self.send_off[s], self.slot_of[s],
                           self.send_count[s], self.ws_send[s], stream)

@@ -502,3 +502,36 @@ def test_rows_and_rules_can_be_copied():
     logits = torch.randn((5, 8), generator=_gen(1)).to(DEV)
     for other in (copy.deepcopy(rule), pickle.loads(pickle.dumps(rule))):
         assert torch.equal(block.select_experts(logits, other)[0], block.select_experts(logits, rule)[0])
+
+
+def test_refusals():
+    x, w = torch.zeros((4, 64), device=DEV), torch.ones(64, device=DEV)
+    for call in (lambda: block.rms_norm(x, w[:63]), lambda: block.rms_norm(x, torch.ones((64, 2), device=DEV)[:, 0]),
+                 lambda: block.rms_norm(x, w.cpu()), lambda: block.rms_norm(x, w, residual=x[:3]),
+                 lambda: block.rms_norm(x, w, residual=x.bfloat16()), lambda: block.rms_norm(x[0], w),
+                 lambda: block.rms_norm(x.t(), w[:4]), lambda: block.rms_norm_backward(x, x.bfloat16(), w),
+                 lambda: block.rms_norm_backward(x, x, w, dstream=x[:, :32]), lambda: block.mx8_quantize(x.t()),
+                 lambda: block.select_experts(x, block.RouterRule(2, balance=w.bfloat16())),
+                 lambda: block.select_experts(x, block.RouterRule(2, balance=w[:63])),
+                 lambda: block.select_experts(x, block.RouterRule(2, balance=w.cpu())),
+                 lambda: block.select_experts_backward(x[:, :3], x[:, :2], x[:, :2].int(), x, block.RouterRule(2)),
+                 lambda: block.select_experts_backward(x[:, :2], x[:, :2], x[:, :2].long(), x, block.RouterRule(2)),
+                 lambda: block.swiglu_checkpoint(x, counts=torch.ones(2, dtype=torch.int32, device=DEV)),
+                 lambda: block.swiglu_checkpoint(x, counts=torch.ones(1, device=DEV)),
+                 lambda: block.swiglu_checkpoint(x, counts=torch.ones(1, dtype=torch.int32)),
+                 lambda: block.swiglu_checkpoint(x, out=x), lambda: block.swiglu_checkpoint(x, saved=block.mx8_quantize(x[:2])),
+                 lambda: block.swiglu_backward(x[:, :32], block.mx8_quantize(x), out=x.bfloat16()),
+                 lambda: block.swiglu_backward(x[:, :32], block.mx8_quantize(x), hidden_out=x)):
+        with pytest.raises((ValueError, TypeError)):
+            call()
+    for call in (lambda: block.rms_norm(x, w, eps=-1.0), lambda: block.rms_norm(x, w, eps=math.nan),
+                 lambda: block.rms_norm(x[:, :40], w[:40], form="mx8"), lambda: block.rms_norm(x[:, 1:33], w[:32], form="mx8"),
+                 lambda: block.rms_norm(x[:1].expand(4, 64), w), lambda: block.mx8_quantize(x[:, :40]),
+                 lambda: block.rms_norm(torch.zeros((1, 16416), device=DEV), torch.ones(16416, device=DEV)),
+                 lambda: block.select_experts(x, block.RouterRule(65)), lambda: block.select_experts(x, block.RouterRule(2, groups=3)),
+                 lambda: block.select_experts(x, block.RouterRule(2, groups=64, top_groups=1)),
+                 lambda: block.select_experts(x, block.RouterRule(2, group_best=0)),
+                 lambda: block.select_experts(x, block.RouterRule(2, scale=0.0)),
+                 lambda: block.swiglu_checkpoint(torch.zeros((4, 130), device=DEV)[:, 1:129])):
+        with pytest.raises(B.MoeError):
+            call()
