@@ -12,6 +12,7 @@ allocator (so that it can be captured, and calls on several streams share nothin
 tensors that do not fit, ``binding.MoeError`` for sizes that the library refuses.
 """
 
+import functools
 from dataclasses import dataclass, field
 
 import torch
@@ -163,6 +164,9 @@ def rms_norm(x, weight, residual=None, eps=1e-6, form="act"):
     return (y if q is None else q if y is None else (y, q)), (x if s is None else s)
 
 
+_workspace_bytes = functools.lru_cache(maxsize=256)(B.rms_norm_workspace_size)
+
+
 def rms_norm_backward(dy, s, weight, dstream=None, eps=1e-6):
     """(dx, dweight): the gradient of x (and of the residual) like dy, and the weight's in fp32.  s as rms_norm gave it; dstream:
     the gradient that reached s beside the norm."""
@@ -178,7 +182,7 @@ def rms_norm_backward(dy, s, weight, dstream=None, eps=1e-6):
     with dev:
         dx = _new(dy)
         dweight = torch.empty((cols,), dtype=torch.float32, device=dy.device)
-        ws = torch.empty((B.rms_norm_workspace_size(rows, cols),), dtype=torch.uint8, device=dy.device)
+        ws = torch.empty((_workspace_bytes(rows, cols),), dtype=torch.uint8, device=dy.device)
         B.rms_norm_backward(code, rows, cols, dy, ldy, s, lds, weight, wcode, eps, dstream, ldt, dx, cols * dy.itemsize,
                             dweight, ws, st)
     return dx, dweight

@@ -121,7 +121,7 @@ rms_norm_kernel(NormArgs a) {
 template <class C, class T, int V, bool STREAM>
 __global__ void __launch_bounds__(C::NT)
 rms_norm_backward_kernel(NormBackArgs a) {
-  constexpr bool AHEAD = C::NC <= 2 && C::NT < 1024;
+  constexpr bool AHEAD = C::NC <= 3 && C::NT < 1024;
   __shared__ float part[4][C::NT / 64];
   const int tid = threadIdx.x % C::TPR, sub = threadIdx.x / C::TPR;
   const int pieces = (int)(a.cols / V);
@@ -219,8 +219,11 @@ norm_dweight_kernel(const float* __restrict__ part, int64_t parts, int64_t cols,
   }
 }
 
-// Threads to a row by its pieces.  V = 1 (rows that are not 16-byte aligned) has the fewest forms.
-template <int V, class F>
+// Threads to a row by its pieces.  V = 1 (rows that are not 16-byte aligned) has
+// the fewest forms.  Rows of 6144 bf16 values: backward 575 us with 256 threads
+// of 3 pieces, 623 with 384 of 2, 608 with 768 of 1 (65,536 rows); forward 84
+// us with 384 threads, 88 with 256 (8192 rows).
+template <int V, bool BACKWARD, class F>
 void with_row(int64_t pieces, F f) {
   if constexpr (V == 1) {
     if (pieces <= 256) f(RowCfg<64, 4>());
@@ -231,7 +234,7 @@ void with_row(int64_t pieces, F f) {
     else if (pieces <= 128) f(RowCfg<64, 2>());
     else if (pieces <= 256) f(RowCfg<128, 2>());
     else if (pieces <= 512) f(RowCfg<256, 2>());
-    else if (pieces <= 768) f(RowCfg<384, 2>());
+    else if (pieces <= 768) f(RowCfg<BACKWARD ? 256 : 384, BACKWARD ? 3 : 2>());
     else if (pieces <= 1024) f(RowCfg<512, 2>());
     else if (V == 8 || pieces <= 2048) f(RowCfg<1024, 2>());  // 16,384 values at most
     else f(RowCfg<1024, V == 8 ? 2 : 4>());
@@ -240,7 +243,7 @@ void with_row(int64_t pieces, F f) {
 
 template <class T, int V, bool STREAM>
 hipError_t run_norm(const NormArgs& a, hipStream_t st) {
-  with_row<V>(a.cols / V, [&](auto cfg) {
+  with_row<V, false>(a.cols / V, [&](auto cfg) {
     using C = decltype(cfg);
     constexpr int64_t most = (int64_t)C::RPB << 21;  // rows of a launch, which has fewer than 2^32 threads
     for (int64_t r = 0; r < a.rows; r += most) {
@@ -262,7 +265,7 @@ hipError_t run_norm(const NormArgs& a, hipStream_t st) {
 
 template <class T, int V, bool STREAM>
 hipError_t run_norm_backward(const NormBackArgs& a, hipStream_t st) {
-  with_row<V>(a.cols / V, [&](auto cfg) {
+  with_row<V, true>(a.cols / V, [&](auto cfg) {
     using C = decltype(cfg);
     launch((rms_norm_backward_kernel<C, T, V, STREAM>), dim3((unsigned)(a.parts / C::RPB)), dim3(C::NT), 0, st, a);
   });
