@@ -34,12 +34,16 @@ class Mx8Rows(ScaledRows):
 
     _strides = staticmethod(_mx8_strides)
 
+    @property
+    def shape(self):
+        return tuple(self._codes.shape)   # a byte a value
+
     @classmethod
     def empty(cls, shape, device):
         """Rows of the given shape [..., rows, cols], not yet written."""
         cb, sb = _mx8_strides(shape[-1])
-        codes = torch.empty(tuple(shape[:-1]) + (cb,), dtype=torch.uint8, device=device)
-        scales = torch.empty(tuple(shape[:-1]) + (sb,), dtype=torch.uint8, device=device)
+        codes = torch.empty(shape, dtype=torch.uint8, device=device)
+        scales = torch.empty((*shape[:-1], sb), dtype=torch.uint8, device=device)
         return cls._made(codes, scales, shape[-1], cb, sb, (codes.data_ptr(), scales.data_ptr()))
 
 
@@ -98,7 +102,7 @@ def mx8_quantize(x):
     ld = _bytes(x, "x")
     with dev:
         q = Mx8Rows.empty(x.shape, x.device)
-        B.mx8_quantize(code, q.rows, q.cols, x, ld, q.arg, st)
+        B.mx8_quantize(code, x.numel() // q.cols, q.cols, x, ld, q.arg, st)
     return q
 
 
@@ -109,8 +113,8 @@ def mx8_dequantize(q, dtype=torch.bfloat16):
         raise TypeError(f"mx8_dequantize gives bf16 or fp32, not {dtype}")
     st, dev = _on(_eight(q, "q").codes)
     with dev:
-        out = torch.empty(q.shape, dtype=dtype, device=q.codes.device)
-        B.mx8_dequantize(code, q.rows, q.cols, q.arg, out, q.cols * out.itemsize, st)
+        out = torch.empty_like(q.codes, dtype=dtype, memory_format=torch.contiguous_format)
+        B.mx8_dequantize(code, out.numel() // q.cols, q.cols, q.arg, out, q.cols * out.itemsize, st)
     return out
 
 

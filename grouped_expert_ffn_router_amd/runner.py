@@ -781,11 +781,11 @@ class ScaledRows:
         """Checks the tensors and takes their strides."""
         codes, scales = self._codes, self._scales
         cb, sb = self._strides(self.cols)
+        cs, ss = codes.shape, scales.shape
         if codes.dtype != torch.uint8 or scales.dtype != torch.uint8:
             raise TypeError("codes and scales are uint8")
-        if codes.shape[:-1] != scales.shape[:-1] or codes.shape[-1] != cb or scales.shape[-1] < sb:
-            raise ValueError(f"codes {tuple(codes.shape)} and scales {tuple(scales.shape)} are not rows of {self.cols} "
-                             "values")
+        if cs[:-1] != ss[:-1] or cs[-1] != cb or ss[-1] < sb:
+            raise ValueError(f"codes {tuple(cs)} and scales {tuple(ss)} are not rows of {self.cols} values")
         if codes.device != scales.device:
             raise ValueError("codes and scales are on different devices")
         self.code_stride, self.scale_stride = _row_stride(codes, "codes"), _row_stride(scales, "scales")
