@@ -5,7 +5,9 @@
 // The order is that of the scores as 64-bit arithmetic has them.  It is found
 // in fp32: every comparison that decides something (neighbours among the k + 1
 // best, the groups around the last one kept) has to differ by more than the
-// fp32 scores can be off, or the token is ordered again from fp64 scores.
+// fp32 scores can be off.  Where neighbours do not (one token in 2000), the k + 1
+// best are put in order by their fp64 scores; where that leaves open which they
+// are, or the groups do not differ, the whole token is ordered again in fp64.
 // Without a bias the k best are ordered by the logits themselves, which both
 // scores are monotone in, so that there nothing is off.
 
@@ -81,14 +83,13 @@ struct GroupDiv {  // expert -> group; exact below 2048
   __device__ int of(int e) const { return (int)(((float)e + 0.5f) * inv); }
 };
 
-// One token in fp64: its k picks, pick r in lane r, an expert that is out as its
-// complement.  The lanes have the experts as in the kernel below.
-template <int EPL>
-__device__ __forceinline__ int select_exactly(const SelectRule& r, const float* row, const float* balance, int E, int k,
-                                           GroupDiv div) {
-  const int lane = lane_id(), e0 = lane * EPL;
-  double top = 0, inv_sum = 1;
-  if (r.score == SOFTMAX) {
+// The scores of one token's logits in fp64 (the softmax's sum by the whole wave).
+struct Score64 {
+  bool softmax;
+  double top, inv_sum;
+  __device__ Score64(const SelectRule& r, const float* row, int E) : softmax(r.score == SOFTMAX), top(0), inv_sum(1) {
+    if (!softmax) return;
+    const int lane = lane_id();
     float m = -INFINITY;
     for (int e = lane; e < E; e += 64) m = fmaxf(m, row[e]);
 #pragma unroll
@@ -98,13 +99,25 @@ __device__ __forceinline__ int select_exactly(const SelectRule& r, const float* 
     for (int e = lane; e < E; e += 64) s += exp((double)row[e] - top);
     inv_sum = 1.0 / wave_sum(s);
   }
+  // The key of expert e's rank.
+  __device__ uint64_t key(const float* row, const float* balance, int e) const {
+    const double l = row[e];
+    const double s = softmax ? exp(l - top) * inv_sum : 1.0 / (1.0 + exp(-l));
+    return l == -INFINITY ? OUT_KEY64 : rank_key64(balance ? s + (double)balance[e] : s);
+  }
+};
+
+// One token in fp64: its k picks, pick r in lane r, an expert that is out as its
+// complement.  The lanes have the experts as in the kernel below.
+template <int EPL>
+__device__ __forceinline__ int select_exactly(const SelectRule& r, const float* row, const float* balance, int E, int k,
+                                           GroupDiv div) {
+  const int lane = lane_id(), e0 = lane * EPL;
+  const Score64 scores(r, row, E);
   uint64_t key[EPL];
 #pragma unroll
   for (int j = 0; j < EPL; ++j) {
-    const int e = min(e0 + j, E - 1);
-    const double l = row[e];
-    const double s = r.score == SOFTMAX ? exp(l - top) * inv_sum : 1.0 / (1.0 + exp(-l));
-    key[j] = l == -INFINITY ? OUT_KEY64 : rank_key64(balance ? s + (double)balance[e] : s);
+    key[j] = scores.key(row, balance, min(e0 + j, E - 1));
     if (e0 + j >= E) key[j] = 0;
     __builtin_amdgcn_sched_barrier(0);  // one after the other: side by side they take hundreds of registers
   }
@@ -350,13 +363,13 @@ select_rule_kernel(SelectRule r, const float* __restrict__ logits, int64_t ld, c
     for (int j = 0; j < EPL; ++j)
       if (!(aligned ? keep : kept >> (div.of(e0 + j) & 63) & 1)) orig[j] = min(orig[j], OUT_KEY);
   }
-  // k rounds, and one more to see how near the next key is
+  // k rounds, and two more to see how near the next keys are
   uint32_t key[EPL];
 #pragma unroll
   for (int j = 0; j < EPL; ++j) key[j] = orig[j];
   sort_down<EPL>(key);
   int from = 0, chosen = 0;  // lane i: the lane that held pick i, and its key
-  const int rounds = balance && k < E ? k + 1 : k;
+  const int rounds = balance ? min(k + 2, E) : k;
   for (int i = 0; i < rounds; ++i) {
     const uint32_t m = wave_top(key[0]);
     const int owner = __ffsll((unsigned long long)__ballot(key[0] == m)) - 1;
@@ -370,12 +383,17 @@ select_rule_kernel(SelectRule r, const float* __restrict__ logits, int64_t ld, c
     }
   }
   const uint32_t mk = (uint32_t)chosen;
+  // lane i: whether picks i and i + 1 may be the other way round
+  bool near = false;
   if (balance) {
     const uint32_t after = (uint32_t)__shfl_down(chosen, 1);
     if (lane + 1 < rounds && after > OUT_KEY) {
       const float x = rank_value(mk), y = rank_value(after);
-      close |= !(x - y > unit + 0x1p-23f * (fabsf(x) + fabsf(y)));
+      near = !(x - y > unit + 0x1p-23f * (fabsf(x) + fabsf(y)));
     }
+    const uint64_t nears = __ballot(near);
+    near = nears & ((1ull << k) - 1);
+    close |= (nears >> (k - 1) & 3) == 3;  // which the first k + 1 are is open
   }
   int e;
   bool out;
@@ -387,8 +405,8 @@ select_rule_kernel(SelectRule r, const float* __restrict__ logits, int64_t ld, c
     // a lane's equal keys were taken in the order of its registers
     int nth = 0;
     const int from1 = __shfl_up(from, 1), chosen1 = __shfl_up(chosen, 1);
-    if (__any(lane > 0 && lane < k && from1 == from && chosen1 == chosen))
-      for (int d = 1; d < k; ++d) {
+    if (__any(lane > 0 && lane <= k && from1 == from && chosen1 == chosen))
+      for (int d = 1; d <= k; ++d) {
         const int from_d = __shfl(from, lane - d), chosen_d = __shfl(chosen, lane - d);
         nth += lane >= d && from_d == from && chosen_d == chosen;
       }
@@ -402,6 +420,20 @@ select_rule_kernel(SelectRule r, const float* __restrict__ logits, int64_t ld, c
     }
     e = from * EPL + at;
     out = mk <= OUT_KEY;
+    if (near) {  // the first k + 1 in their order
+      const Score64 scores(r, row, E);
+      const int n = min(k + 1, E);
+      const uint64_t mine = out ? OUT_KEY64 : scores.key(row, balance, lane < n ? e : 0);
+      int place = 0;
+      for (int p = 0; p < n; ++p) {
+        const uint64_t other = ((uint64_t)(uint32_t)__builtin_amdgcn_readlane((int)(mine >> 32), p) << 32) |
+                               (uint32_t)__builtin_amdgcn_readlane((int)mine, p);
+        place += other > mine || (other == mine && __builtin_amdgcn_readlane(e, p) < e);
+      }
+      const int moved = __builtin_amdgcn_ds_permute((lane < n ? place : lane) * 4, out ? ~e : e);
+      out = moved < 0;
+      e = out ? ~moved : moved;
+    }
   }
   float x = -INFINITY;
   if (lane < k && !out) x = row[e];

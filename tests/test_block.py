@@ -279,6 +279,34 @@ def test_select_and_its_gradient(T, E, k, rule):
     assert ((got - want).abs() <= size * (64 + 2 * spread) * U + 2.0 ** -126).all()
 
 
+@pytest.mark.parametrize("rule", RULES, ids=lambda r: "-".join(str(v) for v in r.values()))
+@pytest.mark.parametrize("E,k", [(8, 2), (24, 4), (32, 31), (33, 3), (64, 8), (100, 5), (128, 1), (256, 8), (300, 16), (384, 8), (512, 31),
+                                 (516, 8)])
+def test_select_for_many_tokens(E, k, rule):
+    """Batches large enough that a wave takes two tokens (an odd number of them): each token as in 64 bits."""
+    rule = dict(rule)
+    groups = rule.get("groups", 1)
+    if E % groups or rule.get("top_groups", 1) * (E // groups) < k:
+        pytest.skip("a rule this shape has no room for")
+    gen = _gen(E * 3 + k)
+    T, some = 5003, 60
+    logits = torch.randn((some, E), generator=gen) * 2
+    logits[1, ::2], logits[2], logits[3, 1:], logits[4, :E // 2] = -math.inf, -math.inf, -math.inf, -math.inf
+    logits[5], logits[6] = 0.25, -0.0
+    logits[7, E // 2] = math.nan
+    balance = torch.randn((E,), generator=gen) * 0.1 if rule.pop("balance", False) else None
+    r = block.RouterRule(k, balance=None if balance is None else balance.to(DEV), **rule)
+    at = torch.randint(0, some, (T,), generator=gen)
+    idx, w = (t.cpu() for t in block.select_experts(logits[at].to(DEV), r))
+    fine = torch.arange(some) != 7
+    want_idx, want_w = R.select(logits.double()[fine], k, balance=None if balance is None else balance.double(), **rule)
+    place = torch.cumsum(fine, 0) - 1
+    ok = at != 7
+    assert torch.equal(idx[ok], want_idx[place[at[ok]]])
+    _weights_within(w[ok], want_w[place[at[ok]]], logits.double()[at[ok]])
+    assert torch.equal(idx[~ok], torch.arange(k, dtype=torch.int32).expand(int((~ok).sum()), k)) and w[~ok].isnan().all()
+
+
 def test_select_strided_logits():
     wide = torch.randn((70, 120), generator=_gen(2)).to(DEV)
     rule = block.RouterRule(3, score="sigmoid", balance=torch.zeros(101, device=DEV))
@@ -315,7 +343,7 @@ def test_equal_and_nearly_equal_scores(score, groups):
 
 def test_many_tokens_are_ordered_as_in_64_bits():
     """Enough tokens that some neighbours are closer than fp32 scores tell apart."""
-    logits = torch.randn((40000, 384), generator=_gen(4)) * 1.5
+    logits = torch.randn((40001, 384), generator=_gen(4)) * 1.5
     balance = torch.randn((384,), generator=_gen(5)) * 0.05
     for score in ("sigmoid", "softmax"):
         rule = block.RouterRule(8, score=score, balance=balance.to(DEV), groups=8, top_groups=4)
