@@ -307,6 +307,24 @@ def test_select_for_many_tokens(E, k, rule):
     assert torch.equal(idx[~ok], torch.arange(k, dtype=torch.int32).expand(int((~ok).sum()), k)) and w[~ok].isnan().all()
 
 
+@pytest.mark.parametrize("E,groups,top_groups,best,k", [(1, 1, 1, 2, 1), (2, 2, 1, 2, 1), (12, 12, 4, 1, 4), (64, 64, 3, 2, 3), (96, 6, 2, 1, 4),
+                                                        (128, 2, 1, 2, 8), (320, 16, 5, 2, 6), (384, 8, 4, 2, 8), (384, 8, 7, 1, 32),
+                                                        (1536, 48, 7, 2, 8), (2048, 64, 10, 2, 16)])
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+def test_select_in_groups_of_any_size(E, groups, top_groups, best, k, score):
+    gen = _gen(E + groups)
+    logits = torch.randn((24, E), generator=gen)
+    logits[1, torch.randperm(E, generator=gen)[:E // 2]] = -math.inf
+    logits[2, :-1] = -math.inf
+    logits[3] = 1.5
+    for b in (None, torch.randn((E,), generator=gen) * 0.1, torch.full((E,), -0.25)):
+        kw = dict(score=score, groups=groups, top_groups=top_groups, group_best=best)
+        idx, w = block.select_experts(logits.to(DEV), block.RouterRule(k, balance=None if b is None else b.to(DEV), **kw))
+        want_idx, want_w = R.select(logits.double(), k, balance=None if b is None else b.double(), **kw)
+        assert torch.equal(idx.cpu(), want_idx)
+        _weights_within(w, want_w, logits.double())
+
+
 def test_select_strided_logits():
     wide = torch.randn((70, 120), generator=_gen(2)).to(DEV)
     rule = block.RouterRule(3, score="sigmoid", balance=torch.zeros(101, device=DEV))
