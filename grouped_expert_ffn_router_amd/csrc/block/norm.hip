@@ -174,7 +174,8 @@ rms_norm_backward_kernel(NormBackArgs a) {
     Row next;
     if (AHEAD) load(next, row + stride);
     row_sums<C>(sums, part + slot);
-    const float r = 1.0f / sqrtf(sums[0] / (float)a.cols + a.eps);
+    // (0 past the last row, where eps 0 would make it infinite)
+    const float r = row < a.rows ? 1.0f / sqrtf(sums[0] / (float)a.cols + a.eps) : 0.0f;
     const float mean = sums[1] * r / (float)a.cols;  // of g n
 #pragma unroll
     for (int i = 0; i < C::NC; ++i) {

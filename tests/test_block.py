@@ -189,6 +189,23 @@ def test_rms_norm_gradient_by_differences():
         assert abs((loss(x, w + d) - loss(x, w - d)) / (2 * step) - float(dw[j])) < 1e-5
 
 
+@pytest.mark.parametrize("rows,cols", [(1, 64), (2, 5), (5, 512), (1027, 64), (4099, 5)])
+def test_rms_norm_backward_without_eps(rows, cols):
+    """Workgroups of several rows have places past the last row."""
+    gen = _gen(rows)
+    s, dy, w = _rand(gen, (rows, cols), torch.float32), _rand(gen, (rows, cols), torch.float32), _rand(gen, (cols,), torch.float32)
+    dx, dw = block.rms_norm_backward(dy, s, w, eps=0.0)
+    want, dw_want = R.norm_backward(R.bits64(dy), R.bits64(s), R.bits64(w), None, 0.0)
+    assert torch.isfinite(dx).all() and torch.isfinite(dw).all()
+    # as in test_rms_norm_backward; a column's sum takes `rows` / 16 + 100 steps at most
+    r = (R.bits64(s) ** 2).mean(-1, keepdim=True) ** -0.5
+    n, g = (R.bits64(s) * r).abs(), (R.bits64(dy) * R.bits64(w)).abs()
+    rel = _norm_slack(cols)
+    assert ((R.bits64(dx) - want).abs() <= r * (g * (rel + 6 * U) + n * (g * n).mean(-1, keepdim=True) * (4 * rel + 100 * U))
+            + want.abs() * 2 * U).all()
+    assert ((R.bits64(dw) - dw_want).abs() <= (R.bits64(dy).abs() * n).sum(0) * (rel + (rows / 16 + 100) * U)).all()
+
+
 def test_rms_norm_in_place():
     """The sum over the residual, the norm over x; the gradient over either of its inputs."""
     gen = _gen(8)
