@@ -227,7 +227,16 @@ class RouterRule:
 
     def choose(self, logits, idx, w, stream=None):
         """Writes the choice for logits [T, E] into idx [T, k] int32 and w [T, k] fp32 (contiguous)."""
-        T, E = logits.shape
+        T, E = _logits(logits)
+        for t, dtype, what in ((idx, torch.int32, "idx"), (w, torch.float32, "w")):
+            _like(t, (T, self.top_k), dtype, logits.device, what)
+            if not t.is_contiguous():
+                raise ValueError(f"{what} must be contiguous")
+        st, dev = _on(logits)
+        with dev:
+            self._choose(logits, T, E, idx, w, st if stream is None else stream)
+
+    def _choose(self, logits, T, E, idx, w, stream):
         if self.balance is not None:
             if self.balance.dtype != torch.float32:
                 raise ValueError(f"balance is {self.balance.dtype}, not fp32")
@@ -248,7 +257,7 @@ def select_experts(logits, rule):
     with dev:
         idx = torch.empty((T, rule.top_k), dtype=torch.int32, device=logits.device)
         w = torch.empty((T, rule.top_k), dtype=torch.float32, device=logits.device)
-        rule.choose(logits, idx, w, st)
+        rule._choose(logits, T, E, idx, w, st)
     return idx, w
 
 

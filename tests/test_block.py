@@ -569,6 +569,7 @@ def test_rows_and_rules_can_be_copied():
 
 def test_refusals():
     x, w = torch.zeros((4, 64), device=DEV), torch.ones(64, device=DEV)
+    i2, w2 = torch.zeros((4, 2), dtype=torch.int32, device=DEV), torch.zeros((4, 2), device=DEV)
     for call in (lambda: block.rms_norm(x, w[:63]), lambda: block.rms_norm(x, torch.ones((64, 2), device=DEV)[:, 0]),
                  lambda: block.rms_norm(x, w.cpu()), lambda: block.rms_norm(x, w, residual=x[:3]),
                  lambda: block.rms_norm(x, w, residual=x.bfloat16()), lambda: block.rms_norm(x[0], w),
@@ -577,6 +578,10 @@ def test_refusals():
                  lambda: block.select_experts(x, block.RouterRule(2, balance=w.bfloat16())),
                  lambda: block.select_experts(x, block.RouterRule(2, balance=w[:63])),
                  lambda: block.select_experts(x, block.RouterRule(2, balance=w.cpu())),
+                 lambda: block.RouterRule(2).choose(x, i2, w2[:3]), lambda: block.RouterRule(2).choose(x, i2.long(), w2),
+                 lambda: block.RouterRule(2).choose(x, i2, w2.bfloat16()), lambda: block.RouterRule(2).choose(x.bfloat16(), i2, w2),
+                 lambda: block.RouterRule(2).choose(x, i2, x[:, :2]), lambda: block.RouterRule(2).choose(x, i2.cpu(), w2),
+                 lambda: block.RouterRule(2).choose(x[0], i2, w2), lambda: block.RouterRule(2).choose(x.cpu(), i2.cpu(), w2.cpu()),
                  lambda: block.select_experts_backward(x[:, :3], x[:, :2], x[:, :2].int(), x, block.RouterRule(2)),
                  lambda: block.select_experts_backward(x[:, :2], x[:, :2], x[:, :2].long(), x, block.RouterRule(2)),
                  lambda: block.swiglu_checkpoint(x, counts=torch.ones(2, dtype=torch.int32, device=DEV)),
