@@ -228,25 +228,54 @@ __device__ __forceinline__ void wait_reads(Frags<2>& f, int (&s)[4]) {
                ::"memory");
 }
 
+// Inclusive prefix sum over the wave.
+__device__ __forceinline__ int wave_prefix(int v) {
+  const int lane = lane_id();
+#pragma unroll
+  for (int off = 1; off < 64; off *= 2) {
+    const int x = __shfl_up(v, off);
+    v += lane >= off ? x : 0;
+  }
+  return v;
+}
+
 // Tile of workgroup `bid`: the tiles of the rows that exist, group by group and
 // 4 tile rows at a time inside a group, in 8 contiguous ranges, one for each
 // XCD (workgroups go round-robin to the XCDs), so that an XCD's L2 sees
-// neighbouring tiles.  False: none is left.
+// neighbouring tiles.  The groups' tiles are added up by a wave, 64 groups at a
+// time: groups of 128 rows x 128 x 512 take 7 us for 64 of them, 15 for 384, 480
+// for 4096 (counts looked at one after the other, as in ops/mx.hip: 14, 74, 5300).
+// False: none is left.
 template <int BM>
 __device__ __forceinline__ bool tile_of(const int32_t* counts, int max_rows, int groups, int tiles_n, int bid, int& g, int& tm,
                                         int& tn) {
-  int total = 0;
-  for (int i = 0; i < groups; ++i) total += (group_rows(counts, i, max_rows) + BM - 1) / BM * tiles_n;
+  const int lane = lane_id();
+  auto tile_rows = [&](int i) { return i < groups ? (group_rows(counts, i, max_rows) + BM - 1) / BM : 0; };
+  int total = 0, upto = 0;  // upto: of the first 64 groups, a lane's and those before it
+  for (int first = 0; first < groups; first += 64) {
+    const int p = wave_prefix(tile_rows(first + lane));
+    if (first == 0) upto = p;
+    total += __builtin_amdgcn_readlane(p, 63);
+  }
+  total *= tiles_n;
   const int xcd = bid & 7, at = bid >> 3, per = total >> 3, rem = total & 7;
   if (at >= per + (xcd < rem ? 1 : 0)) return false;
-  int t = xcd * per + min(xcd, rem) + at, mt = 0;
-  for (g = 0; g < groups; ++g) {
-    mt = (group_rows(counts, g, max_rows) + BM - 1) / BM;
-    if (t < mt * tiles_n) break;
-    t -= mt * tiles_n;
+  int t = xcd * per + min(xcd, rem) + at, first = 0;
+  for (;;) {  // to the 64 groups that have it
+    const int all = __builtin_amdgcn_readlane(upto, 63) * tiles_n;
+    if (t < all) break;
+    t -= all;
+    first += 64;
+    if (first >= groups) return false;
+    upto = wave_prefix(tile_rows(first + lane));
   }
-  const int band = t / (4 * tiles_n), first = band * 4, size = min(mt - first, 4), rest = t - band * 4 * tiles_n;
-  tm = first + rest % size;
+  const int in = __ffsll((unsigned long long)__ballot(t < upto * tiles_n)) - 1;
+  const int before = in > 0 ? __builtin_amdgcn_readlane(upto, max(in - 1, 0)) : 0;
+  const int mt = __builtin_amdgcn_readlane(upto, in) - before;
+  g = first + in;
+  t -= before * tiles_n;
+  const int band = t / (4 * tiles_n), row = band * 4, size = min(mt - row, 4), rest = t - band * 4 * tiles_n;
+  tm = row + rest % size;
   tn = rest / size;
   return true;
 }

@@ -2,12 +2,14 @@
 // scores, a balance bias that counts for the choice alone, groups of experts,
 // the k best, weights renormalised over them), and the logits' gradient (gfx950).
 //
-// The order is that of the scores as 64-bit arithmetic has them.  It is found
+// The order is that of the scores as 64-bit arithmetic has them (ranks nearer
+// than its own rounding, a few 2^-53 of them, in either order).  It is found
 // in fp32: every comparison that decides something (neighbours among the k + 1
 // best, the groups around the last one kept) has to differ by more than the
-// fp32 scores can be off.  Where neighbours do not (one token in 2000), the k + 1
-// best are put in order by their fp64 scores; where that leaves open which they
-// are, or the groups do not differ, the whole token is ordered again in fp64.
+// fp32 scores can be off.  Where neighbours do not (about one token in 2000), the
+// k + 1 best are put in order by their fp64 scores; where that leaves open which
+// they are, all experts by theirs.  Groups that do not differ are chosen by fp64
+// scores, and the experts in them as before.
 // Without a bias the k best are ordered by the logits themselves, which both
 // scores are monotone in, so that there nothing is off.
 
@@ -107,52 +109,58 @@ struct Score64 {
   }
 };
 
-// One token in fp64: its k picks, pick r in lane r, an expert that is out as its
-// complement.  The lanes have the experts as in the kernel below.
+// One token's ranks in fp64; the lanes have the experts as in the kernel below.
 template <int EPL>
-__device__ __forceinline__ int select_exactly(const SelectRule& r, const float* row, const float* balance, int E, int k,
-                                           GroupDiv div) {
-  const int lane = lane_id(), e0 = lane * EPL;
+__device__ __forceinline__ void keys64(const SelectRule& r, const float* row, const float* balance, int E, uint64_t (&key)[EPL]) {
+  const int e0 = lane_id() * EPL;
   const Score64 scores(r, row, E);
-  uint64_t key[EPL];
 #pragma unroll
   for (int j = 0; j < EPL; ++j) {
     key[j] = scores.key(row, balance, min(e0 + j, E - 1));
     if (e0 + j >= E) key[j] = 0;
-    __builtin_amdgcn_sched_barrier(0);  // one after the other: side by side they take hundreds of registers
+    // two at a time: side by side they take hundreds of registers
+    if (j & 1) __builtin_amdgcn_sched_barrier(0);
   }
-  if (r.top_groups < r.groups) {
-    uint64_t mine = 0;  // lane g: the score of group g
-    for (int g = 0; g < r.groups; ++g) {
-      uint64_t a = 0, b = 0;  // this lane's two best of the group
-#pragma unroll
-      for (int j = 0; j < EPL; ++j) {
-        const uint64_t x = div.of(e0 + j) == g ? key[j] : 0;
-        if (x > a) { b = a; a = x; }
-        else if (x > b) b = x;
-      }
-      const uint64_t first = wave_max64(a);
-      const int owner = __ffsll((unsigned long long)__ballot(a == first)) - 1;
-      const uint64_t second = wave_max64(lane == owner ? b : a);
-      uint64_t score = first;
-      if (r.group_best > 1 && second > OUT_KEY64) score = rank_key64(rank_value64(first) + rank_value64(second));
-      if (lane == g) mine = score;
-    }
-    int better = 0;
-    for (int g = 0; g < r.groups; ++g) {
-      const uint64_t other = ((uint64_t)(uint32_t)__builtin_amdgcn_readlane((int)(mine >> 32), g) << 32) |
-                             (uint32_t)__builtin_amdgcn_readlane((int)mine, g);
-      better += other > mine || (other == mine && g < lane);
-    }
-    const uint64_t kept = __ballot(lane < r.groups && better < r.top_groups);
+}
+
+// The groups that stay by those ranks, a bit each.
+template <int EPL>
+__device__ __forceinline__ uint64_t groups64(const SelectRule& r, GroupDiv div, const uint64_t (&key)[EPL]) {
+  const int lane = lane_id(), e0 = lane * EPL;
+  uint64_t mine = 0;  // lane g: the score of group g
+  for (int g = 0; g < r.groups; ++g) {
+    uint64_t a = 0, b = 0;  // this lane's two best of the group
 #pragma unroll
     for (int j = 0; j < EPL; ++j) {
-      const int e = e0 + j;
-      if (e >= E) continue;
-      if (!(kept >> div.of(e) & 1)) key[j] = OUT_KEY64;
-      else if (!balance) key[j] = rank_key64((double)row[e]);
+      const uint64_t x = div.of(e0 + j) == g ? key[j] : 0;
+      if (x > a) { b = a; a = x; }
+      else if (x > b) b = x;
     }
+    const uint64_t first = wave_max64(a);
+    const int owner = __ffsll((unsigned long long)__ballot(a == first)) - 1;
+    const uint64_t second = wave_max64(lane == owner ? b : a);
+    uint64_t score = first;
+    if (r.group_best > 1 && second > OUT_KEY64) score = rank_key64(rank_value64(first) + rank_value64(second));
+    if (lane == g) mine = score;
   }
+  int better = 0;
+  for (int g = 0; g < r.groups; ++g) {
+    const uint64_t other = ((uint64_t)(uint32_t)__builtin_amdgcn_readlane((int)(mine >> 32), g) << 32) |
+                           (uint32_t)__builtin_amdgcn_readlane((int)mine, g);
+    better += other > mine || (other == mine && g < lane);
+  }
+  return __ballot(lane < r.groups && better < r.top_groups);
+}
+
+// One token's k picks by its ranks in fp64 among the experts of the groups in
+// `kept` (group g in bit g step): pick r in lane r, an expert that is out as its
+// complement.
+template <int EPL>
+__device__ __forceinline__ int picks64(GroupDiv div, uint64_t kept, int step, int E, int k, uint64_t (&key)[EPL]) {
+  const int lane = lane_id(), e0 = lane * EPL;
+#pragma unroll
+  for (int j = 0; j < EPL; ++j)
+    if (e0 + j < E && !(kept >> (div.of(e0 + j) * step) & 1)) key[j] = OUT_KEY64;
   int my = 0;
   for (int i = 0; i < k; ++i) {
     uint64_t best = 0;
@@ -216,10 +224,10 @@ __device__ __forceinline__ void merge_two(uint32_t& a, uint32_t& b, uint32_t a2,
 // it, and a shift of that lane's keys.  Which expert a key was is looked up
 // once at the end.
 //
-// Bound by instructions (390 a wave for 8 of 384 without groups and bias), not by
+// Bound by instructions (387 a wave for 8 of 384 without groups and bias), not by
 // the 4 E bytes a token: 65,536 tokens of 384 experts 40 us (the bytes 22 at a
-// copy's rate), in 8 groups with a bias 78; 8192 tokens 7.3 and 12; one token
-// 3.4 and 5.1, the length of the chain.  All ranks equal: 46 us for 8192 tokens.
+// copy's rate), in 8 groups with a bias 73; 8192 tokens 7.3 and 12; one token
+// 3.3 and 5.1, the length of the chain.  All ranks equal: 51 us for 8192 tokens.
 // Two tokens a wave (32 lanes with 12 experts each) took 37 us and 78 for the
 // first two, 20 for 8192 in groups.  `wide`: rows may be read 8 or 16 bytes at a time.
 template <int EPL>
@@ -310,7 +318,8 @@ select_rule_kernel(SelectRule r, const float* __restrict__ logits, int64_t ld, c
   // of the largest score, exp and its argument 3 2^-24, the sum EPL + 8.
   const float unit = r.score == SOFTMAX ? inv_sum * ((EPL + 12) * 0x1p-23f) : 0x1p-21f;
   const GroupDiv div{(float)r.groups / (float)E};
-  bool close = false;
+  uint64_t kept = ~0ull;  // groups that stay: group g in bit g kept_step
+  int kept_step = 1;
   if (grouped) {
     // Groups of whole lanes, a power of two of them, are reduced side by side
     // in their lanes; others one after the other, group g's score in lane g.
@@ -352,17 +361,23 @@ select_rule_kernel(SelectRule r, const float* __restrict__ logits, int64_t ld, c
       const uint32_t other = (uint32_t)__builtin_amdgcn_readlane((int)mine, g * stride);
       better += other > mine || (other == mine && g < gid);
     }
-    const bool keep = gid < r.groups && better < r.top_groups;
     // the last group kept and the first one dropped; two that are out tie by index
     const int last = __ffsll((unsigned long long)__ballot(gid < r.groups && better == r.top_groups - 1)) - 1;
     const int next = __ffsll((unsigned long long)__ballot(gid < r.groups && better == r.top_groups)) - 1;
     const uint32_t klast = (uint32_t)__builtin_amdgcn_readlane((int)mine, last);
     const uint32_t knext = (uint32_t)__builtin_amdgcn_readlane((int)mine, next);
-    if (knext > OUT_KEY) {
-      const float x = rank_value(klast), y = rank_value(knext);
-      close |= !(x - y > 2 * unit + 0x1p-22f * (fabsf(x) + fabsf(y)));
+    const float x = rank_value(klast), y = rank_value(knext);
+    bool keep;  // this lane's experts, where groups are of whole lanes
+    if (knext > OUT_KEY && !(x - y > 2 * unit + 0x1p-22f * (fabsf(x) + fabsf(y)))) {
+      uint64_t exact[EPL];
+      keys64<EPL>(r, row, balance, E, exact);
+      kept = groups64<EPL>(r, div, exact);
+      keep = kept >> (gid & 63) & 1;
+    } else {
+      keep = gid < r.groups && better < r.top_groups;
+      kept = __ballot(keep);
+      kept_step = stride;
     }
-    const uint64_t kept = __ballot(keep);
 #pragma unroll
     for (int j = 0; j < EPL; ++j)
       if (!(aligned ? keep : kept >> (div.of(e0 + j) & 63) & 1)) orig[j] = min(orig[j], OUT_KEY);
@@ -387,22 +402,23 @@ select_rule_kernel(SelectRule r, const float* __restrict__ logits, int64_t ld, c
     }
   }
   const uint32_t mk = (uint32_t)chosen;
-  // lane i: whether picks i and i + 1 may be the other way round
-  bool near = false;
+  bool near = false, open = false;  // the first k + 1 may be in another order; which they are is open
   if (balance) {
     const uint32_t after = (uint32_t)__shfl_down(chosen, 1);
     if (lane + 1 < rounds && after > OUT_KEY) {
       const float x = rank_value(mk), y = rank_value(after);
       near = !(x - y > unit + 0x1p-23f * (fabsf(x) + fabsf(y)));
     }
-    const uint64_t nears = __ballot(near);
+    const uint64_t nears = __ballot(near);  // bit i: picks i and i + 1 may be the other way round
     near = nears & ((1ull << k) - 1);
-    close |= (nears >> (k - 1) & 3) == 3;  // which the first k + 1 are is open
+    open = (nears >> (k - 1) & 3) == 3;
   }
   int e;
   bool out;
-  if (__any(close)) {
-    const int my = select_exactly<EPL>(r, row, balance, E, k, div);
+  if (open) {
+    uint64_t exact[EPL];
+    keys64<EPL>(r, row, balance, E, exact);
+    const int my = picks64<EPL>(div, kept, kept_step, E, k, exact);
     out = my < 0;
     e = out ? ~my : my;
   } else {

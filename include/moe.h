@@ -499,7 +499,8 @@ int moe_mxb_gemm(int32_t out_dtype, int32_t groups, int64_t max_rows, int64_t n,
  * y or y8 is given.  cols <= MOE_NORM_COLS_MAX.  Addresses and strides are
  * multiples of the value's size; with 16-byte aligned rows and cols a multiple
  * of 8 (bf16) or 4 (fp32) values are moved 16 bytes at a time.  Squares are
- * summed in fp32, so a row whose squares exceed 2^127 gives 0. */
+ * summed in fp32, so a row whose squares exceed 2^127 gives 0; a row of zeros
+ * with eps 0 gives NaN. */
 #define MOE_NORM_COLS_MAX 16384
 int moe_rms_norm(int32_t act_dtype, int64_t rows, int64_t cols, const void* x, int64_t x_stride_bytes,
                  const void* residual, int64_t residual_stride_bytes, const void* weight, int32_t weight_dtype, float eps,
@@ -527,13 +528,14 @@ int moe_rms_norm_backward(int32_t act_dtype, int64_t rows, int64_t cols, const v
  *   rank         score + balance[e] (the bias counts for the choice alone)
  *   groups       the experts in `groups` blocks of E / groups (at most 64); the
  *                top_groups blocks with the largest sum of their group_best (1
- *                or 2) largest ranks stay, equal ones by lower index
+ *                or 2) largest ranks stay, equal ones by lower index (-infinity
+ *                counts only where a block has no other rank)
  *   choice       the top_k largest ranks of the groups that stay, in descending
  *                order, equal ones by lower expert index
  *   weight       score of a chosen expert, divided by the sum over the chosen
  *                ones if `renormalise`, times `scale`
- * Ranks are compared as 64-bit arithmetic has them (without a bias, the logits
- * are).  An expert whose logit or rank is -infinity is out: it is chosen only
+ * Ranks are compared as 64-bit arithmetic has them, to its rounding (without a
+ * bias, the logits are).  An expert whose logit or rank is -infinity is out: it is chosen only
  * after all others, by lower index, with weight 0.  Where the chosen scores add
  * up to 0 in fp32 (all are out, or below 2^-149) the weights are 0.  A token
  * with a NaN among its logits or ranks, or under softmax a logit of +infinity,
@@ -576,6 +578,7 @@ int moe_swiglu_checkpoint(int32_t act_dtype, int32_t groups, int64_t max_rows, i
 
 /* Its backward pass at the saved values a (gate) and b (up): with
  * sg = sigmoid(a), dgate = dh * b * sg * (1 + a * (1 - sg)) and dup = dh * a * sg.
+ * A saved block that held a NaN or an infinity reads as NaN.
  *   dgate_up  as gate_up, output
  *   h         h again, from the saved values (the second projection's weight
  *             gradient needs it), or NULL */
