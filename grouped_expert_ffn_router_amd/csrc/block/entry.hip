@@ -208,8 +208,8 @@ int moe_rms_norm_backward(int32_t act_dtype, int64_t rows, int64_t cols, const v
     if (dsum && (rc = rows_ok(dsum, dsum_stride_bytes, cols, size, size, "dsum"))) return rc;
     NEED(ws, "ws");
   }
-  const NormBackArgs a{rows, cols, dy, sum, dsum, weight, dy_stride_bytes, sum_stride_bytes, dsum_stride_bytes, dx_stride_bytes,
-                       dx, dweight, (float*)ws, norm_parts(rows, cols), eps, bf16, weight_dtype == MOE_ACT_F32};
+  NormBackArgs a{rows, cols, dy, sum, dsum, weight, dy_stride_bytes, sum_stride_bytes, dsum_stride_bytes, dx_stride_bytes,
+                 dx, dweight, (float*)ws, 0, eps, bf16, weight_dtype == MOE_ACT_F32};
   if (rows > 0)
     LAUNCH("rms_norm_backward", launch_rms_norm_backward(a, (hipStream_t)stream), "moe_rms_norm_backward");
   LAUNCH("norm_dweight", launch_norm_dweight(a, (hipStream_t)stream), "moe_rms_norm_backward dweight");

@@ -206,6 +206,40 @@ def test_rms_norm_backward_without_eps(rows, cols):
     assert ((R.bits64(dw) - dw_want).abs() <= (R.bits64(dy).abs() * n).sum(0) * (rel + (rows / 16 + 100) * U)).all()
 
 
+@pytest.mark.parametrize("dtype", ACTS)
+@pytest.mark.parametrize("cols", [1, 3, 4, 7, 8, 9, 63, 100, 129, 191, 255, 257, 509, 1023, 1029, 2047, 3001, 4095, 6143, 8193, 16383])
+def test_rms_norm_rows_of_any_alignment(cols, dtype):
+    """Inputs at any offset, outputs inside wider rows whose other values stay; both passes."""
+    rows, gen = 19, _gen(cols)
+    code, size = runner._DTYPE[dtype], dtype.itemsize
+    wide = lambda at, pad: torch.full((rows, cols + pad), 7.0, dtype=dtype, device=DEV)[:, at:at + cols]  # noqa: E731
+    x, res, dy, t = (wide(at, at + 1) for at in (1, 0, 3, 2))
+    for v in (x, res, dy, t):
+        v.copy_(_rand(gen, (rows, cols), dtype))
+    w = torch.full((cols + 3,), 7.0, dtype=dtype, device=DEV)[3:].copy_(_rand(gen, (cols,), dtype))
+    buf = [torch.full((rows, cols + 5), 7.0, dtype=dtype, device=DEV) for _ in range(3)]
+    s, y, dx = (b[:, at:at + cols] for at, b in zip((1, 2, 3), buf))
+    ld = lambda v: v.stride(0) * size  # noqa: E731
+    B.rms_norm(code, rows, cols, x, ld(x), res, ld(res), w, code, 1e-5, s, ld(s), y, ld(y), None)
+    dw = torch.full((cols + 2,), 7.0, device=DEV)
+    ws = torch.empty(B.rms_norm_workspace_size(rows, cols), dtype=torch.uint8, device=DEV)
+    B.rms_norm_backward(code, rows, cols, dy, ld(dy), s, ld(s), w, code, 1e-5, t, ld(t), dx, ld(dx), dw[1:], ws)
+    for at, b in zip((1, 2, 3), buf):
+        assert (b[:, :at] == 7).all() and (b[:, at + cols:] == 7).all()
+    assert dw[0] == 7 and dw[-1] == 7
+    want, s64 = R.norm(R.bits64(x), R.bits64(w), R.bits64(res), 1e-5)
+    _within(s, s64, s64.abs() * U, "s")
+    _within(y, want, want.abs() * _norm_slack(cols), "y")
+    s, dy, w, t = R.bits64(s), R.bits64(dy), R.bits64(w), R.bits64(t)
+    want, dw_want = R.norm_backward(dy, s, w, t, 1e-5)
+    r = ((s * s).mean(-1, keepdim=True) + 1e-5) ** -0.5   # the bounds of test_rms_norm_backward
+    n, g = (s * r).abs(), (dy * w).abs()
+    rel = _norm_slack(cols)
+    _within(dx, want, r * (g * (rel + 6 * U) + n * (g * n).mean(-1, keepdim=True) * (4 * rel + 100 * U)) + (want.abs() + t.abs()) * 2 * U,
+            "dx")
+    assert ((R.bits64(dw[1:-1]) - dw_want).abs() <= (dy.abs() * n).sum(0) * (rel + 100 * U) + dw_want.abs() * U).all()
+
+
 def test_rms_norm_in_place():
     """The sum over the residual, the norm over x; the gradient over either of its inputs."""
     gen = _gen(8)
