@@ -31,18 +31,18 @@ __device__ __forceinline__ int group_rows(const int32_t* counts, int g, int max_
   return counts ? min(max(counts[g], 0), max_rows) : max_rows;
 }
 
-// Output rows of any alignment: 4 columns at a time where `vec` says that rows
-// and columns stay aligned to 4 values, else one by one.
+// Output rows of any alignment, 4 columns at a time.
 template <class T>
 struct Out {
   char* p;
   int64_t ld;  // bytes
-  bool vec, wide;  // rows aligned to 4 values; to 16 bytes with n a multiple of 8 values
   __device__ T* row(int64_t r) const { return (T*)(p + r * ld); }
   __device__ void store4(T* r, int n, int N, const float (&v)[4]) const {
-    if (vec && n + 4 <= N) {
-      if constexpr (sizeof(T) == 2) *(uint2*)(r + n) = make_uint2(f32x2_to_bf16x2(v[0], v[1]), f32x2_to_bf16x2(v[2], v[3]));
-      else *(float4*)(r + n) = make_float4(v[0], v[1], v[2], v[3]);
+    if (n + 4 <= N) {
+      if constexpr (sizeof(T) == 2)
+        *(i32x2_any*)(r + n) = i32x2_any{(int)f32x2_to_bf16x2(v[0], v[1]), (int)f32x2_to_bf16x2(v[2], v[3])};
+      else
+        *(i32x4_any*)(r + n) = i32x4_any{__float_as_int(v[0]), __float_as_int(v[1]), __float_as_int(v[2]), __float_as_int(v[3])};
       return;
     }
 #pragma unroll
@@ -304,25 +304,18 @@ __device__ __forceinline__ void store_staged(const Out<T>& out, int64_t row0, in
       }
   }
   __syncthreads();
-  if (out.wide) {
-    constexpr int RPI = 64 / CH;  // rows a store instruction covers
-    const int c = lane % CH;
+  constexpr int RPI = 64 / CH;  // rows a store instruction covers
+  const int c = lane % CH, n = n0 + c * 8;
 #pragma unroll 4
-    for (int it = 0; it < RPW / RPI; ++it) {
-      const int row = wave * RPW + it * RPI + lane / CH;
-      if (m0 + row < M && n0 + c * 8 < N)
-        *(uint4*)(out.row(row0 + row) + n0 + c * 8) = *(const uint4*)(smem + row * RB + ((c ^ (row & (CH - 1))) << 4));
-    }
-  } else {
-    for (int r = 0; r < RPW; ++r) {
-      const int row = wave * RPW + r;
-      if (m0 + row >= M) return;
-      T* dst = out.row(row0 + row) + n0;
-#pragma unroll
-      for (int x = 0; x < C::BN / 64; ++x) {
-        const int col = x * 64 + lane;
-        if (n0 + col < N) dst[col] = *(const bf16_t*)(smem + row * RB + (((col >> 3) ^ (row & (CH - 1))) << 4) + (col & 7) * 2);
-      }
+  for (int it = 0; it < RPW / RPI; ++it) {
+    const int row = wave * RPW + it * RPI + lane / CH;
+    if (m0 + row >= M || n >= N) continue;
+    const char* src = smem + row * RB + ((c ^ (row & (CH - 1))) << 4);
+    T* dst = out.row(row0 + row) + n;
+    if (n + 8 <= N) {
+      *(i32x4_any*)dst = *(const i32x4*)src;
+    } else {
+      for (int i = 0; i < N - n; ++i) dst[i] = ((const bf16_t*)src)[i];
     }
   }
 }
@@ -548,8 +541,7 @@ void run_tiles(const MxGemmArgs& q, const Operand& a, const Operand& b, const Ou
 template <class T>
 hipError_t run_mx8_gemm(const MxGemmArgs& q, int cus, hipStream_t st) {
   const Operand a{q.a, q.max_rows}, b{q.b, q.n};
-  const uintptr_t at = (uintptr_t)q.out | (uintptr_t)q.ldo;
-  const Out<T> out{(char*)q.out, q.ldo, at % (4 * sizeof(T)) == 0, at % 16 == 0 && q.n % 8 == 0};
+  const Out<T> out{(char*)q.out, q.ldo};
   if (q.max_rows > 64) {
     if constexpr (sizeof(T) == 4) {
       run_tiles<Tile<128>>(q, a, b, out, st);
