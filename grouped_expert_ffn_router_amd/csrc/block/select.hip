@@ -217,6 +217,42 @@ __device__ __forceinline__ void merge_two(uint32_t& a, uint32_t& b, uint32_t a2,
   a = max(a, a2);
 }
 
+// A lane's values e0 .. e0 + EPL - 1 of a row of E, 16 or 8 bytes at a time where
+// it has that many, at any alignment; those past the row are any of its values.
+// 16,384 rows of 1001 experts 25 us, with values one at a time 37.
+template <int EPL>
+__device__ __forceinline__ void lane_values(const float* row, int e0, int E, float (&l)[EPL]) {
+  constexpr int W = EPL % 4 == 0 ? 4 : EPL % 2 == 0 ? 2 : 1;  // (E > 64 where W > 1)
+#pragma unroll
+  for (int j = 0; j < EPL; j += W) {
+    const float* at = row + min(e0 + j, E - W);
+    if constexpr (W == 4) {
+      const i32x4_any d = *(const i32x4_any*)at;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) l[j + i] = __int_as_float(d[i]);
+    } else if constexpr (W == 2) {
+      const i32x2_any d = *(const i32x2_any*)at;
+      l[j] = __int_as_float(d[0]);
+      l[j + 1] = __int_as_float(d[1]);
+    } else {
+      l[j] = *at;
+    }
+  }
+  if (W > 1 && E % W) {  // a piece that crosses the row's end was loaded up to it
+#pragma unroll
+    for (int j = 0; j < EPL; j += W) {
+      const int n = e0 + j - (E - W);
+#pragma unroll
+      for (int by = 1; by < W; ++by)
+#pragma unroll
+        for (int i = 0; i < W - 1; ++i) {  // one place down, up to n times
+          const float stay = l[j + i], moved = l[j + i + 1];
+          l[j + i] = n >= by ? moved : stay;
+        }
+    }
+  }
+}
+
 // One wave per token.  A lane has the experts EPL lane .. EPL lane + EPL - 1, so
 // that of equal keys the lower lane's, and in a lane the lower register's, is
 // the lower expert's.  Each lane sorts its keys once; a round of the choice is
@@ -226,15 +262,14 @@ __device__ __forceinline__ void merge_two(uint32_t& a, uint32_t& b, uint32_t a2,
 //
 // Bound by instructions (387 a wave for 8 of 384 without groups and bias), not by
 // the 4 E bytes a token: 65,536 tokens of 384 experts 40 us (the bytes 22 at a
-// copy's rate), in 8 groups with a bias 73; 8192 tokens 7.3 and 12; one token
-// 3.3 and 5.1, the length of the chain.  All ranks equal: 51 us for 8192 tokens.
+// copy's rate), in 8 groups with a bias 72; 8192 tokens 7.3 and 11; one token
+// 3.3 and 4.7, the length of the chain.  All ranks equal: 50 us for 8192 tokens.
 // Two tokens a wave (32 lanes with 12 experts each) took 37 us and 78 for the
-// first two, 20 for 8192 in groups.  `wide`: rows may be read 8 or 16 bytes at a time.
+// first two, 20 for 8192 in groups.
 template <int EPL>
 __global__ void __launch_bounds__(256)
 select_rule_kernel(SelectRule r, const float* __restrict__ logits, int64_t ld, const float* __restrict__ balance, int64_t T,
-                   int E, int k, bool wide, int32_t* __restrict__ idx, float* __restrict__ w) {
-  constexpr int W = EPL % 4 == 0 ? 4 : EPL % 2 == 0 ? 2 : 1;
+                   int E, int k, int32_t* __restrict__ idx, float* __restrict__ w) {
   const int64_t t = (int64_t)blockIdx.x * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int lane = lane_id(), e0 = lane * EPL;
   if (t >= T) return;
@@ -242,24 +277,7 @@ select_rule_kernel(SelectRule r, const float* __restrict__ logits, int64_t ld, c
   const bool grouped = r.top_groups < r.groups;
   const bool full = E == 64 * EPL;  // else lanes past the last expert read it again and drop what they read
   float l[EPL];
-  if (wide) {
-#pragma unroll
-    for (int j = 0; j < EPL; j += W) {
-      const float* at = row + min(e0 + j, E - W);
-      if constexpr (W == 4) {
-        const float4 d = *(const float4*)at;
-        l[j] = d.x; l[j + 1] = d.y; l[j + 2] = d.z; l[j + 3] = d.w;
-      } else if constexpr (W == 2) {
-        const float2 d = *(const float2*)at;
-        l[j] = d.x; l[j + 1] = d.y;
-      } else {
-        l[j] = *at;
-      }
-    }
-  } else {
-#pragma unroll
-    for (int j = 0; j < EPL; ++j) l[j] = row[min(e0 + j, E - 1)];
-  }
+  lane_values<EPL>(row, e0, E, l);
   if (!full) {
 #pragma unroll
     for (int j = 0; j < EPL; ++j)
@@ -288,10 +306,12 @@ select_rule_kernel(SelectRule r, const float* __restrict__ logits, int64_t ld, c
   for (int j = 0; j < EPL; ++j) orig[j] = rank_key(l[j]);
   uint32_t score[EPL];
   if (grouped || balance) {
+    float bias[EPL];
+    if (balance) lane_values<EPL>(balance, e0, E, bias);
 #pragma unroll
     for (int j = 0; j < EPL; ++j) {
       float v = r.score == SOFTMAX ? __expf(l[j] - top) * inv_sum : __builtin_amdgcn_rcpf(1.0f + __expf(-l[j]));
-      if (balance) v += balance[min(e0 + j, E - 1)];
+      if (balance) v += bias[j];
       if (l[j] == -INFINITY) v = -INFINITY;
       bad |= !(v == v);
       score[j] = rank_key(v);
@@ -590,10 +610,7 @@ hipError_t launch_select_rule(const SelectRule& r, const float* logits, int64_t 
     const float* l = logits + t * ld;
     int32_t* i = idx + t * k;
     float* o = w + t * k;
-    // the bytes that a lane reads at a time: 4 values, or 2, where it has a multiple of them
-    const auto wide = [&](int n) { return E % n == 0 && ld % n == 0 && (uintptr_t)l % (4 * n) == 0; };
-#define SEL(N) \
-  launch(select_rule_kernel<N>, grid, dim3(256), 0, st, r, l, ld, balance, n, E, k, wide(N % 4 == 0 ? 4 : N % 2 == 0 ? 2 : 1), i, o)
+#define SEL(N) launch(select_rule_kernel<N>, grid, dim3(256), 0, st, r, l, ld, balance, n, E, k, i, o)
     if (epl <= 1) SEL(1);
     else if (epl <= 2) SEL(2);
     else if (epl <= 4) SEL(4);

@@ -334,7 +334,7 @@ def test_select_and_its_gradient(T, E, k, rule):
 @pytest.mark.parametrize("E,k", [(8, 2), (24, 4), (32, 31), (33, 3), (64, 8), (100, 5), (128, 1), (256, 8), (300, 16), (384, 8), (512, 31),
                                  (516, 8)])
 def test_select_for_many_tokens(E, k, rule):
-    """Batches large enough that a wave takes two tokens (an odd number of them): each token as in 64 bits."""
+    """Many tokens, an odd number of them: each as in 64 bits."""
     rule = dict(rule)
     groups = rule.get("groups", 1)
     if E % groups or rule.get("top_groups", 1) * (E // groups) < k:
@@ -374,6 +374,27 @@ def test_select_in_groups_of_any_size(E, groups, top_groups, best, k, score):
         want_idx, want_w = R.select(logits.double(), k, balance=None if b is None else b.double(), **kw)
         assert torch.equal(idx.cpu(), want_idx)
         _weights_within(w, want_w, logits.double())
+
+
+@pytest.mark.parametrize("E", [65, 66, 67, 127, 129, 130, 131, 253, 255, 257, 319, 383, 385, 387, 509, 511, 513, 515, 767, 1001, 1022, 1023,
+                               1025, 1026, 1027, 2045, 2046, 2047])
+def test_select_rows_of_any_width_and_alignment(E):
+    gen = _gen(E)
+    T, k = 45, 8
+    wide = torch.randn((T, E + 5), generator=gen) * 2
+    wide[1] = 0.5
+    wide[2, ::2] = -math.inf
+    wide[3, 9:] = -math.inf
+    all_bias = torch.randn((E + 3,), generator=gen) * 0.1
+    for at in (0, 1, 2, 3):
+        logits, b = wide[:, at:at + E], all_bias[at:at + E].clone()
+        for balance in (None, b):
+            room = torch.empty(E + 3, device=DEV)[at:at + E]   # the bias at that offset too
+            given = None if balance is None else room.copy_(b)
+            idx, w = block.select_experts(wide.to(DEV)[:, at:at + E], block.RouterRule(k, score="sigmoid", balance=given))
+            want_idx, want_w = R.select(logits.double(), k, balance=None if balance is None else b.double(), score="sigmoid")
+            assert torch.equal(idx.cpu(), want_idx)
+            _weights_within(w, want_w, logits.double())
 
 
 def test_select_strided_logits():
