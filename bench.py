@@ -52,6 +52,10 @@ SOURCES = ["grouped_expert_ffn_router_amd/csrc/api.hip", "grouped_expert_ffn_rou
 # what the MX-FP4 operators and the few-token layer are built from (they include headers of the above)
 OPERATOR_SOURCES = ["grouped_expert_ffn_router_amd/csrc/ops/" + f
                     for f in ("entry.hip", "few.h", "few.hip", "mx.h", "mx.hip")] + SOURCES[2:]
+# what the operators around the experts' products are built from
+BLOCK_SOURCES = ["grouped_expert_ffn_router_amd/csrc/block/" + f
+                 for f in ("block.h", "entry.hip", "mx8_gemm.hip", "norm.hip", "rows8.hip", "select.hip")] + [
+                     "grouped_expert_ffn_router_amd/csrc/ops/mx.h"] + SOURCES[2:]
 
 
 def parse():
