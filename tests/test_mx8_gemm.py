@@ -90,6 +90,26 @@ def test_rows_behind_the_counts_are_left_alone(M, N, K, counts, dtype):
         assert (fresh[g, rows[g]:] == 0).all() and torch.equal(fresh[g, :rows[g]], out[g, :rows[g]])
 
 
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("G,M,N,K", [(63, 300, 140, 32), (64, 70, 20, 64), (65, 260, 20, 32), (128, 90, 300, 32), (129, 140, 20, 32),
+                                     (1000, 70, 20, 32), (4096, 66, 17, 32), (4096, 5, 17, 32)])
+def test_many_groups(G, M, N, K, dtype):
+    """Tiles are dealt out 64 groups at a time: some groups empty, most, all but one, all, none."""
+    a, b = _operands(G + M, G, M, N, K)
+    gen = torch.Generator().manual_seed(G)
+    some = torch.randint(-M // 2, M + 9, (G,), generator=gen, dtype=torch.int32)
+    few = torch.where(torch.rand((G,), generator=gen) < 0.02, some, 0).int()
+    first, last = torch.zeros(G, dtype=torch.int32), torch.zeros(G, dtype=torch.int32)
+    first[0], last[-1] = M, 1
+    whole = block.mx8_gemm(a, b, dtype=dtype)
+    _check(whole, a, b, [M] * G)
+    for counts in (some, few, first, last, torch.zeros(G, dtype=torch.int32)):
+        out = torch.full((G, M, N), 7.0, dtype=dtype, device=DEV)
+        block.mx8_gemm(a, b, counts=counts.to(DEV), out=out)
+        there = torch.arange(M)[None, :, None] < counts[:, None, None]
+        assert torch.equal(out, torch.where(there.to(DEV), whole, torch.full_like(out, 7.0)))
+
+
 @pytest.mark.parametrize("M", [9, 130])
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
 def test_extreme_and_nan_scales_and_codes(M, dtype):
