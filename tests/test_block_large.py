@@ -89,3 +89,27 @@ def test_product(dtype):
     _say("product", dtype)
     out, out0 = block.mx8_gemm(a, b, dtype=dtype), block.mx8_gemm(a0, b, dtype=dtype)
     assert torch.equal(out[-4096:], out0) and torch.equal(out[:4096], out0)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("cols", [40, 99, 255, 513, 1023, 2047, 4099, 6143, 8203, 16381])
+def test_norm_of_unaligned_rows_past_the_caches(cols, dtype):
+    """More bytes than the caches hold, rows that end inside a piece: row by row as in small calls, and nothing beside them."""
+    some = 1001
+    rows = (150_000_000 // (cols * dtype.itemsize) + some) // some * some + 7
+    gen = torch.Generator(device=DEV).manual_seed(cols)
+    x, r, d = (torch.randn((some, cols), generator=gen, device=DEV).to(dtype) for _ in range(3))
+    w = torch.randn((cols,), generator=gen, device=DEV).to(dtype)
+    at = torch.arange(rows, device=DEV) % some
+    y, s = block.rms_norm(x[at], w, residual=r[at])
+    y0, s0 = block.rms_norm(x, w, residual=r)
+    assert torch.equal(y, y0[at]) and torch.equal(s, s0[at])
+    dx, dw = block.rms_norm_backward(d[at], s, w, dstream=r[at])
+    dx0, _ = block.rms_norm_backward(d, s0, w, dstream=r)
+    assert torch.equal(dx, dx0[at])
+    s64, d64, times = s0.double(), d.double(), torch.bincount(at).double()[:, None]
+    n = s64 * ((s64 * s64).mean(-1, keepdim=True) + 1e-6) ** -0.5
+    want, size = (times * d64 * n).sum(0), (times * d64 * n).abs().sum(0)
+    # a thread adds up at most rows / 256 rows of a part, 16 parts of a workgroup are joined, 16 parts a thread and 64 threads; n
+    # is off by 60 steps or fewer
+    assert ((dw.double() - want).abs() <= size * (rows / 256 + 16 + 16 + 64 + 60) * 2.0 ** -24).all()
