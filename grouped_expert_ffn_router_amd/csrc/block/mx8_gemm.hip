@@ -18,6 +18,9 @@
 
 #include "block.h"
 
+#include <algorithm>
+#include <cmath>
+
 namespace moe {
 
 namespace {
@@ -538,11 +541,26 @@ void run_tiles(const MxGemmArgs& q, const Operand& a, const Operand& b, const Ou
          q.k, q.groups, (int)tiles_n);
 }
 
+// Up to 64 rows: whether tiles of 128 x 128 are faster.  Times beside the launch
+// in units of K / 10 ns.  Without tiles: a CU's share of the workgroups, which
+// read each row's lines by themselves (two workgroups at a time where there are
+// more than CUs).  By tiles: the steps' latency, until a CU has more than one;
+// twice the matrix instructions with an fp32 output; a start and an end of 1.3
+// us.  The rows are max_rows, as the launch does not know the counts.  8 groups of
+// 64 rows x 4096 x 6144 to bf16 26 us by tiles and 109 without, of 8 rows 24 and
+// 34; 64 x 4096 x 6144 20 and 15; 48 groups of one row x 2048 x 2048 22 and 20.
+bool few_by_tiles(const MxGemmArgs& q, int cus) {
+  const double groups = q.groups, k = q.k;
+  const double workgroups = groups * ((q.n + 15) / 16) / cus, share = workgroups <= 1 ? 1 : std::max(2.0, workgroups);
+  const double tiles = groups * ((q.n + 127) / 128) / cus, step = q.bf16 ? 27 : 57;
+  return share * (3 + 4.5 * q.max_rows / 16) > step * std::max(1.0, 1.1 * tiles) + 13000 / k;
+}
+
 template <class T>
 hipError_t run_mx8_gemm(const MxGemmArgs& q, int cus, hipStream_t st) {
   const Operand a{q.a, q.max_rows}, b{q.b, q.n};
   const Out<T> out{(char*)q.out, q.ldo};
-  if (q.max_rows > 64) {
+  if (q.max_rows > 64 || few_by_tiles(q, cus)) {
     if constexpr (sizeof(T) == 4) {
       run_tiles<Tile<128>>(q, a, b, out, st);
     } else {
@@ -554,7 +572,7 @@ hipError_t run_mx8_gemm(const MxGemmArgs& q, int cus, hipStream_t st) {
         const int64_t tiles = q.groups * ((q.max_rows + tile - 1) / tile) * ((q.n + tile - 1) / tile);
         return (double)((tiles + at_once - 1) / at_once);
       };
-      if (rounds(128, 2 * cus) * 0.65 < rounds(256, cus)) run_tiles<Tile<128>>(q, a, b, out, st);
+      if (q.max_rows <= 64 || rounds(128, 2 * cus) * 0.65 < rounds(256, cus)) run_tiles<Tile<128>>(q, a, b, out, st);
       else run_tiles<Tile<256>>(q, a, b, out, st);
     }
     return hipGetLastError();

@@ -92,7 +92,9 @@ def test_rows_behind_the_counts_are_left_alone(M, N, K, counts, dtype):
 
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
 @pytest.mark.parametrize("G,M,N,K", [(63, 300, 140, 32), (64, 70, 20, 64), (65, 260, 20, 32), (128, 90, 300, 32), (129, 140, 20, 32),
-                                     (1000, 70, 20, 32), (4096, 66, 17, 32), (4096, 5, 17, 32)])
+                                     (1000, 70, 20, 32), (4096, 66, 17, 32), (4096, 5, 17, 32),
+                                     # up to 64 rows by tiles
+                                     (8, 40, 2100, 640), (30, 64, 1500, 1056), (100, 33, 700, 512), (64, 16, 513, 544)])
 def test_many_groups(G, M, N, K, dtype):
     """Tiles are dealt out 64 groups at a time: some groups empty, most, all but one, all, none."""
     a, b = _operands(G + M, G, M, N, K)
