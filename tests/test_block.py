@@ -3,6 +3,7 @@
 import copy
 import math
 import pickle
+import threading
 
 import pytest
 import torch
@@ -610,6 +611,43 @@ def test_calls_on_another_stream_and_the_same_bits_again():
     torch.cuda.synchronize()
     for a, b, c in zip(first, second, third):
         assert torch.equal(a, b) and torch.equal(a, c)
+
+
+def test_calls_from_two_threads():
+    """Each on a stream of its own, the same rows and rule: the bits of one thread's calls."""
+    gen = _gen(21)
+    x, t = _rand(gen, (700, 1023), torch.bfloat16), _rand(gen, (700, 1023), torch.bfloat16)
+    w, logits = _rand(gen, (1023,), torch.bfloat16), _rand(gen, (900, 384), torch.float32)
+    gate_up = _rand(gen, (3, 90, 128), torch.bfloat16)
+    rule = block.RouterRule(8, score="sigmoid", balance=_rand(gen, (384,), torch.float32), groups=8, top_groups=4)
+
+    def calls():
+        y, s = block.rms_norm(x, w, residual=t)
+        dx, dw = block.rms_norm_backward(t, s, w, dstream=x)
+        idx, wt = block.select_experts(logits, rule)
+        h, saved = block.swiglu_checkpoint(gate_up)
+        return [y, s, dx, dw, idx, wt, block.select_experts_backward(wt, wt, idx, logits, rule), h, block.swiglu_backward(h, saved)[0]]
+
+    want = calls()
+    torch.cuda.synchronize()
+    wrong = []
+
+    def work():
+        stream = torch.cuda.Stream()
+        with torch.cuda.stream(stream):
+            for _ in range(20):
+                got = calls()
+                stream.synchronize()
+                wrong.extend(i for i, (a, b) in enumerate(zip(got, want)) if not torch.equal(a, b))
+            stream.synchronize()
+        wrong.append(None)   # came to its end
+
+    threads = [threading.Thread(target=work) for _ in range(2)]
+    for th in threads:
+        th.start()
+    for th in threads:
+        th.join()
+    assert wrong == [None, None]
 
 
 def test_rows_and_rules_can_be_copied():
