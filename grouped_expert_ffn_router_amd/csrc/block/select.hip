@@ -478,10 +478,19 @@ select_rule_kernel(SelectRule r, const float* __restrict__ logits, int64_t ld, c
   float x = -INFINITY;
   if (lane < k && !out) x = row[e];
   // a hardware reciprocal where a quotient is wanted: within an ulp
+  // Scores that are divided by their sum count relative to the largest chosen
+  // one: of any size, what the logits' differences say of them.
   float s;
-  if (r.score == SOFTMAX && r.renorm) s = exp_of(x - rank_value(wave_top(rank_key(x))));  // relative to the largest chosen
-  else if (r.score == SOFTMAX) s = exp_of(x - top) * inv_sum;
-  else s = __builtin_amdgcn_rcpf(1.0f + exp_of(-x));
+  if (r.score == SOFTMAX && r.renorm) {
+    s = exp_of(x - rank_value(wave_top(rank_key(x))));
+  } else if (r.score == SOFTMAX) {
+    s = exp_of(x - top) * inv_sum;
+  } else if (r.renorm) {  // 1 / (1 + e^-x) times e^-c, c the largest chosen logit, at most 0: then no term of the largest is above 1
+    const float c = fminf(rank_value(wave_top(rank_key(x))), 0.f);
+    s = __builtin_amdgcn_rcpf(exp_of(c) + exp_of(c - x));
+  } else {
+    s = __builtin_amdgcn_rcpf(1.0f + exp_of(-x));
+  }
   s = x == -INFINITY ? 0.f : s;
   if (r.renorm) {
     const float sum = wave_sum(s);

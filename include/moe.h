@@ -535,8 +535,11 @@ int moe_rms_norm_backward(int32_t act_dtype, int64_t rows, int64_t cols, const v
  *                ones if `renormalise`, times `scale`
  * Ranks are compared as 64-bit arithmetic has them, to its rounding (without a
  * bias, the logits are).  An expert whose logit or rank is -infinity is out: it is chosen only
- * after all others, by lower index, with weight 0.  Where the chosen scores add
- * up to 0 in fp32 (all are out, or below 2^-149) the weights are 0.  A token
+ * after all others, by lower index, with weight 0.  With `renormalise` the
+ * chosen scores count relative to the largest of them, however small that one
+ * is: the weights add up to `scale`, and are all 0 only where all are out.  A
+ * score below 2^-126 (of the largest with `renormalise`, else of 1) may count as 0.
+ * A token
  * with a NaN among its logits or ranks, or under softmax a logit of +infinity,
  * gets experts 0 .. top_k - 1 and NaN weights.
  *   logits    [T][E] fp32 at logits_stride values a row; E <= 2048

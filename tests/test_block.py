@@ -471,6 +471,49 @@ def test_nan_and_infinite_logits():
     assert idx[0, 0] == 5 and 6 not in idx[0].tolist()
 
 
+@pytest.mark.parametrize("rule", [dict(), dict(scale=2.5), dict(balance=True), dict(groups=4, top_groups=2), dict(renormalise=False)],
+                         ids=lambda r: "-".join(r) or "plain")
+def test_sigmoid_weights_of_very_negative_logits(rule):
+    """Scores near and below the smallest fp32 value: the weights divide what the logits' differences say, and so does the gradient."""
+    rule, gen = dict(rule, score="sigmoid"), _gen(17)
+    T, E, k = 40, 40, 4
+    logits = torch.empty((T, E))
+    for i, v in enumerate((-80.0, -86.0, -87.5, -88.0, -89.0, -95.0, -104.0, -120.0, -500.0)):
+        logits[i] = v
+        logits[9 + i] = v + torch.randn((E,), generator=gen)
+        logits[18 + i] = v - 8 * torch.rand((E,), generator=gen)
+    logits[27:] = -90 + 5 * torch.randn((T - 27, E), generator=gen)
+    logits[28, 11] = 3.0                               # one score that is not small
+    logits[29], logits[29, 3], logits[29, 30] = -math.inf, -87.0, -89.0   # 0.88 and 0.12
+    logits[30], logits[30, 7] = -math.inf, -130.0      # one expert is in
+    logits[31] = -math.inf
+    logits[32, 5], logits[32, 6] = -1.0, -0.0
+    balance = torch.randn((E,), generator=gen) * 0.1 if rule.pop("balance", False) else None
+    r = block.RouterRule(k, balance=None if balance is None else balance.to(DEV), **rule)
+    idx, w = block.select_experts(logits.to(DEV), r)
+    want_idx, want = R.select(logits.double(), k, balance=None if balance is None else balance.double(), **rule)
+    assert torch.equal(idx.cpu(), want_idx)
+    # relative to e^c, c the largest chosen logit or 0: the argument c - x is rounded once, each exponential takes 4 steps, the sum,
+    # the reciprocals and the products 10 more, in the numerator and under the line
+    x = logits.double().gather(1, want_idx.long())
+    span = (x.amax(1, keepdim=True).clamp(max=0.0) - x).nan_to_num(0.0, 0.0, 0.0).amax(1, keepdim=True)
+    steps = (48 + 2 * span) * U
+    assert ((R.bits64(w) - want).abs() <= want * steps + 2.0 ** -126).all()
+    if rule.get("renormalise", True):   # whatever the scores' size
+        total = R.bits64(w).sum(1)
+        assert ((total - rule.get("scale", 1.0)).abs()[torch.arange(T) != 31] < 1e-5).all() and total[31] == 0
+    dw = torch.randn((T, k), generator=gen)
+    got = R.bits64(block.select_experts_backward(dw.to(DEV), w, idx, logits.to(DEV), r))
+    leaf = logits.double().clamp(min=-1e4).requires_grad_()
+    args = rule.get("renormalise", True), rule.get("scale", 1.0)
+    (R.select_weights(leaf, want_idx, x.isinf(), "sigmoid", *args) * dw.double()).sum().backward()
+    # w (1 - sigmoid) (dw - mean): a factor of at most twice the largest dw, the steps of w in it and in the mean, 16 of its own;
+    # w is also off by 2^-126 (a smaller score may count as 0), which that factor multiplies
+    most = 2 * dw.double().abs().amax(1, keepdim=True)
+    tol = torch.zeros_like(got).scatter_(1, want_idx.long(), want * most * 2 * (steps + 16 * U)) + 2.0 ** -126 * (1 + most)
+    assert ((got - leaf.grad).abs() <= tol).all()
+
+
 def test_gradient_of_an_expert_named_twice_and_of_none():
     rule = block.RouterRule(4, score="softmax", renormalise=True)
     logits = torch.randn((1, 12), generator=_gen(3)).to(DEV)
