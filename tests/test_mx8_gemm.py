@@ -73,6 +73,62 @@ def test_product_of_many_tiles(M, N, K, dtype):
     _check(block.mx8_gemm(a, b, dtype=dtype), a, b, [M])
 
 
+def _tile(G, M, N):
+    """The tile that a bf16 output of more than 64 rows gets: 256 unless tiles of 128, two at a time on a CU and 0.65 of the time,
+    are faster."""
+    cus = torch.cuda.get_device_properties(0).multi_processor_count
+    assert M > 64
+    rounds = lambda t, places: -(-(G * -(-M // t) * -(-N // t)) // places)  # noqa: E731
+    return 128 if rounds(128, 2 * cus) * 0.65 < rounds(256, cus) else 256
+
+
+@pytest.mark.parametrize("M,N,K", [(2900, 2881, 544), (2830, 3001, 736), (2817, 2945, 832), (2901, 2890, 1024), (2830, 3001, 1120),
+                                   (2945, 2823, 1248), (2900, 2897, 2080), (2999, 2817, 4128)])
+def test_long_rows_by_tiles_of_256(M, N, K):
+    """5 to 33 steps of 128 values: every buffer again and again, scales of the next four steps loaded in between, last steps of 32,
+    64, 96 and 128 values."""
+    assert _tile(1, M, N) == 256
+    a, b = _operands(M + K, 1, M, N, K)
+    _check(block.mx8_gemm(a, b), a, b, [M])
+
+
+def test_groups_by_tiles_of_256():
+    """With counts, columns and rows that end inside a tile, and rows of the output at any alignment."""
+    G, M, N, K, counts = 4, 1501, 1499, 1120, [1501, 0, 37, 1333]
+    assert _tile(G, M, N) == 256
+    a, b = _operands(8, G, M, N, K)
+    wide = torch.full((G, M, N + 4), 7.0, dtype=torch.bfloat16, device=DEV)
+    out = wide[..., 3:3 + N]
+    block.mx8_gemm(a, b, counts=torch.tensor(counts, dtype=torch.int32, device=DEV), out=out)
+    _check(out, a, b, counts)
+    assert (wide[..., :3] == 7).all() and (wide[..., 3 + N:] == 7).all()
+    for g in range(G):
+        assert (out[g, counts[g]:] == 7).all()
+
+
+@pytest.mark.parametrize("M,N,K", [(16, 4099, 2080), (64, 4099, 6144), (130, 700, 512), (500, 512, 16416), (1000, 513, 4128),
+                                   (2900, 2881, 544), (2900, 2900, 6144)])
+def test_bf16_outputs_are_off_by_their_rounding(M, N, K):
+    """Over the whole output, on normal operands: the mean square of the rounding to bf16 alone, within 2 % (it is the mean over
+    65,000 outputs and more), and the 1e-4 of an output's RMS that the matrix unit cuts off, three times over."""
+    gen = torch.Generator().manual_seed(K)
+    a = block.mx8_quantize(torch.randn((M, K), generator=gen).bfloat16().to(DEV))
+    b = runner.mx_quantize((torch.randn((N, K), generator=gen) / 64).to(DEV))
+    want = R.decode8(a.codes, a.scales) @ _decode4(b.codes, b.scales).T
+    got = R.bits64(block.mx8_gemm(a, b))
+    own = (want.to(torch.bfloat16).double() - want).pow(2).mean()
+    assert (got - want).pow(2).mean() <= 1.02 * own + (3e-4) ** 2 * want.pow(2).mean()
+
+
+@pytest.mark.parametrize("M,N,K", [(16, 40, 2080), (64, 48, 4128), (300, 200, 1120), (500, 512, 16416), (2900, 2881, 2080), (2817, 2945, 1248)])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_a_last_block_that_outweighs_the_others(M, N, K, dtype):
+    """Its scale 2^20 times theirs: what is missing or wrong there is not lost in the sum over the others."""
+    a, b = _operands(K, 1, M, N, K, a_scales=(110, 112), b_scales=(126, 128))
+    a.scales[:, :, K // 32 - 1] += 20
+    _check(block.mx8_gemm(a, b, dtype=dtype), a, b, [M])
+
+
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
 @pytest.mark.parametrize("M,N,K,counts", [(50, 40, 96, [50, 0, 17, -4, 99]), (300, 130, 288, [300, 0, 1, 129, 400, 256]),
                                           (1200, 700, 160, [1200, 3, 0, 700])])
