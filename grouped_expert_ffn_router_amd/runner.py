@@ -19,6 +19,7 @@ are provided:
 """
 
 import contextlib
+import dataclasses
 import threading
 
 import numpy as np
@@ -85,6 +86,13 @@ def _rule_of(rule, shape):
     return rule
 
 
+def _rule_as_it_is(rule):
+    """The rule with a balance of its own, which no longer follows the caller's."""
+    if rule is None or rule.balance is None:
+        return rule
+    return dataclasses.replace(rule, balance=rule.balance.clone())
+
+
 def _route(rule, dims, x, w_router, w_down, bias, bias_row_tokens, logits, z, idx, w, ws, stream=None):
     """Router and latent projection; a rule (block.RouterRule) chooses and weights the experts in the place of the softmax
     over the k largest logits."""
@@ -109,7 +117,9 @@ class OneRankLayer:
     products on them (moe_mx_expert_gemm), which rounds the tokens' rows and
     the hidden rows to 4 bits too.  rule: a block.RouterRule by which the
     experts are chosen and weighted, here and in the layers below (None: the
-    softmax over the k largest logits)."""
+    softmax over the k largest logits).  Its balance is read at every step; the
+    other ranks' pools, which are made at set-up, stay those of the balance at
+    that time."""
 
     def __init__(self, shape, inp, device="cuda", gather="fused", keep_source_logits=False, live_waves=0,
                  experts="act", rule=None):
@@ -313,12 +323,14 @@ class RaggedOneRankLayer(OneRankLayer):
     sized to the largest number of rows any wave keeps (moe_dims.wave_rows),
     from per-expert arrival counts taken at set-up (the counts a dropless
     exchange would send ahead of the rows, split by expert); otherwise every
-    expert has a bank of expert_rows rows."""
+    expert has a bank of expert_rows rows.  The segments and banks hold the
+    choices made at set-up, so the layer keeps its ``rule`` as it is then: a
+    balance that the caller changes afterwards counts for a new layer."""
 
     def __init__(self, shape, inp, expert_rows, device="cuda", gather="fused", ragged_banks=True, live_waves=2,
                  experts="act", rule=None):
         from workload.configs import exact_fit
-        self.experts, self.rule = _expert_form(experts), _rule_of(rule, shape)
+        self.experts, self.rule = _expert_form(experts), _rule_as_it_is(_rule_of(rule, shape))
         if "sources" not in inp:
             raise ValueError("the ragged layer needs a workload whose other ranks route their own tokens")
         self.shape, self.device, self.gather = shape, device, gather
