@@ -190,6 +190,21 @@ def test_rms_norm_gradient_by_differences():
         assert abs((loss(x, w + d) - loss(x, w - d)) / (2 * step) - float(dw[j])) < 1e-5
 
 
+@pytest.mark.parametrize("dtype", ACTS)
+@pytest.mark.parametrize("rows,cols", [(2077, 1000), (4097, 6144), (9001, 2056), (20011, 96), (70001, 40), (70001, 5)])
+def test_rms_norm_weight_gradient_over_many_rows(rows, cols, dtype):
+    gen = _gen(rows)
+    s, dy, w = _rand(gen, (rows, cols), dtype), _rand(gen, (rows, cols), dtype), _rand(gen, (cols,), dtype)
+    dw = block.rms_norm_backward(dy, s, w, eps=1e-5)[1]
+    assert torch.equal(dw, block.rms_norm_backward(dy, s, w, eps=1e-5)[1])
+    s, dy = R.bits64(s), R.bits64(dy)
+    n = s * ((s * s).mean(-1, keepdim=True) + 1e-5) ** -0.5
+    # at least min(rows, 1024) threads take a column's rows, one after the other; 16 of them at most are joined to a part, 4096 parts
+    # at most are added by 64 threads, and those 64; a product and its two factors' places beside them
+    steps = rows / 1024 + 1 + 16 + 4096 / 64 + 64 + 4
+    assert ((R.bits64(dw) - (dy * n).sum(0)).abs() <= (dy * n).abs().sum(0) * (_norm_slack(cols) + steps * U)).all()
+
+
 @pytest.mark.parametrize("rows,cols", [(1, 64), (2, 5), (5, 512), (1027, 64), (4099, 5)])
 def test_rms_norm_backward_without_eps(rows, cols):
     """Workgroups of several rows have places past the last row."""
