@@ -74,10 +74,11 @@ __device__ __forceinline__ void mx8_store_scale(uint8_t* row, int b, int blocks,
 
 // Values past the caches (STREAM): a call that touches more than the 256 MB
 // Infinity Cache reads and writes them with nontemporal accesses, so that what
-// it writes does not push out what it has yet to read.  Norm of 8192 x 6144 with
-// both outputs 84 and 71 us, backward of 65,536 x 6144 640 and 620, SwiGLU step
-// of a wave 154 and 135.  Smaller ones leave what they wrote to the next kernel:
-// 2048 x 6144 and the quantisation after it 28.4 us, 29.4 with nontemporal stores.
+// it writes does not push out what it has yet to read.  Ordinary and nontemporal:
+// norm of 8192 x 6144 with both outputs 85 and 75 us, backward of 65,536 x 6144 with
+// a gradient beside the norm 632 and 590, SwiGLU step of two experts of 10,050 rows
+// x 2048 135 and 119.  Smaller ones leave what they wrote to the next kernel: norm
+// of 2048 x 6144 and the quantisation after it 26.1 and 28.7.
 constexpr int64_t STREAM_BYTES = 1ll << 28;
 
 template <bool STREAM, class V>

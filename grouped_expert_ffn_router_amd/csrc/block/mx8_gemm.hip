@@ -78,8 +78,11 @@ __device__ __forceinline__ i32x8 fp8_large(i32x8 v) {
 // their sums meet in LDS.  The 16 scales of a piece are one 16-byte load, whose
 // dword j holds those of MFMA j.  The last piece may end early: codes past the
 // row are read from its last chunk, and their scales are 0 on both sides
-// (2^-254: nothing in fp32).  1 and 16 rows x 4096 x 6144 7 us (the bytes 2.9), 64
-// rows 15: every workgroup reads all rows of A for its 16 columns.
+// (2^-254: nothing in fp32).  1, 16, 32 and 64 rows x 4096 x 6144 5.2, 7.3, 10.2 and
+// 16 us (the bytes 2.8 to 3).  The compiler moves a piece's loads down between its
+// matrix instructions, which makes about three trips to memory of it with 16 rows,
+// eight with 32 and more with 64; and every workgroup reads all rows of A for its
+// 16 columns.
 template <int MT, int NW, class T>
 __global__ void __launch_bounds__(NW * 64)
 mx8_gemm_rows(Operand a, Operand b, Out<T> out, const int32_t* counts, int max_rows, int N, int K) {
@@ -171,11 +174,12 @@ mx8_gemm_rows(Operand a, Operand b, Out<T> out, const int32_t* counts, int max_r
 // place of what is missing, and clears the scales of those blocks on both
 // sides: 2^-254 adds nothing to an fp32 sum, and a NaN there is a NaN of the row.
 //
-// MI355X: 8192 x 6144 x 6144 to bf16 219 us, 2.83 PFLOP/s (2.1 times the rate of a
-// large bf16 library product on the card), the matrix units busy 72 % of the
-// cycles at the 1.9 GHz that the power limit leaves; to fp32, with twice the
-// matrix instructions and tiles of 128 x 128 (the parts of A take registers), 505.
-// Slower here: two buffers instead of three with addresses worked out anew at
+// MI355X: 8192 x 6144 x 6144 to bf16 219-233 us, 2.7-2.8 PFLOP/s (2.1 times the
+// rate of a large bf16 library product on the card), the matrix units busy 72 %
+// of the cycles at the 1.9 GHz that the power limit leaves (tens of calls without a
+// pause bring the clock further down: up to 290 us); to fp32, with twice the matrix
+// instructions and tiles of 128 x 128 (the parts of A take registers), 505-534.
+// Slower here, beside 219: two buffers instead of three with addresses worked out anew at
 // each read (236), 4 scale bytes a row loaded with every step, which leaves no
 // bank conflicts but has 64 lanes read 64 lines (250).
 template <int B_>
@@ -246,8 +250,8 @@ __device__ __forceinline__ int wave_prefix(int v) {
 // 4 tile rows at a time inside a group, in 8 contiguous ranges, one for each
 // XCD (workgroups go round-robin to the XCDs), so that an XCD's L2 sees
 // neighbouring tiles.  The groups' tiles are added up by a wave, 64 groups at a
-// time: groups of 128 rows x 128 x 512 take 7 us for 64 of them, 15 for 384, 480
-// for 4096 (counts looked at one after the other, as in ops/mx.hip: 14, 74, 5300).
+// time: groups of 128 rows x 128 x 512 take 6.5 us for 64 of them, 16 for 384,
+// 490 for 4096 (counts looked at one after the other, as in ops/mx.hip: 14, 74, 5300).
 // False: none is left.
 template <int BM>
 __device__ __forceinline__ bool tile_of(const int32_t* counts, int max_rows, int groups, int tiles_n, int bid, int& g, int& tm,

@@ -5,9 +5,9 @@
 //   with n = s r, g = dy w:  dx = r (g - n mean(g n)) + dstream,  dw = sum over rows of dy n
 //
 // Bound by bytes: 8192 x 6144 bf16 with a residual, the sum, bf16 and 8-bit rows
-// out, 71 us (6.4 TB/s); backward of 65,536 x 6144 with a gradient beside the
-// norm 569 us (5.7 TB/s) and the sum of its 1024 partial rows 10; one row 3 us, a
-// launch and a trip to memory.
+// out, 72-76 us (6.0-6.3 TB/s); backward of 65,536 x 6144 with a gradient beside
+// the norm 569-580 us (5.6-5.7 TB/s) and the sum of its 1024 partial rows 10; one
+// row 3 us, a launch and a trip to memory.
 
 #include "block.h"
 
@@ -64,8 +64,12 @@ __device__ __forceinline__ void row_sums(float (&v)[K], float (*part)[C::NT / 64
 // How a row is cut into pieces of V values.  EVEN: whole pieces, 16-byte aligned;
 // else (rows of any alignment, V values at least) the last one may have fewer: it
 // is loaded from V values before the row's end on, and those of the piece before
-// it are dropped.  16,384 bf16 rows of 4099 values 111 us and backward 138 (of 4096
-// values 90 and 105); one value at a time they took 339 and 277.
+// it are dropped.  16,384 bf16 rows of 4099 values 111 us and backward 136 (of 4096
+// values 90 and 107); one value at a time they took 339 and 277.  Unaligned fp32
+// rows of 8193 values and more are furthest from aligned ones: the backward pass of
+// their 16 columns a thread wants more than the 128 registers that 1024 threads
+// leave, and 23 of them go to memory (4096 x 12,001 205 us, 12,000 155; 8201 154,
+// 8200 114).
 template <class T, int V, bool STREAM, bool EVEN>
 struct Cut {
   using IV = std::conditional_t<EVEN, i32x4, i32x4_any>;
@@ -304,10 +308,14 @@ norm_dweight_kernel(const float* __restrict__ part, int64_t parts, int64_t cols,
 }
 
 // Threads to a row by its pieces (V = 1: rows of fewer values than 16 bytes
-// hold).  Rows of 6144 bf16 values: backward 575 us with 256 threads of 3 pieces,
-// 623 with 384 of 2, 608 with 768 of 1 (65,536 rows); forward 84 us with 384
-// threads, 88 with 256 (8192 rows).  65,536 rows of 100 bf16 values with 16 lanes
-// to a row 12 us and backward 15.5, with a wave to a row 28 and 44.
+// hold).  Rows of 6144 bf16 values, 256 threads of 3 pieces, 384 of 2 and 768 of 1:
+// backward of 65,536 rows 448, 490 and 510 us, with a gradient beside the norm 590,
+// 613 and 590, of 8192 rows with one 88, 99 and 95 (all with the sum of the partial
+// rows).  Forward with 256 and with 384 threads: 8192 rows with both outputs 78 and
+// 75 us, without the 8-bit ones 68 and 65 (2048 rows and the quantisation after it
+// 24 and 26: the larger calls decide).  65,536 rows of 100 bf16 values with 16
+// lanes to a row 9 us, 12 with a residual, and backward 15.6; with a wave to a row
+// 28 with a residual and backward 44.
 template <int V, bool BACKWARD, class F>
 void with_row(int64_t pieces, F f) {
   if constexpr (V == 1) {

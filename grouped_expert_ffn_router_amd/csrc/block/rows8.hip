@@ -39,8 +39,9 @@ __device__ __forceinline__ void places(int64_t block, int per, Place (&p)[U]) {
 // One lane takes 16 bytes of activations (8 bf16 or 4 fp32 values), so a block
 // of 32 is a group of 4 or 8 neighbouring lanes, whose largest magnitude is a
 // maximum over bit patterns taken with DPP moves.  Bound by bytes: 8192 x 6144
-// back to bf16 23 us (6.6 TB/s; a copy of 4 GB reaches 4.8 on this card, a
-// kernel that mostly reads 6.8).
+// from bf16 and back to it 24 us each (6.4 TB/s; a copy of 4 GB reaches 4.8 on
+// this card, a kernel that mostly reads 6.8, and here part of the operands are in
+// the caches).
 
 constexpr int UNROLL = 2;  // pieces a lane
 
@@ -99,9 +100,9 @@ mx8_dequantize_kernel(Rows8 q, int64_t rows, int64_t block0, int per, char* __re
 // Everything between the loads and the stores is fp32 (exp and reciprocal are
 // the hardware's: (2 + 1.5 |a|) 2^-24 off).  A lane has 16 bytes of gate values and
 // the up values that belong to them.  Bound by bytes: two experts of 12,562
-// places, 80 % of them taken, x 2048 hidden units in bf16, forward 61 us (5.4
-// TB/s), backward with h again 73 us (5.7 TB/s); with two pieces a lane 63 and 76,
-// with four 67 and 83.
+// places, 80 % of them taken, x 2048 hidden units in bf16, forward 56 us (5.9
+// TB/s), backward with h again 65 us (6.4 TB/s); with two pieces a lane 3 and 4 %
+// more, with four 10 and 14.
 
 template <class T, bool STREAM>
 __global__ void __launch_bounds__(256)

@@ -260,12 +260,13 @@ __device__ __forceinline__ void lane_values(const float* row, int e0, int E, flo
 // it, and a shift of that lane's keys.  Which expert a key was is looked up
 // once at the end.
 //
-// Bound by instructions (387 a wave for 8 of 384 without groups and bias), not by
-// the 4 E bytes a token: 65,536 tokens of 384 experts 40 us (the bytes 22 at a
-// copy's rate), in 8 groups with a bias 72; 8192 tokens 7.3 and 11; one token
-// 3.3 and 4.7, the length of the chain.  All ranks equal: 50 us for 8192 tokens.
-// Two tokens a wave (32 lanes with 12 experts each) took 37 us and 78 for the
-// first two, 20 for 8192 in groups.
+// Bound by instructions (390 a wave for 8 of 384 without groups and bias), not by
+// the 4 E bytes a token: 65,536 tokens of 384 experts 39-42 us (the bytes 22 at a
+// copy's rate), with sigmoid scores, a bias and 4 of 8 groups 67; 8192 tokens 7.5
+// and 12.4, 12 to 18 in groups over draws of the logits; one token 3.2 and 4.8, the
+// length of the chain.  All ranks of 8192 tokens equal: 24 us, in groups 50.
+// Two tokens a wave (32 lanes with 12 experts each) took 8 % less for 65,536
+// tokens without groups, 8 % more in groups, and 80 % more for 8192 in groups.
 template <int EPL>
 __global__ void __launch_bounds__(256)
 select_rule_kernel(SelectRule r, const float* __restrict__ logits, int64_t ld, const float* __restrict__ balance, int64_t T,
@@ -511,7 +512,9 @@ select_rule_kernel(SelectRule r, const float* __restrict__ logits, int64_t ld, c
 //   softmax                 dl_e = w_e dw_e [e chosen] - scale m p_e   (p: the softmax over all)
 // and 0 elsewhere.  One wave per token: its row of terms is laid out in LDS
 // (zeros, then each pick's term) and stored whole, so that the time is that of
-// writing the row (8192 x 384: 4.5 us; with each term compared into its lane 7.8).
+// writing the row (8192 x 384: 4.5-5.5 us; with each term compared into its lane
+// 7.8).  The softmax without renormalisation reads its logits three times, 4 bytes
+// a lane: 11.5 us, 65,536 tokens 70 (their bytes 42 at a copy's rate).
 // Picks of one expert are added up in their order; that there
 // are some shows where a pick does not read its own mark back.
 

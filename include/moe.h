@@ -498,8 +498,9 @@ int moe_mxb_gemm(int32_t out_dtype, int32_t groups, int64_t max_rows, int64_t n,
  *                 16-byte aligned
  * y or y8 is given.  cols <= MOE_NORM_COLS_MAX.  Addresses and strides are
  * multiples of the value's size (16-byte aligned rows are the fastest).
- * Squares are summed in fp32, so a row whose squares exceed 2^127 gives 0; a row
- * of zeros with eps 0 gives NaN. */
+ * Squares are summed in fp32, so a row whose squares exceed 2^127 gives 0, and
+ * squares below 2^-149 count as 0.  With eps 0 a row of zeros gives NaN, and one
+ * whose squares all count as 0 infinities. */
 #define MOE_NORM_COLS_MAX 16384
 int moe_rms_norm(int32_t act_dtype, int64_t rows, int64_t cols, const void* x, int64_t x_stride_bytes,
                  const void* residual, int64_t residual_stride_bytes, const void* weight, int32_t weight_dtype, float eps,
