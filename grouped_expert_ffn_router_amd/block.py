@@ -200,7 +200,8 @@ _SCORES = {"softmax": B.MOE_SCORE_SOFTMAX, "sigmoid": B.MOE_SCORE_SIGMOID}
 @dataclass(frozen=True, eq=False)
 class RouterRule:
     """How a router's logits choose and weight experts (moe_router_rule in include/moe.h).  The rule itself does not change;
-    balance, fp32 [E], is read at each call, so that a program can adjust it in place."""
+    balance, fp32 [E], is read at each call, so that a program can adjust it in place (runner.RaggedOneRankLayer keeps the one
+    that it was made with)."""
 
     top_k: int
     score: str = "softmax"        # or "sigmoid"
